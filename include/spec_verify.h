@@ -41,17 +41,19 @@
 extern "C" {
 #endif
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+/* SPEC_F16 is a type of the paged cache (below); the logit entry points refuse it. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype;
 
 enum {
   SPEC_OK = 0,
   SPEC_ERR_INVALID_ARG = -1,  /* null pointer, B < 1, gamma outside 1..31, V bad */
   SPEC_ERR_UNSUPPORTED = -2,  /* dtype / shape not supported by this build      */
-  SPEC_ERR_ALIGNMENT = -3,    /* a logit pointer is not 16-byte aligned         */
+  SPEC_ERR_ALIGNMENT = -3,    /* a pointer or stride is not a multiple of 16 bytes */
   SPEC_ERR_WORKSPACE = -4,    /* workspace null, misaligned or too small        */
   SPEC_ERR_CUDA = -5,         /* a CUDA runtime call or kernel launch failed    */
   SPEC_ERR_TIMEOUT = -6,      /* device side: a bounded wait ran out            */
-  SPEC_ERR_DEVICE_INPUT = -7, /* device side: a draft token outside [0, V)      */
+  SPEC_ERR_DEVICE_INPUT = -7, /* device side: a draft token outside [0, V), or a
+                                 page, length or axis outside its range       */
   SPEC_ERR_STATE = -8,        /* host round driver: inconsistent bookkeeping   */
   SPEC_ERR_DEVICE_BOUNDS = -9 /* device side, bounds-checked build only: an
                                  index outside its extent (access skipped)    */
@@ -378,6 +380,124 @@ typedef struct {
 
 int spec_round_update(spec_round_state *states, const int32_t *num_accepted, int B,
                       int gamma_min, int gamma_max, int64_t *kv_keep, int *first_bad);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The verify pass's cached attention: a paged key/value cache, the append that
+ * fills it, and the attention that reads it.
+ *
+ * In each layer of the target's verify pass ("第 8 章 …", 为什么一次前向能验证多个 token)
+ * the new positions of every sequence (the newest token and its drafts) are
+ * rotated to their positions and appended to the sequence's pages
+ * (spec_kv_append), and each of them attends to the prefix that the whole
+ * batch shares, to the sequence's own pages, and to the new positions that it
+ * may see (spec_prefix_attention).  After the round spec_round_update's
+ * kv_keep says how many entries stay; the next append overwrites the rest.
+ *
+ * Arguments that both calls share (device memory unless said otherwise):
+ *   cache        HOST struct, below: the pools of key and value pages
+ *   q_indptr     int32 [B+1]: the new positions of sequence b are rows
+ *                q_indptr[b] .. q_indptr[b+1]-1 of the [N, ...] tensors
+ *                (non-decreasing from 0; rows from q_indptr[B] to N are padding
+ *                and are neither read nor written)
+ *   block_table  int32 [B, table_width]: the pages of sequence b in order;
+ *                entry i sits in slot i % page_size of page
+ *                block_table[b, i / page_size].  Entries of pages that the
+ *                length does not reach are not read.
+ *   kv_len       int32 [B]: entries of sequence b's own pages WITH the new
+ *                positions (q_len[b] <= kv_len[b] <= table_width * page_size);
+ *                new position i is entry kv_len[b] - q_len[b] + i.  The shared
+ *                prefix is not counted.
+ *   workspace    spec_attention_workspace_bytes() bytes, 256-byte aligned,
+ *                zeroed once; calls that share one must not overlap
+ * Every length and table is read on the device, so a captured graph serves
+ * rounds of other lengths.  A length outside its range is clamped, and a page
+ * outside [0, n_pages) is neither read (its keys read as zero) nor written;
+ * either makes spec_verify_status return SPEC_ERR_DEVICE_INPUT.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct {
+  void *k_pages, *v_pages;  /* device pools; both have the strides below            */
+  int64_t page_stride;      /* elements from a page to the next                     */
+  int64_t slot_stride;      /* from an entry of a page to the next                  */
+  int64_t head_stride;      /* from a head to the next; a head's dims are adjacent  */
+  int64_t n_pages;
+  int32_t page_size;        /* entries a page holds                                 */
+  int32_t n_heads;          /* key/value heads                                      */
+  int32_t head_dim;         /* a multiple of 8 up to 512                            */
+  int32_t dtype;            /* SPEC_BF16 or SPEC_F16, for q, k, v and outputs too   */
+} spec_kv_cache;
+
+/*
+ * Bytes of workspace for either call with up to B sequences, N new positions,
+ * n_q_heads query heads of head_dim.
+ */
+int spec_attention_workspace_bytes(int B, int N, int n_q_heads, int head_dim, size_t *bytes);
+
+/*
+ * Rotate the new queries and keys to their positions and append keys and
+ * values to the cache, in one launch.
+ *
+ *   q [N, n_q_heads, D], k and v [N, n_heads, D]   elements; strides in elements
+ *                between positions and between heads, so all three can be views
+ *                of one projection's output
+ *   q_out        [N, n_q_heads, D] contiguous; must not overlap q
+ *   inv_freq     float32 [rot_dim / 2]: angle per position of each pair
+ *   positions    int32 [n_axes, N] (row a: the positions on axis a, such as
+ *                time, height and width), or NULL: position_base + the entry's
+ *                index, one axis
+ *   axis         int32 [rot_dim / 2], the axis of each frequency in
+ *                [0, n_axes), or NULL: all on axis 0
+ *   rot_dim      even, 0 .. D; dims from rot_dim on are copied.  0: no
+ *                rotation (inv_freq may be NULL)
+ *   interleaved  0: pair f is dims (f, f + rot_dim/2); 1: dims (2f, 2f + 1)
+ *
+ * With angle t = position * inv_freq (reduced exactly enough for positions up
+ * to 2^31): x' = x cos t - y sin t, y' = x sin t + y cos t, in fp32, rounded
+ * once.  Pointers and strides must be multiples of 16 bytes; else
+ * SPEC_ERR_ALIGNMENT.
+ */
+int spec_kv_append(const spec_kv_cache *cache, const void *q, int64_t q_pos_stride,
+                   int64_t q_head_stride, const void *k, int64_t k_pos_stride,
+                   int64_t k_head_stride, const void *v, int64_t v_pos_stride,
+                   int64_t v_head_stride, int n_q_heads, int N, const int32_t *q_indptr, int B,
+                   const int32_t *block_table, int table_width, const int32_t *kv_len,
+                   const float *inv_freq, const int32_t *positions, int n_axes,
+                   const int32_t *axis, int rot_dim, int interleaved, int64_t position_base,
+                   void *q_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Attention of every new position over the shared prefix, its sequence's
+ * pages and the new positions before it:
+ *   out[n, h] = sum_t softmax_t(scale * q[n, h] . k_t) v_t,
+ *   lse[n, h] = ln sum_t exp(scale * q[n, h] . k_t)       (lse may be NULL)
+ * over the prefix_len entries of the pages prefix_table (int32 [ceil(prefix_len
+ * / page_size)]; NULL when prefix_len is 0), every entry of the sequence older
+ * than the new positions, and, of these, entry j for position i where
+ *   draft_mask == NULL: j <= i (the drafts are one chain);
+ *   else: bit j of draft_mask[n] (uint64 [N]) is set (several candidates in
+ *   one pass; a position sees itself only if its own bit is set, and new
+ *   positions from the 65th on are seen by none).
+ * Query head h reads key head h / (n_q_heads / n_heads).  A position that sees
+ * nothing gives out 0 and lse -inf.  The prefix's keys and values are read
+ * once for the whole batch, not once a sequence.
+ *
+ *   q, out  [N, n_q_heads, D], strides in elements, multiples of 16 bytes
+ *
+ * Products of the 16-bit values on the tensor cores, sums and softmax in fp32;
+ * the weights are rounded to the cache's type for the product with v.  Entries
+ * past a length may hold anything; values of live entries must be finite, also
+ * where a mask hides them.  Limits: D 64 or 128, page_size a multiple of 8,
+ * n_q_heads a multiple of n_heads and at most 128 times it (else
+ * SPEC_ERR_UNSUPPORTED); scale > 0.
+ */
+int spec_prefix_attention(const spec_kv_cache *cache, const void *q, int64_t q_pos_stride,
+                          int64_t q_head_stride, int n_q_heads, int N, const int32_t *q_indptr,
+                          int B, const int32_t *prefix_table, int64_t prefix_len,
+                          const int32_t *block_table, int table_width, const int32_t *kv_len,
+                          const uint64_t *draft_mask, float scale, void *out,
+                          int64_t out_pos_stride, int64_t out_head_stride, float *lse,
+                          void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Synchronise `stream`, then return the device-side status recorded in

@@ -13,7 +13,7 @@ import os
 
 from . import _build
 
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_F16 = 0, 1, 2
 SPEC_OK = 0
 SPEC_ERR_INVALID_ARG = -1
 SPEC_ERR_UNSUPPORTED = -2
@@ -34,6 +34,7 @@ EXPORTED = (
     "spec_verify_greedy_multi", "spec_round_update", "spec_verify_topkp_workspace_bytes",
     "spec_verify_sample_topkp", "spec_centroid_head_workspace_bytes", "spec_centroid_head",
     "spec_verify_sparse_workspace_bytes", "spec_verify_sample_sparse",
+    "spec_attention_workspace_bytes", "spec_kv_append", "spec_prefix_attention",
 )
 
 
@@ -44,7 +45,7 @@ class SpecVerifyError(RuntimeError):
 
 
 _lib = None
-_vp, _sz, _i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_vp, _sz, _i, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64
 
 
 def lib_path() -> str:
@@ -82,6 +83,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.spec_verify_sparse_workspace_bytes.argtypes = [_i, _i, _i, ctypes.POINTER(_sz)]
     lib.spec_verify_sample_sparse.argtypes = [_vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i,
                                               _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.spec_attention_workspace_bytes.argtypes = [_i, _i, _i, _i, ctypes.POINTER(_sz)]
+    lib.spec_kv_append.argtypes = [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i, _i, _vp, _i, _vp, _i, _vp,
+                                   _vp, _vp, _i, _vp, _i, _i, _i64, _vp, _vp, _sz, _vp]
+    lib.spec_prefix_attention.argtypes = [_vp, _vp, _i64, _i64, _i, _i, _vp, _i, _vp, _i64, _vp, _i, _vp, _vp,
+                                          ctypes.c_float, _vp, _i64, _i64, _vp, _vp, _sz, _vp]
     lib.spec_verify_status.argtypes = [_vp, _vp]
     lib.spec_verify_error_string.argtypes = [_i]
     lib.spec_verify_error_string.restype = ctypes.c_char_p
@@ -397,3 +403,154 @@ def spec_verify_sample_sparse(target_logits, cand_tok, cand_logit, cand_count, d
         cand_tok.shape[1], _ptr(draft_tokens), _ptr(temperature), _ptr(u_accept), _ptr(u_resample), B, g1 - 1, V,
         _ptr(out_tokens), _ptr(out_num_accepted), _ptr(out_debug), _ptr(workspace), _nbytes(workspace),
         _stream(stream)), "spec_verify_sample_sparse")
+
+
+# ---------------------------------------------------------------------------
+# the paged key/value cache: append with rotary positions, shared-prefix attention
+# ---------------------------------------------------------------------------
+class SpecKvCache(ctypes.Structure):
+    """spec_kv_cache: the pools of a paged cache (strides in elements)."""
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("page_stride", _i64), ("slot_stride", _i64),
+                ("head_stride", _i64), ("n_pages", _i64), ("page_size", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+def make_kv_cache(k_pages, v_pages) -> SpecKvCache:
+    """The cache over pools [n_pages, page_size, n_heads, head_dim] (bf16 or
+    fp16, any strides but the last; both alike).  A pool stored
+    [n_pages, n_heads, page_size, head_dim] is passed as its transpose(1, 2).
+    The struct keeps the tensors alive."""
+    import torch
+    codes = {torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+    if k_pages.dtype not in codes or v_pages.dtype != k_pages.dtype:
+        raise SpecVerifyError(SPEC_ERR_UNSUPPORTED, f"cache dtypes {k_pages.dtype}, {v_pages.dtype}")
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() \
+            or k_pages.stride(3) != 1:
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"cache pools {tuple(k_pages.shape)} with strides "
+                              f"{k_pages.stride()}, {tuple(v_pages.shape)} with {v_pages.stride()}")
+    n_pages, page_size, n_heads, head_dim = k_pages.shape
+    page_stride, slot_stride, head_stride, _ = k_pages.stride()
+    cache = SpecKvCache(k_pages.data_ptr(), v_pages.data_ptr(), page_stride, slot_stride, head_stride, n_pages,
+                        page_size, n_heads, head_dim, codes[k_pages.dtype])
+    cache.tensors = (k_pages, v_pages)
+    cache.address = ctypes.addressof(cache)
+    return cache
+
+
+def spec_attention_workspace_bytes(B: int, N: int, n_q_heads: int, head_dim: int) -> int:
+    out = _sz(0)
+    _check(load().spec_attention_workspace_bytes(B, N, n_q_heads, head_dim, ctypes.byref(out)),
+           "spec_attention_workspace_bytes")
+    return out.value
+
+
+def make_attention_workspace(B: int, N: int, n_q_heads: int, head_dim: int, device="cuda"):
+    """Allocate (torch) and zero a workspace for spec_kv_append and spec_prefix_attention."""
+    return _aligned_zeros(spec_attention_workspace_bytes(B, N, n_q_heads, head_dim), device)
+
+
+def _positions_first(name, cache, *tensors):
+    """Shared checks of [N, heads, head_dim] tensors: the cache's dtype and
+    head_dim, one N, adjacent dims."""
+    pool = cache.tensors[0]
+    N, D = tensors[0].shape[0], pool.shape[3]
+    for t in tensors:
+        if t.dtype != pool.dtype:
+            raise SpecVerifyError(SPEC_ERR_UNSUPPORTED, f"{name}: dtype {t.dtype}, cache {pool.dtype}")
+        if t.dim() != 3 or t.shape[0] != N or t.shape[2] != D or t.stride(2) != 1:
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: shape {tuple(t.shape)} strides {t.stride()}, "
+                                  f"expected [{N}, heads, {D}] with adjacent dims")
+
+
+def _batch_checks(name, q_indptr, block_table, kv_len):
+    import torch
+    B = kv_len.shape[0]
+    for t, shape in ((q_indptr, (B + 1,)), (kv_len, (B,)), (block_table, (B, block_table.shape[-1]))):
+        if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous "
+                                  f"int32 {shape}")
+    return B
+
+
+def _on_gpu(name, *tensors):
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: a tensor of {tuple(t.shape)} is not on the GPU")
+
+
+def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspace, inv_freq=None, positions=None,
+                   axis=None, interleaved=False, position_base=0, stream=None) -> None:
+    """Rotate the new queries and keys and append keys and values to the cache.
+
+    cache from make_kv_cache; q [N, n_q_heads, D], k and v [N, n_heads, D]
+    (views of one projection's output are fine); q_out [N, n_q_heads, D]
+    contiguous; q_indptr int32 [B+1], block_table int32 [B, width], kv_len
+    int32 [B] (the new positions counted); inv_freq float32 [rot_dim / 2] (None:
+    no rotation); positions int32 [n_axes, N] and axis int32 [rot_dim / 2], or
+    None for position_base + the entry's index."""
+    import torch
+    _positions_first("spec_kv_append", cache, q, k, v, q_out)
+    B = _batch_checks("spec_kv_append", q_indptr, block_table, kv_len)
+    n_axes, rot = 1, 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.shape[0]
+        if inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, "spec_kv_append: inv_freq must be contiguous float32")
+    if positions is not None:
+        n_axes = positions.shape[0]
+        if positions.dtype != torch.int32 or tuple(positions.shape) != (n_axes, q.shape[0]) \
+                or not positions.is_contiguous():
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_kv_append: positions {positions.dtype} "
+                                  f"{tuple(positions.shape)}, expected contiguous int32 [n_axes, {q.shape[0]}]")
+    if axis is not None and (axis.dtype != torch.int32 or 2 * axis.numel() != rot or not axis.is_contiguous()):
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_kv_append: axis {axis.dtype} {tuple(axis.shape)}, expected "
+                              f"contiguous int32 [{rot // 2}]")
+    n_heads = cache.n_heads
+    if k.shape[1] != n_heads or v.shape[1] != n_heads or q_out.shape != q.shape or not q_out.is_contiguous():
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_kv_append: q {tuple(q.shape)}, k {tuple(k.shape)}, "
+                              f"v {tuple(v.shape)}, q_out {tuple(q_out.shape)}, {n_heads} cache heads")
+    _on_gpu("spec_kv_append", cache.tensors[0], cache.tensors[1], q, k, v, q_out, q_indptr, block_table, kv_len,
+            inv_freq, positions, axis, workspace)
+    _check(load().spec_kv_append(
+        cache.address, q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
+        v.stride(0), v.stride(1), q.shape[1], q.shape[0], q_indptr.data_ptr(), B, block_table.data_ptr(),
+        block_table.shape[1], kv_len.data_ptr(), _ptr(inv_freq), _ptr(positions), n_axes, _ptr(axis), rot,
+        1 if interleaved else 0, position_base, q_out.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
+        _stream(stream)), "spec_kv_append")
+
+
+def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspace, prefix_table=None, prefix_len=0,
+                          draft_mask=None, scale=None, lse=None, stream=None) -> None:
+    """Attention of the new positions over the shared prefix and their
+    sequences' pages.
+
+    q, out [N, n_q_heads, D] in the cache's dtype; prefix_table int32
+    [>= ceil(prefix_len / page_size)]; draft_mask int64 [N] (64 bits, bit j: the
+    position sees new entry j) or None for a chain; scale defaults to
+    D ** -0.5; lse float32 [N, n_q_heads] or None.  The rest as spec_kv_append."""
+    import torch
+    _positions_first("spec_prefix_attention", cache, q, out)
+    B = _batch_checks("spec_prefix_attention", q_indptr, block_table, kv_len)
+    N, n_q_heads, D = q.shape
+    if out.shape != q.shape:
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: q {tuple(q.shape)}, out {tuple(out.shape)}")
+    if prefix_len > 0 and (prefix_table is None or prefix_table.dtype != torch.int32 or prefix_table.dim() != 1
+                           or not prefix_table.is_contiguous()
+                           or prefix_table.shape[0] * cache.page_size < prefix_len):
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: prefix_table does not hold the pages of "
+                              f"{prefix_len} entries")
+    if draft_mask is not None and (draft_mask.dtype != torch.int64 or tuple(draft_mask.shape) != (N,)
+                                   or not draft_mask.is_contiguous()):
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: draft_mask {draft_mask.dtype} "
+                              f"{tuple(draft_mask.shape)}, expected contiguous int64 [{N}]")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (N, n_q_heads)
+                            or not lse.is_contiguous()):
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: lse {lse.dtype} {tuple(lse.shape)}, "
+                              f"expected contiguous float32 [{N}, {n_q_heads}]")
+    _on_gpu("spec_prefix_attention", cache.tensors[0], cache.tensors[1], q, out, q_indptr, block_table, kv_len,
+            prefix_table, draft_mask, lse, workspace)
+    _check(load().spec_prefix_attention(
+        cache.address, q.data_ptr(), q.stride(0), q.stride(1), n_q_heads, N, q_indptr.data_ptr(), B,
+        _ptr(prefix_table), prefix_len, block_table.data_ptr(), block_table.shape[1], kv_len.data_ptr(),
+        _ptr(draft_mask), D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1),
+        _ptr(lse), workspace.data_ptr(), _nbytes(workspace), _stream(stream)), "spec_prefix_attention")

@@ -1,0 +1,209 @@
+// attention.cu — host side of the paged cache's calls: argument checks,
+// workspace layout and launches behind spec_kv_append and
+// spec_prefix_attention.
+#include <cuda.h>
+#include <cmath>
+
+#include "attend.cuh"
+#include "common.cuh"
+#include "host.cuh"
+#include "kvappend.cuh"
+#include "spec_verify.h"
+
+using namespace specv;
+
+namespace {
+
+struct AttnLayout {
+  size_t header, total;
+};
+
+AttnLayout attn_layout(int B, int N, int n_q_heads, int D) {
+  AttnLayout L;
+  size_t off = 0;
+  L.header = off;
+  off += align_up(sizeof(WsHeader), 256);
+  L.total = off;
+  return L;
+}
+
+constexpr int kMaxRowsPerCall = 1 << 24;
+
+int check_sizes(int B, int N, int n_q_heads, int D) {
+  if (B < 1 || B > 65535 || N < 1 || N > kMaxRowsPerCall || n_q_heads < 1 || n_q_heads > 4096 || D < 8 || D > 512 ||
+      (D % 8) != 0)
+    return SPEC_ERR_INVALID_ARG;
+  return SPEC_OK;
+}
+
+bool vec8(int64_t stride) { return (stride & 7) == 0; }
+
+// What both calls check of the cache, the batch and the workspace.
+int check_common(const spec_kv_cache* c, int n_q_heads, int N, const int32_t* q_indptr, int B,
+                 const int32_t* block_table, int table_width, const int32_t* kv_len, const void* ws,
+                 size_t ws_bytes) {
+  if (c == nullptr || c->k_pages == nullptr || c->v_pages == nullptr || q_indptr == nullptr ||
+      block_table == nullptr || kv_len == nullptr)
+    return SPEC_ERR_INVALID_ARG;
+  if (c->dtype != SPEC_BF16 && c->dtype != SPEC_F16) return SPEC_ERR_UNSUPPORTED;
+  if (int e = check_sizes(B, N, n_q_heads, c->head_dim)) return e;
+  if (c->n_heads < 1 || c->n_heads > n_q_heads || c->page_size < 1 || c->n_pages < 1 || c->n_pages > INT32_MAX ||
+      table_width < 1)
+    return SPEC_ERR_INVALID_ARG;
+  if (c->page_stride < 0 || c->slot_stride < 0 || c->head_stride < 0) return SPEC_ERR_INVALID_ARG;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !vec8(c->page_stride) || !vec8(c->slot_stride) ||
+      !vec8(c->head_stride))
+    return SPEC_ERR_ALIGNMENT;
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 ||
+      ws_bytes < attn_layout(B, N, n_q_heads, c->head_dim).total)
+    return SPEC_ERR_WORKSPACE;
+  return SPEC_OK;
+}
+
+PagedView view_of(const spec_kv_cache* c) {
+  PagedView v;
+  v.k = static_cast<uint16_t*>(c->k_pages);
+  v.v = static_cast<uint16_t*>(c->v_pages);
+  v.page_stride = c->page_stride;
+  v.slot_stride = c->slot_stride;
+  v.head_stride = c->head_stride;
+  v.n_pages = c->n_pages;
+  v.page_size = c->page_size;
+  v.n_heads = c->n_heads;
+  return v;
+}
+
+PagedBatch batch_of(const spec_kv_cache* c, int N, const int32_t* q_indptr, int B, const int32_t* block_table,
+                    int table_width, const int32_t* kv_len, void* ws) {
+  PagedBatch b;
+  b.q_indptr = q_indptr;
+  b.block_table = block_table;
+  b.kv_len = kv_len;
+  b.B = B;
+  b.N = N;
+  b.table_width = table_width;
+  b.page_size = c->page_size;
+  b.status = reinterpret_cast<int*>(ws);
+  return b;
+}
+
+template <typename T>
+int launch_append(const AppendParams& p, int interleaved, cudaStream_t s) {
+  const dim3 grid((p.batch.N + p.tile - 1) / p.tile);
+  const size_t smem = static_cast<size_t>(p.tile) * p.half * sizeof(float2);
+  const cudaError_t e = interleaved ? launch_pdl(kv_append_kernel<T, true>, grid, dim3(kAppendThreads), smem, s, p)
+                                    : launch_pdl(kv_append_kernel<T, false>, grid, dim3(kAppendThreads), smem, s, p);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+template <typename T>
+int launch_attend(const AttendParams& p, cudaStream_t s) {
+  const int64_t items = static_cast<int64_t>(p.batch.N) * p.n_q_heads;
+  const dim3 grid(static_cast<unsigned>((items + 3) / 4));
+  const cudaError_t e = p.D == 64 ? launch_pdl(attend_simple_kernel<T, 64>, grid, dim3(128), 0, s, p)
+                                  : launch_pdl(attend_simple_kernel<T, 128>, grid, dim3(128), 0, s, p);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int spec_attention_workspace_bytes(int B, int N, int n_q_heads, int head_dim, size_t* bytes) {
+  if (bytes == nullptr) return SPEC_ERR_INVALID_ARG;
+  if (int e = check_sizes(B, N, n_q_heads, head_dim)) return e;
+  *bytes = attn_layout(B, N, n_q_heads, head_dim).total;
+  return SPEC_OK;
+}
+
+int spec_kv_append(const spec_kv_cache* cache, const void* q, int64_t q_pos_stride, int64_t q_head_stride,
+                   const void* k, int64_t k_pos_stride, int64_t k_head_stride, const void* v, int64_t v_pos_stride,
+                   int64_t v_head_stride, int n_q_heads, int N, const int32_t* q_indptr, int B,
+                   const int32_t* block_table, int table_width, const int32_t* kv_len, const float* inv_freq,
+                   const int32_t* positions, int n_axes, const int32_t* axis, int rot_dim, int interleaved,
+                   int64_t position_base, void* q_out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (q == nullptr || k == nullptr || v == nullptr || q_out == nullptr) return SPEC_ERR_INVALID_ARG;
+  if (int e = check_common(cache, n_q_heads, N, q_indptr, B, block_table, table_width, kv_len, workspace,
+                           workspace_bytes))
+    return e;
+  const int D = cache->head_dim;
+  if (rot_dim < 0 || rot_dim > D || (rot_dim & 1) != 0 || (rot_dim > 0 && inv_freq == nullptr)) return SPEC_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return SPEC_ERR_INVALID_ARG;
+  // without positions there is one axis; with several, each frequency names its own
+  if (n_axes < 1 || n_axes > 16 || (positions == nullptr && n_axes != 1) ||
+      (n_axes > 1 && axis == nullptr && rot_dim > 0) || position_base < 0)
+    return SPEC_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !vec8(q_pos_stride) ||
+      !vec8(q_head_stride) || !vec8(k_pos_stride) || !vec8(k_head_stride) || !vec8(v_pos_stride) ||
+      !vec8(v_head_stride))
+    return SPEC_ERR_ALIGNMENT;
+  // a head's second half is read after its first half may have been written
+  if (q == q_out) return SPEC_ERR_INVALID_ARG;
+  AppendParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_ps = q_pos_stride;
+  p.q_hs = q_head_stride;
+  p.k_ps = k_pos_stride;
+  p.k_hs = k_head_stride;
+  p.v_ps = v_pos_stride;
+  p.v_hs = v_head_stride;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.cache = view_of(cache);
+  p.batch = batch_of(cache, N, q_indptr, B, block_table, table_width, kv_len, workspace);
+  p.inv_freq = inv_freq;
+  p.positions = positions;
+  p.axis = axis;
+  p.position_base = position_base;
+  p.n_axes = n_axes;
+  p.n_q_heads = n_q_heads;
+  p.D = D;
+  p.half = rot_dim / 2;
+  p.tile = N <= 1024 ? 1 : 4;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cache->dtype == SPEC_BF16 ? launch_append<__nv_bfloat16>(p, interleaved, s)
+                                   : launch_append<__half>(p, interleaved, s);
+}
+
+int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_pos_stride, int64_t q_head_stride,
+                          int n_q_heads, int N, const int32_t* q_indptr, int B, const int32_t* prefix_table,
+                          int64_t prefix_len, const int32_t* block_table, int table_width, const int32_t* kv_len,
+                          const uint64_t* draft_mask, float scale, void* out, int64_t out_pos_stride,
+                          int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  if (q == nullptr || out == nullptr) return SPEC_ERR_INVALID_ARG;
+  if (int e = check_common(cache, n_q_heads, N, q_indptr, B, block_table, table_width, kv_len, workspace,
+                           workspace_bytes))
+    return e;
+  if (prefix_len < 0 || (prefix_len > 0 && prefix_table == nullptr) || !(scale > 0.f) || !std::isfinite(scale))
+    return SPEC_ERR_INVALID_ARG;
+  if (n_q_heads % cache->n_heads != 0) return SPEC_ERR_INVALID_ARG;
+  if ((cache->head_dim != 64 && cache->head_dim != 128) || cache->page_size % 8 != 0 ||
+      n_q_heads / cache->n_heads > 128)
+    return SPEC_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(out) || !vec8(q_pos_stride) || !vec8(q_head_stride) || !vec8(out_pos_stride) ||
+      !vec8(out_head_stride))
+    return SPEC_ERR_ALIGNMENT;
+  AttendParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_ps = q_pos_stride;
+  p.q_hs = q_head_stride;
+  p.out = static_cast<uint16_t*>(out);
+  p.o_ps = out_pos_stride;
+  p.o_hs = out_head_stride;
+  p.lse = lse;
+  p.cache = view_of(cache);
+  p.batch = batch_of(cache, N, q_indptr, B, block_table, table_width, kv_len, workspace);
+  p.prefix_table = prefix_table;
+  p.prefix_len = prefix_len;
+  p.draft_mask = draft_mask;
+  p.scale = scale;
+  p.n_q_heads = n_q_heads;
+  p.group = n_q_heads / cache->n_heads;
+  p.D = cache->head_dim;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cache->dtype == SPEC_BF16 ? launch_attend<__nv_bfloat16>(p, s) : launch_attend<__half>(p, s);
+}
+
+}  // extern "C"

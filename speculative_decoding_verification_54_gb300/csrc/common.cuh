@@ -19,6 +19,7 @@ constexpr int kStatusTimeout = 1;
 constexpr int kStatusBadToken = 2;
 constexpr int kStatusTopkOverflow = 4;  // more tied entries than a truncation list holds
 constexpr int kStatusLimit = 8;         // more candidates than the caller's capacity (centroid head)
+constexpr int kStatusBadCache = 32;     // a page, length or axis of the paged cache outside its range
 constexpr int kStatusBounds = 16;       // an index failed its check (bounds-checked build only)
 
 // Bounds checks of the debug build.  Built with -DSPEC_CHECK_BOUNDS, every

@@ -23,6 +23,7 @@
 #include "centroid.cuh"
 #include "common.cuh"
 #include "decide.cuh"
+#include "host.cuh"
 #include "lmhead.cuh"
 #include "lmtail.cuh"
 #include "rowstats.cuh"
@@ -114,8 +115,6 @@ Layout layout(int B, int gamma, int V) {
   return L;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 int check_shape(int B, int gamma, int V) {
   if (B < 1 || B > 65535) return SPEC_ERR_INVALID_ARG;
   if (gamma < 1 || gamma > SPEC_MAX_GAMMA) return SPEC_ERR_INVALID_ARG;
@@ -151,21 +150,6 @@ Plan make_plan_rows(int rows, int V, size_t esize, int sms, int path) {
 
 Plan make_plan(int B, int gamma, int V, size_t esize, int sms, bool sampling, int path) {
   return make_plan_rows(B * (sampling ? (2 * gamma + 1) : (gamma + 1)), V, esize, sms, path);
-}
-
-template <typename Kern, typename... Args>
-cudaError_t launch_pdl(Kern k, dim3 grid, dim3 block, size_t smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
 struct Common {
@@ -427,25 +411,6 @@ int check_lm_shape(int B, int gamma, int V, int H) {
   if (H < kLmTileK || H > 65536 || (H % kLmTileK) != 0) return SPEC_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * (gamma + 1) > kLmMaxRows) return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn g_encode = nullptr;
-std::mutex g_encode_mu;
-
-EncodeTiledFn encoder() {
-  std::lock_guard<std::mutex> lk(g_encode_mu);
-  if (g_encode == nullptr) {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-  }
-  return g_encode;
 }
 
 // 2-D bf16 tensor map over a [rows, H] row-major matrix: boxes of 64 x box_rows
@@ -720,11 +685,11 @@ const char* spec_verify_error_string(int code) {
     case SPEC_OK: return "ok";
     case SPEC_ERR_INVALID_ARG: return "invalid argument";
     case SPEC_ERR_UNSUPPORTED: return "unsupported dtype or shape";
-    case SPEC_ERR_ALIGNMENT: return "logit pointer not 16-byte aligned";
+    case SPEC_ERR_ALIGNMENT: return "pointer or stride not a multiple of 16 bytes";
     case SPEC_ERR_WORKSPACE: return "workspace null, misaligned or too small";
     case SPEC_ERR_CUDA: return "CUDA runtime error";
     case SPEC_ERR_TIMEOUT: return "device wait timed out";
-    case SPEC_ERR_DEVICE_INPUT: return "draft token outside [0, V)";
+    case SPEC_ERR_DEVICE_INPUT: return "draft token outside [0, V), or a page, length or axis outside its range";
     case SPEC_ERR_STATE: return "inconsistent round bookkeeping (kv_len != seq_len - 1 or accepted > gamma)";
     case SPEC_ERR_DEVICE_BOUNDS: return "device index outside its extent (bounds-checked build)";
     default: return "unknown error";
@@ -1107,7 +1072,7 @@ int spec_verify_status(void* workspace, void* stream) {
   if (cudaMemcpy(&st, workspace, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return SPEC_ERR_CUDA;
   if (st != 0 && cudaMemset(workspace, 0, sizeof(int)) != cudaSuccess) return SPEC_ERR_CUDA;
   if (st & kStatusTimeout) return SPEC_ERR_TIMEOUT;
-  if (st & kStatusBadToken) return SPEC_ERR_DEVICE_INPUT;
+  if (st & (kStatusBadToken | kStatusBadCache)) return SPEC_ERR_DEVICE_INPUT;
   if (st & (kStatusTopkOverflow | kStatusLimit)) return SPEC_ERR_UNSUPPORTED;
   if (st & kStatusBounds) return SPEC_ERR_DEVICE_BOUNDS;
   return SPEC_OK;
