@@ -1,99 +1,792 @@
 // attend.cuh — attention of the new positions over a shared prefix and their
-// sequences' pages.
+// sequences' pages, on the tcgen05 tensor cores.
+//
+// Work.  The rows of one key head are its (position, query head) pairs.  Over
+// the prefix the rows of the whole batch are one matrix, so the prefix's keys
+// and values are read once per row block and not once per sequence; over the
+// sequences' own pages the rows of one sequence are.  An item is a block of
+// up to two row tiles (128 rows each: whole positions) against all tiles of
+// 128 keys that its rows see.  The items' key tiles, weighted by their row
+// tiles, form two lines, one over the prefix and one over the own pages, and
+// CTA c takes the c-th equal part of each: lengths are read on the device, so
+// nothing is planned on the host, and one sequence or one head fills the GPU
+// as well as many.  Even CTAs begin with their prefix part (bound by the
+// tensor cores), odd ones with their own-pages part (bound by HBM), so the two
+// overlap.
+//
+// A part of an item leaves, per row, the unnormalised output, its reference
+// exponent m and the sum l: O = sum_t 2^(s_t - m) v_t, l = sum_t 2^(s_t - m)
+// with s in units of log2.  The part that holds an item's first tile writes to
+// the row's own place, any other to its CTA's slab (it is the CTA's first in
+// that line); attend_join_kernel adds a row's parts in a fixed order, so
+// results do not depend on timing.
+//
+// One CTA per SM:
+//   warps 0-3, 4-7  softmax groups 0 and 1, one thread a row.  With two row
+//                   tiles group g has tile g and both read each key tile; with
+//                   one, the groups share its rows and alternate key tiles
+//                   (their halves are joined at the end of the part), so that
+//                   exponentials of one overlap products of the other.
+//   warp 8          the scheduler and producer: finds the CTA's parts, queues
+//                   them for the others and loads key and value tiles (TMA,
+//                   one box per run of a page and 64 dims) into a ring.
+//   warp 9          one thread issues the products: S = Q K^T (both operands
+//                   from shared memory) and O += P V (P from TMEM, where the
+//                   softmax group wrote it over S; V's rows are K).
+// TMEM: S0 S1 (128 columns each) and O0 O1 (D columns each).
+//
+// The reference m of a row rises only when a tile's maximum passes it by more
+// than 2^8, and only then is O (in TMEM) multiplied; weights stay below 256, l
+// and O are exact with respect to any m.
 #pragma once
 
-#include <cfloat>
+#include <type_traits>
 
 #include "kvappend.cuh"
 #include "paged.cuh"
+#include "tc.cuh"
 
 namespace specv {
 
+constexpr int kAtTile = 128;        // rows of a row tile, keys of a key tile
+constexpr int kAtThreads = 320;
+constexpr int kAtRingBytes = 160 * 1024;
+constexpr int kAtMaxCtas = 160;     // slabs in the workspace
+constexpr int kAtQueue = 4;         // parts queued ahead
+constexpr float kAtRise = 8.f;      // log2 of the largest weight
+
 struct AttendParams {
+  CUtensorMap tmK, tmV;  // [page, head, slot, dim], boxes of 64 dims x box_rows slots
   const uint16_t* q;
   int64_t q_ps, q_hs;
   uint16_t* out;
   int64_t o_ps, o_hs;
   float* lse;
-  PagedView cache;
   PagedBatch batch;
+  int n_pages, box_rows;
   const int32_t* prefix_table;
-  int64_t prefix_len;
+  int prefix_len;
   const uint64_t* draft_mask;
-  float scale;
-  int n_q_heads, group, D;
+  float scale_log2;  // scale * log2(e)
+  int n_q_heads, n_heads, group;
+  int tok_tile;      // positions of a row tile: 128 / group
+  int n_ctas;
+  int64_t* off;      // [B + 1] where each sequence begins in the own-pages line
+  float* part_o;     // [2][N * n_q_heads][D]
+  float2* part_ml;   // [2][N * n_q_heads]
+  float* slab_o;     // [n_ctas][2][256][D]
+  float2* slab_ml;   // [n_ctas][2][256]
 };
 
-// One warp per new position and query head; lane i scores key 32 k + i.
+// ---------------------------------------------------------------------------
+// the two lines of work
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int new_positions(const PagedBatch& p) {
+  return min(max(p.q_indptr[p.B], 0), p.N);
+}
+
+// Key tiles that row block rb of a sequence sees.
+__device__ __forceinline__ int block_tiles(const AttendParams& p, const SeqSpan& s, int rb) {
+  const int kv = static_cast<int>(s.kv);
+  const int64_t last = p.draft_mask != nullptr
+                           ? kv
+                           : static_cast<int64_t>(kv) - s.n + min(static_cast<int64_t>(s.n), static_cast<int64_t>(rb + 1) * 2 * p.tok_tile);
+  return last <= 0 ? 0 : static_cast<int>((last + kAtTile - 1) / kAtTile);
+}
+
+// Row tiles of the block: its weight per key tile.
+__device__ __forceinline__ int block_weight(int positions, int tok_tile, int rb) {
+  return positions - rb * 2 * tok_tile > tok_tile ? 2 : 1;
+}
+
+// Weight of one key head's items of a sequence.
+__device__ __forceinline__ int64_t seq_head_weight(const AttendParams& p, const SeqSpan& s) {
+  int64_t w = 0;
+  for (int rb = 0; rb * 2 * p.tok_tile < s.n; ++rb)
+    w += static_cast<int64_t>(block_tiles(p, s, rb)) * block_weight(s.n, p.tok_tile, rb);
+  return w;
+}
+
+struct PrefixLine {
+  int positions, blocks, tiles;
+  int64_t per_head, total;
+};
+__device__ __forceinline__ PrefixLine prefix_line(const AttendParams& p) {
+  PrefixLine L;
+  L.positions = new_positions(p.batch);
+  L.tiles = (p.prefix_len + kAtTile - 1) / kAtTile;
+  L.blocks = (L.positions + 2 * p.tok_tile - 1) / (2 * p.tok_tile);
+  L.per_head = L.blocks > 0
+                   ? static_cast<int64_t>(L.tiles) * (2 * (L.blocks - 1) + block_weight(L.positions, p.tok_tile, L.blocks - 1))
+                   : 0;
+  L.total = L.per_head * p.n_heads;
+  return L;
+}
+
+// CTA c's part of a line of weight W begins at c * W / n; tiles belong to the
+// part that their first unit of weight lies in.
+__device__ __forceinline__ int64_t part_begin(int64_t W, int c, int n) { return W * c / n; }
+__device__ __forceinline__ int tiles_before(int64_t x, int64_t off, int w, int tiles) {
+  if (x <= off) return 0;
+  const int64_t t = (x - off + w - 1) / w;
+  return t < tiles ? static_cast<int>(t) : tiles;
+}
+
+// A part of an item, as the scheduler queues it.
+struct AtPart {
+  int line;           // 0 prefix, 1 own pages, -1 no more
+  int head, first;    // key head, first position
+  int n0, n1;         // positions of the two row tiles (n1 = 0: one tile)
+  int t0, t1;         // key tiles
+  int len, old;       // entries, entries older than the new positions
+  int seq_first, seq_n;
+  int seq;
+};
+
+// 32-byte global store (eight fp32; the address 32-byte aligned)
+__device__ __forceinline__ void st_global_f8(float* q, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(q), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// kernel
+// ---------------------------------------------------------------------------
+template <int D>
+constexpr uint32_t at_smem_bytes() {
+  return 2u * kAtTile * D * 2 + kAtRingBytes + 1024u;
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(128) attend_simple_kernel(const __grid_constant__ AttendParams p) {
-  __shared__ float s_q[4][D];
-  __shared__ int64_t s_row[4][32];
+__global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int kHalves = D / 64;                       // 64-dim halves of a tile
+  constexpr uint32_t kHalfBytes = kAtTile * 128;        // 16 KB
+  constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
+  constexpr int kSlots = kAtRingBytes / kTileBytes;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ __align__(1024) uint8_t at_smem_raw[];
+  uint8_t* smem = at_smem_raw + ((1024u - (smem_u32(at_smem_raw) & 1023u)) & 1023u);
+  uint8_t* qbuf = smem;                    // [2] query tiles
+  uint8_t* ring = smem + 2 * kTileBytes;   // [kSlots] key and value tiles
+  __shared__ __align__(8) uint64_t kv_full[kSlots], kv_empty[kSlots];
+  __shared__ __align__(8) uint64_t part_full[kAtQueue], part_empty[kAtQueue];
+  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], o_full[2], meet[2], done;
+  __shared__ AtPart parts[kAtQueue];
+  __shared__ uint32_t tmem_base;
+  __shared__ int64_t s_warp[kAtThreads / 32];
+  __shared__ int64_t s_total, s_off;
+  __shared__ int s_seq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* const status = p.batch.status;
+  const int cta = static_cast<int>(blockIdx.x);
+  grid_dep_launch();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < kAtQueue; ++i) {
+      mbar_init(&part_full[i], 1);
+      mbar_init(&part_empty[i], 9);  // eight softmax warps and the issuer
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&q_full[g], 4);
+      mbar_init(&s_full[g], 1);
+      mbar_init(&p_full[g], 4);
+      mbar_init(&o_full[g], 1);
+      mbar_init(&meet[g], 8);
+    }
+    mbar_init(&done, 1);
+    fence_mbar_init();
+    s_seq = p.batch.B;
+    s_off = 0;
+  }
+  if (warp == 9) tmem_alloc(&tmem_base, 512);
+  grid_dep_wait();
+
+  // ---- the own-pages line: its weight, and where this CTA's part begins ----
+  const int own_cta = p.n_ctas - 1 - cta;  // mirrored, so that short lines meet on different CTAs
+  int64_t first_weight = 0;
+  {
+    int64_t w = 0;
+    for (int b = threadIdx.x; b < p.batch.B; b += kAtThreads) {
+      const int64_t one = seq_head_weight(p, seq_span(p.batch, b)) * p.n_heads;
+      if (b == static_cast<int>(threadIdx.x)) first_weight = one;
+      w += one;
+    }
+    for (int x = 16; x; x >>= 1) w += __shfl_xor_sync(0xffffffffu, w, x);
+    if (lane == 0) s_warp[warp] = w;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int64_t t = 0;
+      for (int i = 0; i < kAtThreads / 32; ++i) t += s_warp[i];
+      s_total = t;
+    }
+    __syncthreads();
+    const int64_t total = s_total, lo = part_begin(total, own_cta, p.n_ctas);
+    int64_t before = 0;  // weight of the chunks before this one
+    for (int b0 = 0; b0 < p.batch.B; b0 += kAtThreads) {
+      const int b = b0 + threadIdx.x;
+      int64_t one = 0;
+      if (b < p.batch.B) one = b0 == 0 ? first_weight : seq_head_weight(p, seq_span(p.batch, b)) * p.n_heads;
+      int64_t inc = one;
+      for (int x = 1; x < 32; x <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, inc, x);
+        if (lane >= x) inc += o;
+      }
+      if (lane == 31) s_warp[warp] = inc;
+      __syncthreads();
+      int64_t base = before;
+      for (int i = 0; i < warp; ++i) base += s_warp[i];
+      const int64_t off = base + inc - one;
+      if (b < p.batch.B) {
+        if (off <= lo && lo < off + one) {
+          s_seq = b;
+          s_off = off;
+        }
+        if (cta == 0) {
+          p.off[b] = off;
+          if (b == p.batch.B - 1) p.off[b + 1] = off + one;
+        }
+      }
+      for (int i = 0; i < kAtThreads / 32; ++i) before += s_warp[i];
+      __syncthreads();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 256 + D};
+
+  if (warp == 8) {
+    // ---------------- scheduler and producer (the whole warp) ----------------
+    const PrefixLine pl = prefix_line(p);
+    const int n_boxes = kAtTile / p.box_rows;
+    const int my_box = lane % n_boxes, my_half = lane / n_boxes;
+    const bool loads = my_half < kHalves;
+    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
+    int slot = 0, queued = 0;
+    uint32_t loaded = 0;  // tiles, for the ring's phases
+    bool ok = true;
+
+    // one tile (keys or values) of 128 entries from `key0` on, of which `len`
+    // are live; boxes past them read as zero
+    auto load_tile = [&](const CUtensorMap* map, int head, int page, int key0) {
+      if (loaded >= kSlots) ok = ok && mbar_wait(&kv_empty[slot], ((loaded / kSlots) & 1) ^ 1, status, kWaitLimitCycles);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], kTileBytes);
+      __syncwarp();
+      if (loads)
+        tma_load_4d(smem_u32(ring) + slot * kTileBytes + my_half * kHalfBytes + my_box * box_bytes, map, my_half * 64,
+                    (key0 + my_box * p.box_rows) % p.batch.page_size, head, page, &kv_full[slot]);
+      ++loaded;
+      if (++slot == kSlots) slot = 0;
+    };
+    auto page_of = [&](const AtPart& a, int t) {
+      const int64_t key = static_cast<int64_t>(t) * kAtTile + my_box * p.box_rows;
+      if (!loads || t >= a.t1 || key >= a.len) return p.n_pages;  // out of range: the copy fills zeros
+      const int64_t i = key / p.batch.page_size;
+      const int page = a.line == 0 ? p.prefix_table[i]
+                                   : p.batch.block_table[static_cast<int64_t>(a.seq) * p.batch.table_width + i];
+      if (page >= 0 && page < p.n_pages) return page;
+      atomicOr(status, kStatusBadCache);
+      return p.n_pages;
+    };
+    auto run_part = [&](const AtPart& a) {
+      const int q = queued % kAtQueue;
+      if (queued >= kAtQueue)
+        ok = ok && mbar_wait(&part_empty[q], ((queued / kAtQueue) & 1) ^ 1, status, kWaitLimitCycles);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      if (lane == 0) {
+        parts[q] = a;
+        mbar_arrive(&part_full[q]);
+      }
+      ++queued;
+      if (a.line < 0) return;
+      // The order the products want them: with two row tiles K V K V ...; with
+      // one, the groups alternate and the next keys come before these values:
+      // K0 K1 V0 K2 V1 ... .
+      const int n = a.t1 - a.t0;
+      if (a.n1 > 0) {
+        int page = page_of(a, a.t0);
+        for (int t = a.t0; t < a.t1 && ok; ++t) {
+          const int next = page_of(a, t + 1);
+          load_tile(&p.tmK, a.head, page, t * kAtTile);
+          if (ok) load_tile(&p.tmV, a.head, page, t * kAtTile);
+          page = next;
+        }
+      } else {
+        int page = page_of(a, a.t0);
+        load_tile(&p.tmK, a.head, page, a.t0 * kAtTile);
+        for (int i = 0; i < n && ok; ++i) {
+          const int next = page_of(a, a.t0 + i + 1);
+          if (i + 1 < n) load_tile(&p.tmK, a.head, next, (a.t0 + i + 1) * kAtTile);
+          if (ok) load_tile(&p.tmV, a.head, page, (a.t0 + i) * kAtTile);
+          page = next;
+        }
+      }
+    };
+    for (int turn = 0; turn < 2 && ok; ++turn) {
+      AtPart a;
+      a.line = (turn ^ cta) & 1;
+      if (a.line == 0) {
+        const int64_t lo = part_begin(pl.total, cta, p.n_ctas), hi = part_begin(pl.total, cta + 1, p.n_ctas);
+        if (lo >= hi) continue;
+        a.len = a.old = p.prefix_len;
+        a.seq = a.seq_first = a.seq_n = 0;
+        int64_t head = lo / pl.per_head;
+        int rb = static_cast<int>((lo - head * pl.per_head) / (2LL * pl.tiles));
+        for (; head < p.n_heads && ok; ++head, rb = 0) {
+          bool past = false;
+          for (; rb < pl.blocks && ok; ++rb) {
+            const int64_t off = head * pl.per_head + rb * 2LL * pl.tiles;
+            past = off >= hi;
+            if (past) break;
+            const int w = block_weight(pl.positions, p.tok_tile, rb);
+            a.t0 = tiles_before(lo, off, w, pl.tiles);
+            a.t1 = tiles_before(hi, off, w, pl.tiles);
+            if (a.t0 >= a.t1) continue;
+            a.head = static_cast<int>(head);
+            a.first = rb * 2 * p.tok_tile;
+            a.n0 = min(p.tok_tile, pl.positions - a.first);
+            a.n1 = min(p.tok_tile, pl.positions - a.first - a.n0);
+            run_part(a);
+          }
+          if (past) break;
+        }
+      } else {
+        const int64_t lo = part_begin(s_total, own_cta, p.n_ctas), hi = part_begin(s_total, own_cta + 1, p.n_ctas);
+        if (lo >= hi) continue;
+        int64_t off = s_off;
+        for (int b = s_seq; b < p.batch.B && off < hi && ok; ++b) {
+          const SeqSpan s = seq_span(p.batch, b);
+          const int64_t hw = seq_head_weight(p, s);
+          a.len = static_cast<int>(s.kv);
+          a.old = a.len - s.n;
+          a.seq = b;
+          a.seq_first = s.first;
+          a.seq_n = s.n;
+          int head = 0;
+          if (hw > 0 && lo > off) {
+            head = static_cast<int>((lo - off) / hw);
+            off += head * hw;
+          }
+          for (; head < p.n_heads && off < hi && ok; ++head) {
+            for (int rb = 0; rb * 2 * p.tok_tile < s.n && ok; ++rb) {
+              const int tiles = block_tiles(p, s, rb), w = block_weight(s.n, p.tok_tile, rb);
+              a.t0 = tiles_before(lo, off, w, tiles);
+              a.t1 = tiles_before(hi, off, w, tiles);
+              off += static_cast<int64_t>(tiles) * w;
+              if (a.t0 >= a.t1) continue;
+              const int at = rb * 2 * p.tok_tile;
+              a.head = head;
+              a.first = s.first + at;
+              a.n0 = min(p.tok_tile, s.n - at);
+              a.n1 = min(p.tok_tile, s.n - at - a.n0);
+              run_part(a);
+            }
+          }
+        }
+      }
+    }
+    if (ok) {
+      AtPart end = {};
+      end.line = -1;
+      run_part(end);
+    }
+    // the copies of the last tiles land before the CTA exits
+    for (uint32_t i = loaded > kSlots ? loaded - kSlots : 0; i < loaded; ++i)
+      mbar_wait(&kv_full[i % kSlots], (i / kSlots) & 1, status, kWaitLimitCycles);
+  } else if (warp == 9) {
+    // ---------------- issuer (one thread) ----------------
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_f16_f32(kBf16, false, kAtTile, kAtTile);
+      constexpr uint32_t id_pv = idesc_f16_f32(kBf16, true, kAtTile, D);
+      uint32_t base = 0, waited = 0;  // tiles of the ring before this part, tiles known to have landed
+      uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
+      bool ok = true;
+      auto landed = [&](uint32_t i) {
+        for (; ok && waited <= i; ++waited)
+          ok = mbar_wait(&kv_full[waited % kSlots], (waited / kSlots) & 1, status, kWaitLimitCycles);
+        tc_fence_after();
+      };
+      auto qk = [&](int g, uint32_t i) {
+        landed(i);
+        if (!ok) return;
+        const uint64_t ad = smem_desc_k128(smem_u32(qbuf) + g * kTileBytes);
+        const uint64_t bd = smem_desc_k128(smem_u32(ring) + (i % kSlots) * kTileBytes);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t step = (k / 4) * (kHalfBytes >> 4) + (k % 4) * 2;
+          tc_mma(tm_s[g], ad + step, bd + step, id_qk, k > 0);
+        }
+        tc_commit(&s_full[g]);
+      };
+      auto pv = [&](int g, uint32_t i, bool first) {
+        landed(i);
+        ok = ok && mbar_wait(&p_full[g], ph_p[g], status, kWaitLimitCycles);
+        if (!ok) return;
+        ph_p[g] ^= 1;
+        tc_fence_after();
+        const uint64_t bd = smem_desc_mn128(smem_u32(ring) + (i % kSlots) * kTileBytes, kHalfBytes);
+#pragma unroll
+        for (int k = 0; k < kAtTile / 16; ++k)
+          tc_mma_ts(tm_o[g], tm_s[g] + 8 * k, bd + k * (2048 >> 4), id_pv, !first || k > 0);
+      };
+      for (int n = 0; ok; ++n) {
+        const int q = n % kAtQueue;
+        if (!mbar_wait(&part_full[q], (n / kAtQueue) & 1, status, kWaitLimitCycles)) break;
+        const AtPart a = parts[q];
+        mbar_arrive(&part_empty[q]);
+        if (a.line < 0) break;
+        const int tiles = a.t1 - a.t0;
+        const bool two = a.n1 > 0;
+        const int per = two ? tiles : (tiles + 1) / 2;  // key tiles of group 0
+        auto k_at = [&](int t) { return base + (two ? 2 * t : (t == 0 ? 0 : 2 * t - 1)); };
+        auto v_at = [&](int t) { return base + (two ? 2 * t + 1 : min(2 * t + 2, 2 * tiles - 1)); };
+        auto tile_of = [&](int g, int i) { return two ? i : 2 * i + g; };
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (tile_of(g, 0) >= tiles) continue;
+          ok = ok && mbar_wait(&q_full[g], ph_q[g], status, kWaitLimitCycles);
+          ph_q[g] ^= 1;
+          if (ok) qk(g, k_at(tile_of(g, 0)));
+          if (ok && (!two || g == 1)) tc_commit(&kv_empty[k_at(tile_of(g, 0)) % kSlots]);
+        }
+        for (int i = 0; i < per && ok; ++i) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int t = tile_of(g, i), next = tile_of(g, i + 1);
+            if (t >= tiles || !ok) continue;
+            pv(g, v_at(t), i == 0);
+            if (ok && (!two || g == 1)) tc_commit(&kv_empty[v_at(t) % kSlots]);
+            if (next < tiles) {
+              if (ok) qk(g, k_at(next));
+              if (ok && (!two || g == 1)) tc_commit(&kv_empty[k_at(next) % kSlots]);
+            } else {
+              tc_commit(&o_full[g]);
+            }
+          }
+        }
+        base += 2 * tiles;
+      }
+      // nothing is in flight when the TMEM is freed
+      tc_commit(&done);
+      mbar_wait(&done, 0, status, kWaitLimitCycles);
+    }
+  } else {
+    // ---------------- softmax groups ----------------
+    const int g = warp >> 2, quad = warp & 3, r = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    uint8_t* const my_q = qbuf + g * kTileBytes;
+    uint32_t ph_s = 0, ph_o[2] = {0, 0}, ph_meet = 0, base = 0;
+    bool ok = true;
+    // all eight warps meet (a wait with a limit, unlike a barrier instruction)
+    auto meet_all = [&](int i) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&meet[i]);
+      return __all_sync(0xffffffffu, mbar_wait(&meet[i], ph_meet, status, kWaitLimitCycles)) != 0;
+    };
+    auto products_done = [&](int o) {
+      const bool got = __all_sync(0xffffffffu, mbar_wait(&o_full[o], ph_o[o], status, kWaitLimitCycles));
+      ph_o[o] ^= 1;
+      return got;
+    };
+    for (int n = 0; ok; ++n) {
+      const int qi = n % kAtQueue;
+      ok = __all_sync(0xffffffffu, mbar_wait(&part_full[qi], (n / kAtQueue) & 1, status, kWaitLimitCycles));
+      if (!ok) break;
+      const AtPart a = parts[qi];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&part_empty[qi]);
+      if (a.line < 0) break;
+      const int tiles = a.t1 - a.t0;
+      const bool two = a.n1 > 0;
+      const int first = a.first + (two && g == 1 ? a.n0 : 0);
+      const int rows = (two && g == 1 ? a.n1 : a.n0) * p.group;
+      const int mine = two ? tiles : (tiles + 1 - g) / 2;
+      const bool warp_live = quad * 32 < rows;
+      const int tok = first + r / p.group, gq = r % p.group;
+      float m = -INFINITY, l = 0.f;
+
+      if (mine > 0) {
+        // queries, rows past the last one zero
+        for (int i = r; i < kAtTile * (D / 8); i += 128) {
+          const int row = i / (D / 8), c = i % (D / 8);
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (row < rows)
+            v = __ldg(reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(first + row / p.group) * p.q_ps +
+                                                     static_cast<int64_t>(a.head * p.group + row % p.group) * p.q_hs) + c);
+          *reinterpret_cast<uint4*>(my_q + (c / 8) * kHalfBytes + row * 128 + ((c % 8) ^ (row % 8)) * 16) = v;
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[g]);
+      }
+
+      // entries this row sees: all below `lim`, then the mask's bits from `lim` on
+      int lim = a.len;
+      uint64_t bits = 0;
+      if (a.line == 1 && r < rows) {
+        if (p.draft_mask == nullptr) {
+          lim = a.old + (tok - a.seq_first) + 1;
+        } else {
+          lim = a.old;
+          bits = p.draft_mask[tok];
+          if (a.seq_n < 64) bits &= (1ull << a.seq_n) - 1;
+        }
+      }
+      for (int i = 0; i < mine && ok; ++i) {
+        const int t = a.t0 + (two ? i : 2 * i + g);
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[g], ph_s, status, kWaitLimitCycles));
+        if (!ok) break;
+        ph_s ^= 1;
+        tc_fence_after();
+        if (warp_live) {
+          uint32_t s[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_start(tm_s[g] + lanes + 32 * c, s[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_wait(s[c]);
+          const int64_t left = static_cast<int64_t>(lim) - static_cast<int64_t>(t) * kAtTile;
+          if (__any_sync(0xffffffffu, left < kAtTile)) {
+            const int below = left < -128 ? -128 : left > 128 ? 128 : static_cast<int>(left);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int x = below - 32 * c;  // entries of this run below lim
+              uint32_t see = x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1;
+              if (bits != 0) {
+                if (x >= 0 && x < 32) see |= static_cast<uint32_t>(bits << x);
+                if (x < 0 && x > -64) see |= static_cast<uint32_t>(bits >> -x);
+              }
+#pragma unroll
+              for (int j = 0; j < 32; ++j) s[c][j] = (see >> j) & 1 ? s[c][j] : 0xff800000u;  // -inf
+            }
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(s[c][j]));
+          top *= p.scale_log2;
+          const bool rise = top > m + kAtRise || (m == -INFINITY && top > -INFINITY);
+          if (__any_sync(0xffffffffu, rise)) {
+            const float nm = rise ? top : m;
+            const float al = rise ? ex2(m - nm) : 1.f;  // 0 at a row's first keys
+            l *= al;
+            m = nm;
+            if (i > 0) {  // the last product into O is complete: S came after it
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32_start(tm_o[g] + lanes + 32 * c, o);
+                tmem_ld32_wait(o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+                tmem_st32(tm_o[g] + lanes + 32 * c, o);
+              }
+            }
+          }
+          const float sub = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; c += 2) {
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              // 16-bit weights for the product with V, half a step off at most;
+              // the sum keeps them in 32 bits
+              const float e0 = ex2(fmaf(__uint_as_float(s[c + j / 16][2 * (j % 16)]), p.scale_log2, -sub));
+              const float e1 = ex2(fmaf(__uint_as_float(s[c + j / 16][2 * (j % 16) + 1]), p.scale_log2, -sub));
+              sum[j % 2] += e0;
+              sum[2 + j % 2] += e1;
+              w[j] = Pack16<T>::pack(e0, e1);
+            }
+            tmem_st32(tm_s[g] + lanes + 16 * c, w);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+        }
+        // values past the last entry, in its page, may be anything: zero times
+        // that must be zero
+        const int live = static_cast<int>(min(static_cast<int64_t>(kAtTile), a.len - static_cast<int64_t>(t) * kAtTile));
+        const int end = (live + p.box_rows - 1) / p.box_rows * p.box_rows;
+        if (live < end) {
+          const int i0 = t - a.t0;
+          const uint32_t at = base + (two ? 2 * i0 + 1 : min(2 * i0 + 2, 2 * tiles - 1));
+          ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[at % kSlots], (at / kSlots) & 1, status, kWaitLimitCycles));
+          if (!ok) break;
+          uint8_t* v = ring + (at % kSlots) * kTileBytes;
+          for (int x = r; x < (end - live) * 8 * kHalves; x += 128) {
+            const int row = live + x / (8 * kHalves), c = x % (8 * kHalves);
+            *reinterpret_cast<uint4*>(v + (c / 8) * kHalfBytes + row * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_shared();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[g]);
+      }
+      if (!ok) break;
+
+      // ---- the part's results ----
+      float* dst_o;
+      float2* dst_ml;
+      if (a.t0 == 0) {
+        const int64_t row = (static_cast<int64_t>(a.line) * p.batch.N + tok) * p.n_q_heads + a.head * p.group + gq;
+        dst_o = p.part_o + row * D;
+        dst_ml = p.part_ml + row;
+      } else {
+        const int64_t row = (static_cast<int64_t>(cta) * 2 + a.line) * 256 + (two ? g * 128 : 0) + r;
+        dst_o = p.slab_o + row * D;
+        dst_ml = p.slab_ml + row;
+      }
+      float2* xch = reinterpret_cast<float2*>(qbuf);  // [2][128], over the queries once they are read
+      // Every phase of both groups' barriers is waited for by both groups (a
+      // wait tells neighbouring phases apart, not farther ones); with two row
+      // tiles the other group's only after this group's results are out.
+      ok = products_done(two ? g : 0);
+      if (!two && tiles > 1) ok = products_done(1) && ok;
+      if (!ok) break;
+      tc_fence_after();
+      float f0 = 1.f, f1 = 0.f;
+      if (!two) {
+        xch[g * 128 + r] = make_float2(m, l);
+        ok = meet_all(0);
+        if (!ok) break;
+        const float2 o = xch[(g ^ 1) * 128 + r];
+        const float mm = fmaxf(m, o.x);
+        const float fm = m == -INFINITY ? 0.f : ex2(m - mm), fo = o.x == -INFINITY ? 0.f : ex2(o.x - mm);
+        l = g == 0 ? l * fm + o.y * fo : o.y * fo + l * fm;
+        m = mm;
+        f0 = g == 0 ? fm : fo;
+        f1 = g == 0 ? fo : fm;
+      }
+      if (warp_live) {
+        const bool mine_to_write = r < rows;
+        if (two) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            tmem_ld32(tm_o[g] + lanes + 32 * c, v);
+            if (mine_to_write) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8)
+                st_global_f8(dst_o + 32 * c + j, v + j);
+            }
+          }
+        } else {
+          // group g joins its half of the columns
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const int col = g * (D / 2) + 32 * c;
+            float v[32], x[32];
+            tmem_ld32(tm_o[0] + lanes + col, v);
+            if (tiles > 1) {
+              tmem_ld32(tm_o[1] + lanes + col, x);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = v[j] * f0 + x[j] * f1;
+            }
+            if (mine_to_write) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8)
+                st_global_f8(dst_o + col + j, v + j);
+            }
+          }
+        }
+        if (mine_to_write && (two || g == 0)) *dst_ml = make_float2(m, l);
+      }
+      tc_fence_before();
+      if (two) {
+        ok = products_done(g ^ 1);
+      } else {  // O and the queries' buffers are free again once all have read them
+        ok = meet_all(1);
+        ph_meet ^= 1;
+      }
+      base += 2 * tiles;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// join: one warp per row adds its parts
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int kPer = D / 32;  // dims of a lane
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int n = static_cast<int>(row / p.n_q_heads), hq = static_cast<int>(row % p.n_q_heads);
   grid_dep_launch();
   grid_dep_wait();
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + warp;
-  const int n = static_cast<int>(item / p.n_q_heads), h = static_cast<int>(item % p.n_q_heads);
   if (n >= p.batch.N) return;
   const int b = find_seq(p.batch.q_indptr, p.batch.B, n, lane);
   if (b < 0) return;
-  const SeqSpan sp = seq_span(p.batch, b);
-  if (n < sp.first || n >= sp.first + sp.n) return;
-  const int hk = h / p.group;
-  for (int d = lane; d < D; d += 32) s_q[warp][d] = Pack16<T>::up(p.q[n * p.q_ps + h * p.q_hs + d]);
-  __syncwarp();
-  float o[D / 32] = {}, m = -INFINITY, l = 0.f;
-  const int64_t old = sp.kv - sp.n;
-  for (int phase = 0; phase < 2; ++phase) {
-    const int64_t len = phase == 0 ? p.prefix_len : sp.kv;
-    for (int64_t k0 = 0; k0 < len; k0 += 32) {
-      const int64_t key = k0 + lane;
-      int64_t row = -1;
-      bool seen = false;
-      if (key < len) {
-        const int page = phase == 0 ? p.prefix_table[key / p.batch.page_size]
-                                    : p.batch.block_table[static_cast<int64_t>(b) * p.batch.table_width +
-                                                          key / p.batch.page_size];
-        if (page >= 0 && page < p.cache.n_pages)
-          row = page * p.cache.page_stride + (key % p.batch.page_size) * p.cache.slot_stride + hk * p.cache.head_stride;
-        else
-          atomicOr(p.batch.status, kStatusBadCache);
-        const int64_t nw = key - old;
-        seen = phase == 0 || nw < 0 ||
-               (p.draft_mask != nullptr ? nw < 64 && ((p.draft_mask[n] >> nw) & 1) : nw <= n - sp.first);
-      }
-      float s = 0.f;
-      if (row >= 0)
-        for (int d = 0; d < D; ++d) s = fmaf(s_q[warp][d], Pack16<T>::up(p.cache.k[row + d]), s);
-      s = seen ? s * p.scale : -INFINITY;
-      float mt = s;
-      for (int x = 16; x; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-      const float mn = fmaxf(m, mt);
-      if (mn == -INFINITY) continue;
-      const float al = ex2((m - mn) * kLog2e), w = ex2((s - mn) * kLog2e);
-      m = mn;
-      l *= al;
-      for (int i = 0; i < D / 32; ++i) o[i] *= al;
-      float lt = w;
-      for (int x = 16; x; x >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, x);
-      l += lt;
-      s_row[warp][lane] = row;
-      __syncwarp();
-      for (int t = 0; t < 32; ++t) {
-        const float wt = __shfl_sync(0xffffffffu, w, t);
-        const int64_t rt = s_row[warp][t];
-        if (rt < 0 || wt == 0.f) continue;
-        for (int i = 0; i < D / 32; ++i) o[i] = fmaf(wt, Pack16<T>::up(p.cache.v[rt + i * 32 + lane]), o[i]);
-      }
-      __syncwarp();
+  const SeqSpan s = seq_span(p.batch, b);
+  if (n < s.first || n >= s.first + s.n) return;
+  const int head = hq / p.group, gq = hq % p.group;
+
+  float o[kPer] = {}, m = -INFINITY, l = 0.f;
+  // adds the parts of one item: weight w per tile, `tiles` tiles from `off` on
+  // in a line of weight W; `pos` is the row's position in the item's block
+  auto add = [&](int line, int64_t W, int64_t off, int tiles, int w, int pos) {
+    if (tiles == 0) return;
+    const int tile_row = pos % p.tok_tile * p.group + gq + (w == 2 ? pos / p.tok_tile * 128 : 0);
+    // the CTAs whose parts reach into the item
+    const int64_t last = off + static_cast<int64_t>(tiles) * w - 1;
+    const int c0 = static_cast<int>(((off + 1) * p.n_ctas - 1) / W), c1 = static_cast<int>(((last + 1) * p.n_ctas - 1) / W);
+    for (int c = c0; c <= c1; ++c) {
+      const int t0 = tiles_before(part_begin(W, c, p.n_ctas), off, w, tiles);
+      const int t1 = tiles_before(part_begin(W, c + 1, p.n_ctas), off, w, tiles);
+      if (t0 >= t1) continue;
+      const int cta = line == 0 ? c : p.n_ctas - 1 - c;
+      const int64_t at = t0 == 0 ? (static_cast<int64_t>(line) * p.batch.N + n) * p.n_q_heads + hq
+                                 : (static_cast<int64_t>(cta) * 2 + line) * 256 + tile_row;
+      const float2 ml = t0 == 0 ? p.part_ml[at] : p.slab_ml[at];
+      const float* src = (t0 == 0 ? p.part_o : p.slab_o) + at * D + lane * kPer;
+      float x[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] = src[i];
+      if (ml.x == -INFINITY) continue;  // nothing seen: its O is not looked at
+      const float mm = fmaxf(m, ml.x);
+      const float fo = m == -INFINITY ? 0.f : ex2(m - mm), fx = ex2(ml.x - mm);
+      m = mm;
+      l = l * fo + ml.y * fx;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) o[i] = o[i] * fo + x[i] * fx;
     }
+  };
+  if (p.prefix_len > 0) {
+    const PrefixLine pl = prefix_line(p);
+    const int rb = n / (2 * p.tok_tile);
+    add(0, pl.total, head * pl.per_head + rb * 2LL * pl.tiles, pl.tiles, block_weight(pl.positions, p.tok_tile, rb),
+        n - rb * 2 * p.tok_tile);
   }
+  const int64_t begin = p.off[b], total = p.off[p.batch.B];
+  if (p.off[b + 1] > begin) {
+    const int rb = (n - s.first) / (2 * p.tok_tile);
+    int64_t off = begin + head * ((p.off[b + 1] - begin) / p.n_heads);
+    for (int i = 0; i < rb; ++i)
+      off += static_cast<int64_t>(block_tiles(p, s, i)) * block_weight(s.n, p.tok_tile, i);
+    add(1, total, off, block_tiles(p, s, rb), block_weight(s.n, p.tok_tile, rb), n - s.first - rb * 2 * p.tok_tile);
+  }
+
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int i = 0; i < D / 32; ++i)
-    p.out[n * p.o_ps + h * p.o_hs + i * 32 + lane] =
-        static_cast<uint16_t>(Pack16<T>::pack(o[i] * inv, 0.f) & 0xffffu);
+  uint16_t* dst = p.out + n * p.o_ps + hq * p.o_hs + lane * kPer;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2)
+    *reinterpret_cast<uint32_t*>(dst + i) = Pack16<T>::pack(o[i] * inv, o[i + 1] * inv);
   if (lane == 0 && p.lse != nullptr)
-    p.lse[static_cast<int64_t>(n) * p.n_q_heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    p.lse[static_cast<int64_t>(n) * p.n_q_heads + hq] = l > 0.f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
 }
 
 }  // namespace specv

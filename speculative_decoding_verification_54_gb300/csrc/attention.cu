@@ -3,6 +3,7 @@
 // spec_prefix_attention.
 #include <cuda.h>
 #include <cmath>
+#include <mutex>
 
 #include "attend.cuh"
 #include "common.cuh"
@@ -15,16 +16,81 @@ using namespace specv;
 namespace {
 
 struct AttnLayout {
-  size_t header, total;
+  size_t header, off, part_o, part_ml, slab_o, slab_ml, total;
 };
 
+// The parts of the rows (one place per row and line) and of the CTAs (one slab
+// per CTA and line): at most two row tiles each.
 AttnLayout attn_layout(int B, int N, int n_q_heads, int D) {
   AttnLayout L;
+  const size_t rows = 2 * static_cast<size_t>(N) * n_q_heads, slab_rows = size_t(kAtMaxCtas) * 2 * 2 * kAtTile;
   size_t off = 0;
-  L.header = off;
-  off += align_up(sizeof(WsHeader), 256);
+  auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off += align_up(bytes, 256);
+    return at;
+  };
+  L.header = take(sizeof(WsHeader));
+  L.off = take((static_cast<size_t>(B) + 1) * sizeof(int64_t));
+  L.part_o = take(rows * D * sizeof(float));
+  L.part_ml = take(rows * sizeof(float2));
+  L.slab_o = take(slab_rows * D * sizeof(float));
+  L.slab_ml = take(slab_rows * sizeof(float2));
   L.total = off;
   return L;
+}
+
+struct AttnDevice {
+  int sms = 0;
+  bool ready = false;
+};
+
+// SMs of the current device; the first call on a device raises the attention
+// kernels' shared-memory limits.
+int attn_device(int* sms) {
+  constexpr int kMaxDevices = 64;
+  static AttnDevice devices[kMaxDevices];
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SPEC_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(mu);
+  AttnDevice& d = devices[dev];
+  if (!d.ready) {
+    auto raise = [](auto kernel, uint32_t bytes) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) ==
+             cudaSuccess;
+    };
+    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        !raise(attend_kernel<__nv_bfloat16, 64>, at_smem_bytes<64>()) ||
+        !raise(attend_kernel<__nv_bfloat16, 128>, at_smem_bytes<128>()) ||
+        !raise(attend_kernel<__half, 64>, at_smem_bytes<64>()) ||
+        !raise(attend_kernel<__half, 128>, at_smem_bytes<128>()))
+      return SPEC_ERR_CUDA;
+    d.ready = true;
+  }
+  *sms = d.sms;
+  return SPEC_OK;
+}
+
+// The pool [page, head, slot, dim] in boxes of 64 dims x `rows` slots of one
+// head and page (128-byte rows, swizzled); pages past the last read as zero.
+bool encode_pool(CUtensorMap* m, const void* base, const spec_kv_cache* c, int rows) {
+  EncodeTiledFn enc = encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(c->page_size),
+                              static_cast<cuuint64_t>(c->n_heads), static_cast<cuuint64_t>(c->n_pages)};
+  // a dimension of one entry may have any stride, zero too: it is not used
+  auto bytes = [&](int64_t stride, int64_t n) {
+    return static_cast<cuuint64_t>(n == 1 ? c->head_dim : stride) * 2;
+  };
+  const cuuint64_t strides[3] = {bytes(c->slot_stride, c->page_size), bytes(c->head_stride, c->n_heads),
+                                 bytes(c->page_stride, c->n_pages)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, c->dtype == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr int kMaxRowsPerCall = 1 << 24;
@@ -96,13 +162,13 @@ int launch_append(const AppendParams& p, int interleaved, cudaStream_t s) {
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
-template <typename T>
+template <typename T, int D>
 int launch_attend(const AttendParams& p, cudaStream_t s) {
-  const int64_t items = static_cast<int64_t>(p.batch.N) * p.n_q_heads;
-  const dim3 grid(static_cast<unsigned>((items + 3) / 4));
-  const cudaError_t e = p.D == 64 ? launch_pdl(attend_simple_kernel<T, 64>, grid, dim3(128), 0, s, p)
-                                  : launch_pdl(attend_simple_kernel<T, 128>, grid, dim3(128), 0, s, p);
-  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  const int64_t rows = static_cast<int64_t>(p.batch.N) * p.n_q_heads;
+  if (launch_pdl(attend_kernel<T, D>, dim3(p.n_ctas), dim3(kAtThreads), at_smem_bytes<D>(), s, p) != cudaSuccess ||
+      launch_pdl(attend_join_kernel<T, D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, p) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  return SPEC_OK;
 }
 
 }  // namespace
@@ -176,7 +242,7 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
   if (int e = check_common(cache, n_q_heads, N, q_indptr, B, block_table, table_width, kv_len, workspace,
                            workspace_bytes))
     return e;
-  if (prefix_len < 0 || (prefix_len > 0 && prefix_table == nullptr) || !(scale > 0.f) || !std::isfinite(scale))
+  if (prefix_len < 0 || prefix_len > INT32_MAX - kAtTile || (prefix_len > 0 && prefix_table == nullptr) || !(scale > 0.f) || !std::isfinite(scale))
     return SPEC_ERR_INVALID_ARG;
   if (n_q_heads % cache->n_heads != 0) return SPEC_ERR_INVALID_ARG;
   if ((cache->head_dim != 64 && cache->head_dim != 128) || cache->page_size % 8 != 0 ||
@@ -185,7 +251,15 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
   if (!aligned16(q) || !aligned16(out) || !vec8(q_pos_stride) || !vec8(q_head_stride) || !vec8(out_pos_stride) ||
       !vec8(out_head_stride))
     return SPEC_ERR_ALIGNMENT;
+  int sms = 0;
+  if (int e = attn_device(&sms)) return e;
   AttendParams p = {};
+  // a box lies inside one page and one key tile
+  p.box_rows = 8;
+  while (p.box_rows < kAtTile && cache->page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+  if (!encode_pool(&p.tmK, cache->k_pages, cache, p.box_rows) ||
+      !encode_pool(&p.tmV, cache->v_pages, cache, p.box_rows))
+    return SPEC_ERR_INVALID_ARG;  // strides beyond what a tensor map takes
   p.q = static_cast<const uint16_t*>(q);
   p.q_ps = q_pos_stride;
   p.q_hs = q_head_stride;
@@ -193,17 +267,29 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
   p.o_ps = out_pos_stride;
   p.o_hs = out_head_stride;
   p.lse = lse;
-  p.cache = view_of(cache);
   p.batch = batch_of(cache, N, q_indptr, B, block_table, table_width, kv_len, workspace);
+  p.n_pages = static_cast<int>(cache->n_pages);
   p.prefix_table = prefix_table;
-  p.prefix_len = prefix_len;
+  p.prefix_len = static_cast<int>(prefix_len);
   p.draft_mask = draft_mask;
-  p.scale = scale;
+  p.scale_log2 = scale * kLog2e;
   p.n_q_heads = n_q_heads;
+  p.n_heads = cache->n_heads;
   p.group = n_q_heads / cache->n_heads;
-  p.D = cache->head_dim;
+  p.tok_tile = kAtTile / p.group;
+  p.n_ctas = sms < kAtMaxCtas ? sms : kAtMaxCtas;
+  const AttnLayout L = attn_layout(B, N, n_q_heads, cache->head_dim);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.off = reinterpret_cast<int64_t*>(ws + L.off);
+  p.part_o = reinterpret_cast<float*>(ws + L.part_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
+  p.slab_o = reinterpret_cast<float*>(ws + L.slab_o);
+  p.slab_ml = reinterpret_cast<float2*>(ws + L.slab_ml);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cache->dtype == SPEC_BF16 ? launch_attend<__nv_bfloat16>(p, s) : launch_attend<__half>(p, s);
+  const bool bf16 = cache->dtype == SPEC_BF16;
+  if (cache->head_dim == 64)
+    return bf16 ? launch_attend<__nv_bfloat16, 64>(p, s) : launch_attend<__half, 64>(p, s);
+  return bf16 ? launch_attend<__nv_bfloat16, 128>(p, s) : launch_attend<__half, 128>(p, s);
 }
 
 }  // extern "C"
