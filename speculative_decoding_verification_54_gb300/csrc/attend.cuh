@@ -33,6 +33,7 @@
 //   warp 9          one thread issues the products: S = Q K^T (both operands
 //                   from shared memory) and O += P V (P from TMEM, where the
 //                   softmax group wrote it over S; V's rows are K).
+//   warps 10, 11    only fill their warpgroup.
 // TMEM: S0 S1 (128 columns each) and O0 O1 (D columns each).
 //
 // The reference m of a row rises only when a tile's maximum passes it by more
@@ -49,7 +50,11 @@
 namespace specv {
 
 constexpr int kAtTile = 128;        // rows of a row tile, keys of a key tile
-constexpr int kAtThreads = 320;
+constexpr int kAtThreads = 384;     // three warpgroups
+// Registers: the launch gives 168 a thread (65,536 / 384, by 8); the softmax
+// groups hold a row's 128 scores and take 216, the third warpgroup keeps 72:
+// 216 + 216 + 72 = 3 x 168.
+constexpr int kAtSoftmaxRegs = 216, kAtOtherRegs = 72;
 constexpr int kAtRingBytes = 160 * 1024;
 constexpr int kAtMaxCtas = 160;     // slabs in the workspace
 constexpr int kAtQueue = 4;         // parts queued ahead
@@ -72,6 +77,7 @@ struct AttendParams {
   int tok_tile;      // positions of a row tile: 128 / group
   int n_ctas;
   int64_t* off;      // [B + 1] where each sequence begins in the own-pages line
+  int64_t* begin;    // [2][n_ctas + 1] where the parts begin in each line
   float* part_o;     // [2][N * n_q_heads][D]
   float2* part_ml;   // [2][N * n_q_heads]
   float* slab_o;     // [n_ctas][2][256][D]
@@ -123,12 +129,12 @@ __device__ __forceinline__ PrefixLine prefix_line(const AttendParams& p) {
   return L;
 }
 
-// CTA c's part of a line of weight W begins at c * W / n; tiles belong to the
+// Part c of n of a line of weight W begins at W * c / n; tiles belong to the
 // part that their first unit of weight lies in.
 __device__ __forceinline__ int64_t part_begin(int64_t W, int c, int n) { return W * c / n; }
 __device__ __forceinline__ int tiles_before(int64_t x, int64_t off, int w, int tiles) {
   if (x <= off) return 0;
-  const int64_t t = (x - off + w - 1) / w;
+  const int64_t t = w == 2 ? (x - off + 1) >> 1 : x - off;
   return t < tiles ? static_cast<int>(t) : tiles;
 }
 
@@ -142,6 +148,35 @@ struct AtPart {
   int seq_first, seq_n;
   int seq;
 };
+
+// two fp32 operations at once
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void f32x2_split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 // 32-byte global store (eight fp32; the address 32-byte aligned)
 __device__ __forceinline__ void st_global_f8(float* q, const float* v) {
@@ -259,227 +294,214 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 256 + D};
+  auto tm_s = [&](int g) { return tmem + 128 * g; };
+  auto tm_o = [&](int g) { return tmem + 256 + D * g; };
+  if (warp >= 8) {
+    regs_down<kAtOtherRegs>();
+    if (warp == 8) {
+      // ---------------- scheduler and producer (the whole warp) ----------------
+      const PrefixLine pl = prefix_line(p);
+      const int n_boxes = kAtTile / p.box_rows;
+      const int my_box = lane % n_boxes, my_half = lane / n_boxes;
+      const bool loads = my_half < kHalves;
+      const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
+      int slot = 0, queued = 0;
+      uint32_t loaded = 0;  // tiles, for the ring's phases
+      bool ok = true;
 
-  if (warp == 8) {
-    // ---------------- scheduler and producer (the whole warp) ----------------
-    const PrefixLine pl = prefix_line(p);
-    const int n_boxes = kAtTile / p.box_rows;
-    const int my_box = lane % n_boxes, my_half = lane / n_boxes;
-    const bool loads = my_half < kHalves;
-    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
-    int slot = 0, queued = 0;
-    uint32_t loaded = 0;  // tiles, for the ring's phases
-    bool ok = true;
-
-    // one tile (keys or values) of 128 entries from `key0` on, of which `len`
-    // are live; boxes past them read as zero
-    auto load_tile = [&](const CUtensorMap* map, int head, int page, int key0) {
-      if (loaded >= kSlots) ok = ok && mbar_wait(&kv_empty[slot], ((loaded / kSlots) & 1) ^ 1, status, kWaitLimitCycles);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], kTileBytes);
-      __syncwarp();
-      if (loads)
-        tma_load_4d(smem_u32(ring) + slot * kTileBytes + my_half * kHalfBytes + my_box * box_bytes, map, my_half * 64,
-                    (key0 + my_box * p.box_rows) % p.batch.page_size, head, page, &kv_full[slot]);
-      ++loaded;
-      if (++slot == kSlots) slot = 0;
-    };
-    auto page_of = [&](const AtPart& a, int t) {
-      const int64_t key = static_cast<int64_t>(t) * kAtTile + my_box * p.box_rows;
-      if (!loads || t >= a.t1 || key >= a.len) return p.n_pages;  // out of range: the copy fills zeros
-      const int64_t i = key / p.batch.page_size;
-      const int page = a.line == 0 ? p.prefix_table[i]
-                                   : p.batch.block_table[static_cast<int64_t>(a.seq) * p.batch.table_width + i];
-      if (page >= 0 && page < p.n_pages) return page;
-      atomicOr(status, kStatusBadCache);
-      return p.n_pages;
-    };
-    auto run_part = [&](const AtPart& a) {
-      const int q = queued % kAtQueue;
-      if (queued >= kAtQueue)
-        ok = ok && mbar_wait(&part_empty[q], ((queued / kAtQueue) & 1) ^ 1, status, kWaitLimitCycles);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      if (lane == 0) {
-        parts[q] = a;
-        mbar_arrive(&part_full[q]);
-      }
-      ++queued;
-      if (a.line < 0) return;
-      // The order the products want them: with two row tiles K V K V ...; with
-      // one, the groups alternate and the next keys come before these values:
-      // K0 K1 V0 K2 V1 ... .
-      const int n = a.t1 - a.t0;
-      if (a.n1 > 0) {
-        int page = page_of(a, a.t0);
-        for (int t = a.t0; t < a.t1 && ok; ++t) {
-          const int next = page_of(a, t + 1);
-          load_tile(&p.tmK, a.head, page, t * kAtTile);
-          if (ok) load_tile(&p.tmV, a.head, page, t * kAtTile);
-          page = next;
+      // one tile (keys or values) of 128 entries from `key0` on, of which `len`
+      // are live; boxes past them read as zero
+      auto load_tile = [&](const CUtensorMap* map, int head, int page, int key0) {
+        if (loaded >= kSlots) ok = ok && mbar_wait(&kv_empty[slot], ((loaded / kSlots) & 1) ^ 1, status, kWaitLimitCycles);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], kTileBytes);
+        __syncwarp();
+        if (loads)
+          tma_load_4d(smem_u32(ring) + slot * kTileBytes + my_half * kHalfBytes + my_box * box_bytes, map, my_half * 64,
+                      static_cast<uint32_t>(key0 + my_box * p.box_rows) % static_cast<uint32_t>(p.batch.page_size), head, page, &kv_full[slot]);
+        ++loaded;
+        if (++slot == kSlots) slot = 0;
+      };
+      auto page_of = [&](const AtPart& a, int t) {
+        const uint32_t key = static_cast<uint32_t>(t) * kAtTile + my_box * p.box_rows;
+        if (!loads || t >= a.t1 || key >= static_cast<uint32_t>(a.len)) return p.n_pages;  // the copy fills zeros
+        const uint32_t i = key / static_cast<uint32_t>(p.batch.page_size);
+        const int page = a.line == 0 ? p.prefix_table[i]
+                                     : p.batch.block_table[static_cast<int64_t>(a.seq) * p.batch.table_width + i];
+        if (page >= 0 && page < p.n_pages) return page;
+        atomicOr(status, kStatusBadCache);
+        return p.n_pages;
+      };
+      // a free place of the queue
+      auto queue_place = [&]() {
+        const int q = queued % kAtQueue;
+        if (queued >= kAtQueue)
+          ok = ok && mbar_wait(&part_empty[q], ((queued / kAtQueue) & 1) ^ 1, status, kWaitLimitCycles);
+        ok = __all_sync(0xffffffffu, ok);
+        ++queued;
+        return q;
+      };
+#pragma unroll 1
+      for (int turn = 0; turn < 2 && ok; ++turn) {
+        // the prefix's line is that of one sequence of all new positions
+        AtPart a;
+        a.line = (turn ^ cta) & 1;
+        const int64_t total = a.line == 0 ? pl.total : s_total;
+        const int c = a.line == 0 ? cta : own_cta;
+        const int64_t lo = part_begin(total, c, p.n_ctas), hi = part_begin(total, c + 1, p.n_ctas);
+        if (lane == 0) {
+          int64_t* const begin = p.begin + a.line * (p.n_ctas + 1);
+          begin[c] = lo;
+          if (c == p.n_ctas - 1) begin[c + 1] = hi;
         }
-      } else {
-        int page = page_of(a, a.t0);
-        load_tile(&p.tmK, a.head, page, a.t0 * kAtTile);
-        for (int i = 0; i < n && ok; ++i) {
-          const int next = page_of(a, a.t0 + i + 1);
-          if (i + 1 < n) load_tile(&p.tmK, a.head, next, (a.t0 + i + 1) * kAtTile);
-          if (ok) load_tile(&p.tmV, a.head, page, (a.t0 + i) * kAtTile);
-          page = next;
-        }
-      }
-    };
-    for (int turn = 0; turn < 2 && ok; ++turn) {
-      AtPart a;
-      a.line = (turn ^ cta) & 1;
-      if (a.line == 0) {
-        const int64_t lo = part_begin(pl.total, cta, p.n_ctas), hi = part_begin(pl.total, cta + 1, p.n_ctas);
-        if (lo >= hi) continue;
-        a.len = a.old = p.prefix_len;
-        a.seq = a.seq_first = a.seq_n = 0;
-        int64_t head = lo / pl.per_head;
-        int rb = static_cast<int>((lo - head * pl.per_head) / (2LL * pl.tiles));
-        for (; head < p.n_heads && ok; ++head, rb = 0) {
-          bool past = false;
-          for (; rb < pl.blocks && ok; ++rb) {
-            const int64_t off = head * pl.per_head + rb * 2LL * pl.tiles;
-            past = off >= hi;
-            if (past) break;
-            const int w = block_weight(pl.positions, p.tok_tile, rb);
-            a.t0 = tiles_before(lo, off, w, pl.tiles);
-            a.t1 = tiles_before(hi, off, w, pl.tiles);
-            if (a.t0 >= a.t1) continue;
-            a.head = static_cast<int>(head);
-            a.first = rb * 2 * p.tok_tile;
-            a.n0 = min(p.tok_tile, pl.positions - a.first);
-            a.n1 = min(p.tok_tile, pl.positions - a.first - a.n0);
-            run_part(a);
+        int64_t off = a.line == 0 ? 0 : s_off;
+        a.seq = a.line == 0 ? 0 : s_seq;
+#pragma unroll 1
+        for (; off < hi && lo < hi && ok; ++a.seq) {
+          SeqSpan s = {0, pl.positions, 0};
+          int64_t hw = pl.per_head;
+          if (a.line == 1) {
+            s = seq_span(p.batch, a.seq);
+            hw = seq_head_weight(p, s);
           }
-          if (past) break;
-        }
-      } else {
-        const int64_t lo = part_begin(s_total, own_cta, p.n_ctas), hi = part_begin(s_total, own_cta + 1, p.n_ctas);
-        if (lo >= hi) continue;
-        int64_t off = s_off;
-        for (int b = s_seq; b < p.batch.B && off < hi && ok; ++b) {
-          const SeqSpan s = seq_span(p.batch, b);
-          const int64_t hw = seq_head_weight(p, s);
-          a.len = static_cast<int>(s.kv);
-          a.old = a.len - s.n;
-          a.seq = b;
+          a.len = a.line == 0 ? p.prefix_len : static_cast<int>(s.kv);
+          a.old = a.line == 0 ? a.len : a.len - s.n;
           a.seq_first = s.first;
           a.seq_n = s.n;
-          int head = 0;
-          if (hw > 0 && lo > off) {
-            head = static_cast<int>((lo - off) / hw);
-            off += head * hw;
-          }
-          for (; head < p.n_heads && off < hi && ok; ++head) {
-            for (int rb = 0; rb * 2 * p.tok_tile < s.n && ok; ++rb) {
-              const int tiles = block_tiles(p, s, rb), w = block_weight(s.n, p.tok_tile, rb);
+          a.head = 0;
+#pragma unroll 1
+          for (; hw > 0 && lo - off >= hw && a.head < p.n_heads; ++a.head) off += hw;
+#pragma unroll 1
+          for (; a.head < p.n_heads && off < hi && ok; ++a.head) {
+#pragma unroll 1
+            for (int at = 0; at < s.n && ok; at += 2 * p.tok_tile) {
+              const int rb = at / (2 * p.tok_tile);
+              const int tiles = a.line == 0 ? pl.tiles : block_tiles(p, s, rb), w = block_weight(s.n, p.tok_tile, rb);
               a.t0 = tiles_before(lo, off, w, tiles);
               a.t1 = tiles_before(hi, off, w, tiles);
               off += static_cast<int64_t>(tiles) * w;
               if (a.t0 >= a.t1) continue;
-              const int at = rb * 2 * p.tok_tile;
-              a.head = head;
               a.first = s.first + at;
               a.n0 = min(p.tok_tile, s.n - at);
               a.n1 = min(p.tok_tile, s.n - at - a.n0);
-              run_part(a);
+              const int q = queue_place();
+              if (!ok) break;
+              if (lane == 0) {
+                parts[q] = a;
+                mbar_arrive(&part_full[q]);
+              }
+              // The order the products want the tiles in: with two row tiles
+              // K V K V ...; with one, the groups alternate and the next keys
+              // come before these values: K0 K1 V0 K2 V1 ... V.  Step i loads
+              // the keys of `kt` and the values of `vt`.
+              const int lead = a.n1 > 0 ? 0 : 1;
+              int page = page_of(a, a.t0), vpage = page;
+#pragma unroll 1
+              for (int kt = a.t0; kt < a.t1 + lead && ok; ++kt) {
+                const int vt = kt - lead, next = page_of(a, kt + 1);
+                if (kt < a.t1) load_tile(&p.tmK, a.head, page, kt * kAtTile);
+                if (vt >= a.t0 && ok) load_tile(&p.tmV, a.head, lead ? vpage : page, vt * kAtTile);
+                vpage = page;
+                page = next;
+              }
             }
           }
         }
       }
-    }
-    if (ok) {
-      AtPart end = {};
-      end.line = -1;
-      run_part(end);
-    }
-    // the copies of the last tiles land before the CTA exits
-    for (uint32_t i = loaded > kSlots ? loaded - kSlots : 0; i < loaded; ++i)
-      mbar_wait(&kv_full[i % kSlots], (i / kSlots) & 1, status, kWaitLimitCycles);
-  } else if (warp == 9) {
-    // ---------------- issuer (one thread) ----------------
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_f16_f32(kBf16, false, kAtTile, kAtTile);
-      constexpr uint32_t id_pv = idesc_f16_f32(kBf16, true, kAtTile, D);
-      uint32_t base = 0, waited = 0;  // tiles of the ring before this part, tiles known to have landed
-      uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
-      bool ok = true;
-      auto landed = [&](uint32_t i) {
-        for (; ok && waited <= i; ++waited)
-          ok = mbar_wait(&kv_full[waited % kSlots], (waited / kSlots) & 1, status, kWaitLimitCycles);
-        tc_fence_after();
-      };
-      auto qk = [&](int g, uint32_t i) {
-        landed(i);
-        if (!ok) return;
-        const uint64_t ad = smem_desc_k128(smem_u32(qbuf) + g * kTileBytes);
-        const uint64_t bd = smem_desc_k128(smem_u32(ring) + (i % kSlots) * kTileBytes);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t step = (k / 4) * (kHalfBytes >> 4) + (k % 4) * 2;
-          tc_mma(tm_s[g], ad + step, bd + step, id_qk, k > 0);
+      if (ok) {
+        const int q = queue_place();
+        if (ok && lane == 0) {
+          parts[q].line = -1;
+          mbar_arrive(&part_full[q]);
         }
-        tc_commit(&s_full[g]);
-      };
-      auto pv = [&](int g, uint32_t i, bool first) {
-        landed(i);
-        ok = ok && mbar_wait(&p_full[g], ph_p[g], status, kWaitLimitCycles);
-        if (!ok) return;
-        ph_p[g] ^= 1;
-        tc_fence_after();
-        const uint64_t bd = smem_desc_mn128(smem_u32(ring) + (i % kSlots) * kTileBytes, kHalfBytes);
+      }
+      // the copies of the last tiles land before the CTA exits
+#pragma unroll 1
+      for (uint32_t i = loaded > kSlots ? loaded - kSlots : 0; i < loaded; ++i)
+        mbar_wait(&kv_full[i % kSlots], (i / kSlots) & 1, status, kWaitLimitCycles);
+    } else if (warp == 9) {
+      // ---------------- issuer (one thread) ----------------
+      if (lane == 0) {
+        constexpr uint32_t id_qk = idesc_f16_f32(kBf16, false, kAtTile, kAtTile);
+        constexpr uint32_t id_pv = idesc_f16_f32(kBf16, true, kAtTile, D);
+        uint32_t base = 0, waited = 0;  // tiles of the ring before this part, tiles known to have landed
+        uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
+        bool ok = true;
+        auto landed = [&](uint32_t i) {
+          for (; ok && waited <= i; ++waited)
+            ok = mbar_wait(&kv_full[waited % kSlots], (waited / kSlots) & 1, status, kWaitLimitCycles);
+          tc_fence_after();
+        };
+        auto qk = [&](int g, uint32_t i) {
+          landed(i);
+          if (!ok) return;
+          const uint64_t ad = smem_desc_k128(smem_u32(qbuf) + g * kTileBytes);
+          const uint64_t bd = smem_desc_k128(smem_u32(ring) + (i % kSlots) * kTileBytes);
 #pragma unroll
-        for (int k = 0; k < kAtTile / 16; ++k)
-          tc_mma_ts(tm_o[g], tm_s[g] + 8 * k, bd + k * (2048 >> 4), id_pv, !first || k > 0);
-      };
-      for (int n = 0; ok; ++n) {
-        const int q = n % kAtQueue;
-        if (!mbar_wait(&part_full[q], (n / kAtQueue) & 1, status, kWaitLimitCycles)) break;
-        const AtPart a = parts[q];
-        mbar_arrive(&part_empty[q]);
-        if (a.line < 0) break;
-        const int tiles = a.t1 - a.t0;
-        const bool two = a.n1 > 0;
-        const int per = two ? tiles : (tiles + 1) / 2;  // key tiles of group 0
-        auto k_at = [&](int t) { return base + (two ? 2 * t : (t == 0 ? 0 : 2 * t - 1)); };
-        auto v_at = [&](int t) { return base + (two ? 2 * t + 1 : min(2 * t + 2, 2 * tiles - 1)); };
-        auto tile_of = [&](int g, int i) { return two ? i : 2 * i + g; };
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t step = (k / 4) * (kHalfBytes >> 4) + (k % 4) * 2;
+            tc_mma(tm_s(g), ad + step, bd + step, id_qk, k > 0);
+          }
+          tc_commit(&s_full[g]);
+        };
+        auto pv = [&](int g, uint32_t i, bool first) {
+          landed(i);
+          ok = ok && mbar_wait(&p_full[g], ph_p[g], status, kWaitLimitCycles);
+          if (!ok) return;
+          ph_p[g] ^= 1;
+          tc_fence_after();
+          const uint64_t bd = smem_desc_mn128(smem_u32(ring) + (i % kSlots) * kTileBytes, kHalfBytes);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (tile_of(g, 0) >= tiles) continue;
-          ok = ok && mbar_wait(&q_full[g], ph_q[g], status, kWaitLimitCycles);
-          ph_q[g] ^= 1;
-          if (ok) qk(g, k_at(tile_of(g, 0)));
-          if (ok && (!two || g == 1)) tc_commit(&kv_empty[k_at(tile_of(g, 0)) % kSlots]);
-        }
-        for (int i = 0; i < per && ok; ++i) {
+          for (int k = 0; k < kAtTile / 16; ++k)
+            tc_mma_ts(tm_o(g), tm_s(g) + 8 * k, bd + k * (2048 >> 4), id_pv, !first || k > 0);
+        };
+#pragma unroll 1
+        for (int n = 0; ok; ++n) {
+          const int q = n % kAtQueue;
+          if (!mbar_wait(&part_full[q], (n / kAtQueue) & 1, status, kWaitLimitCycles)) break;
+          const AtPart a = parts[q];
+          mbar_arrive(&part_empty[q]);
+          if (a.line < 0) break;
+          const int tiles = a.t1 - a.t0;
+          const bool two = a.n1 > 0;
+          const int per = two ? tiles : (tiles + 1) / 2;  // key tiles of group 0
+          auto k_at = [&](int t) { return base + (two ? 2 * t : (t == 0 ? 0 : 2 * t - 1)); };
+          auto v_at = [&](int t) { return base + (two ? 2 * t + 1 : min(2 * t + 2, 2 * tiles - 1)); };
+          auto tile_of = [&](int g, int i) { return two ? i : 2 * i + g; };
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const int t = tile_of(g, i), next = tile_of(g, i + 1);
-            if (t >= tiles || !ok) continue;
-            pv(g, v_at(t), i == 0);
-            if (ok && (!two || g == 1)) tc_commit(&kv_empty[v_at(t) % kSlots]);
-            if (next < tiles) {
-              if (ok) qk(g, k_at(next));
-              if (ok && (!two || g == 1)) tc_commit(&kv_empty[k_at(next) % kSlots]);
-            } else {
-              tc_commit(&o_full[g]);
+            if (tile_of(g, 0) >= tiles) continue;
+            ok = ok && mbar_wait(&q_full[g], ph_q[g], status, kWaitLimitCycles);
+            ph_q[g] ^= 1;
+            if (ok) qk(g, k_at(tile_of(g, 0)));
+            if (ok && (!two || g == 1)) tc_commit(&kv_empty[k_at(tile_of(g, 0)) % kSlots]);
+          }
+#pragma unroll 1
+          for (int i = 0; i < per && ok; ++i) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const int t = tile_of(g, i), next = tile_of(g, i + 1);
+              if (t >= tiles || !ok) continue;
+              pv(g, v_at(t), i == 0);
+              if (ok && (!two || g == 1)) tc_commit(&kv_empty[v_at(t) % kSlots]);
+              if (next < tiles) {
+                if (ok) qk(g, k_at(next));
+                if (ok && (!two || g == 1)) tc_commit(&kv_empty[k_at(next) % kSlots]);
+              } else {
+                tc_commit(&o_full[g]);
+              }
             }
           }
+          base += 2 * tiles;
         }
-        base += 2 * tiles;
+        // nothing is in flight when the TMEM is freed
+        tc_commit(&done);
+        mbar_wait(&done, 0, status, kWaitLimitCycles);
       }
-      // nothing is in flight when the TMEM is freed
-      tc_commit(&done);
-      mbar_wait(&done, 0, status, kWaitLimitCycles);
     }
   } else {
+    regs_up<kAtSoftmaxRegs>();
     // ---------------- softmax groups ----------------
     const int g = warp >> 2, quad = warp & 3, r = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
@@ -550,7 +572,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         if (warp_live) {
           uint32_t s[4][32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32_start(tm_s[g] + lanes + 32 * c, s[c]);
+          for (int c = 0; c < 4; ++c) tmem_ld32_start(tm_s(g) + lanes + 32 * c, s[c]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32_wait(s[c]);
           const int64_t left = static_cast<int64_t>(lim) - static_cast<int64_t>(t) * kAtTile;
@@ -568,12 +590,16 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
               for (int j = 0; j < 32; ++j) s[c][j] = (see >> j) & 1 ? s[c][j] : 0xff800000u;  // -inf
             }
           }
-          float top = -INFINITY;
+          float tops[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            tops[c] = __uint_as_float(s[c][0]);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(s[c][j]));
-          top *= p.scale_log2;
+            for (int j = 1; j < 31; j += 2)
+              tops[c] = fmaxf(tops[c], fmaxf(__uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1])));
+            tops[c] = fmaxf(tops[c], __uint_as_float(s[c][31]));
+          }
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.scale_log2;
           const bool rise = top > m + kAtRise || (m == -INFINITY && top > -INFINITY);
           if (__any_sync(0xffffffffu, rise)) {
             const float nm = rise ? top : m;
@@ -584,32 +610,37 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 #pragma unroll
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
-                tmem_ld32_start(tm_o[g] + lanes + 32 * c, o);
+                tmem_ld32_start(tm_o(g) + lanes + 32 * c, o);
                 tmem_ld32_wait(o);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
-                tmem_st32(tm_o[g] + lanes + 32 * c, o);
+                tmem_st32(tm_o(g) + lanes + 32 * c, o);
               }
             }
           }
           const float sub = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2), sub2 = f32x2(-sub, -sub);
+          uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int c = 0; c < 4; c += 2) {
-            uint32_t w[32];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < 16; ++j) {
               // 16-bit weights for the product with V, half a step off at most;
               // the sum keeps them in 32 bits
-              const float e0 = ex2(fmaf(__uint_as_float(s[c + j / 16][2 * (j % 16)]), p.scale_log2, -sub));
-              const float e1 = ex2(fmaf(__uint_as_float(s[c + j / 16][2 * (j % 16) + 1]), p.scale_log2, -sub));
-              sum[j % 2] += e0;
-              sum[2 + j % 2] += e1;
+              float e0, e1;
+              f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1])), scale2, sub2),
+                          e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum[j % 4] = add_f32x2(sum[j % 4], f32x2(e0, e1));
               w[j] = Pack16<T>::pack(e0, e1);
             }
-            tmem_st32(tm_s[g] + lanes + 16 * c, w);
+            tmem_st16(tm_s(g) + lanes + 16 * c, w);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          float l0, l1;
+          f32x2_split(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), l0, l1);
+          l += l0 + l1;
           tmem_st_wait();
         }
         // values past the last entry, in its page, may be anything: zero times
@@ -673,7 +704,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             float v[32];
-            tmem_ld32(tm_o[g] + lanes + 32 * c, v);
+            tmem_ld32(tm_o(g) + lanes + 32 * c, v);
             if (mine_to_write) {
 #pragma unroll
               for (int j = 0; j < 32; j += 8)
@@ -686,9 +717,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           for (int c = 0; c < D / 64; ++c) {
             const int col = g * (D / 2) + 32 * c;
             float v[32], x[32];
-            tmem_ld32(tm_o[0] + lanes + col, v);
+            tmem_ld32(tm_o(0) + lanes + col, v);
             if (tiles > 1) {
-              tmem_ld32(tm_o[1] + lanes + col, x);
+              tmem_ld32(tm_o(1) + lanes + col, x);
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = v[j] * f0 + x[j] * f1;
             }
@@ -736,48 +767,69 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const int head = hq / p.group, gq = hq % p.group;
 
   float o[kPer] = {}, m = -INFINITY, l = 0.f;
-  // adds the parts of one item: weight w per tile, `tiles` tiles from `off` on
-  // in a line of weight W; `pos` is the row's position in the item's block
-  auto add = [&](int line, int64_t W, int64_t off, int tiles, int w, int pos) {
+  // adds the parts of one item: `tiles` tiles of weight w from `off` on; `pos`
+  // is the row's position in the item's block
+  auto add = [&](int line, int64_t off, int tiles, int w, int pos) {
     if (tiles == 0) return;
     const int tile_row = pos % p.tok_tile * p.group + gq + (w == 2 ? pos / p.tok_tile * 128 : 0);
-    // the CTAs whose parts reach into the item
-    const int64_t last = off + static_cast<int64_t>(tiles) * w - 1;
-    const int c0 = static_cast<int>(((off + 1) * p.n_ctas - 1) / W), c1 = static_cast<int>(((last + 1) * p.n_ctas - 1) / W);
-    for (int c = c0; c <= c1; ++c) {
-      const int t0 = tiles_before(part_begin(W, c, p.n_ctas), off, w, tiles);
-      const int t1 = tiles_before(part_begin(W, c + 1, p.n_ctas), off, w, tiles);
-      if (t0 >= t1) continue;
-      const int cta = line == 0 ? c : p.n_ctas - 1 - c;
-      const int64_t at = t0 == 0 ? (static_cast<int64_t>(line) * p.batch.N + n) * p.n_q_heads + hq
-                                 : (static_cast<int64_t>(cta) * 2 + line) * 256 + tile_row;
-      const float2 ml = t0 == 0 ? p.part_ml[at] : p.slab_ml[at];
-      const float* src = (t0 == 0 ? p.part_o : p.slab_o) + at * D + lane * kPer;
-      float x[kPer];
+    const int64_t* begin = p.begin + line * (p.n_ctas + 1);
+    for (int c0 = 0; c0 < p.n_ctas; c0 += 32) {
+      // lane i: whether part c0 + i holds tiles of the item, and the item's first
+      const int c = c0 + lane;
+      int t0 = 0, t1 = 0;
+      if (c < p.n_ctas) {
+        t0 = tiles_before(begin[c], off, w, tiles);
+        t1 = tiles_before(begin[c + 1], off, w, tiles);
+      }
+      unsigned parts = __ballot_sync(0xffffffffu, t0 < t1);
+      const unsigned firsts = __ballot_sync(0xffffffffu, t0 == 0);
+      while (parts != 0u) {
+        // up to four parts' loads in flight, added in ascending order
+        float x[4][kPer];
+        float2 ml[4];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) x[i] = src[i];
-      if (ml.x == -INFINITY) continue;  // nothing seen: its O is not looked at
-      const float mm = fmaxf(m, ml.x);
-      const float fo = m == -INFINITY ? 0.f : ex2(m - mm), fx = ex2(ml.x - mm);
-      m = mm;
-      l = l * fo + ml.y * fx;
+        for (int k = 0; k < 4; ++k) {
+          ml[k] = make_float2(-INFINITY, 0.f);
+          if (parts == 0u) continue;
+          const int i = __ffs(parts) - 1;
+          parts &= parts - 1;
+          const bool first = (firsts >> i) & 1;
+          const int cta = line == 0 ? c0 + i : p.n_ctas - 1 - (c0 + i);
+          const int64_t at = first ? (static_cast<int64_t>(line) * p.batch.N + n) * p.n_q_heads + hq
+                                   : (static_cast<int64_t>(cta) * 2 + line) * 256 + tile_row;
+          ml[k] = (first ? p.part_ml : p.slab_ml)[at];
+          const float* src = (first ? p.part_o : p.slab_o) + at * D + lane * kPer;
+          if (kPer == 4)
+            *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(src);
+          else
+            *reinterpret_cast<float2*>(x[k]) = *reinterpret_cast<const float2*>(src);
+        }
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) o[i] = o[i] * fo + x[i] * fx;
+        for (int k = 0; k < 4; ++k) {
+          if (ml[k].x == -INFINITY) continue;  // nothing seen: its O is not looked at
+          const float mm = fmaxf(m, ml[k].x);
+          const float fo = m == -INFINITY ? 0.f : ex2(m - mm), fx = ex2(ml[k].x - mm);
+          m = mm;
+          l = l * fo + ml[k].y * fx;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) o[i] = o[i] * fo + x[k][i] * fx;
+        }
+      }
     }
   };
   if (p.prefix_len > 0) {
     const PrefixLine pl = prefix_line(p);
     const int rb = n / (2 * p.tok_tile);
-    add(0, pl.total, head * pl.per_head + rb * 2LL * pl.tiles, pl.tiles, block_weight(pl.positions, p.tok_tile, rb),
+    add(0, head * pl.per_head + rb * 2LL * pl.tiles, pl.tiles, block_weight(pl.positions, p.tok_tile, rb),
         n - rb * 2 * p.tok_tile);
   }
-  const int64_t begin = p.off[b], total = p.off[p.batch.B];
-  if (p.off[b + 1] > begin) {
+  const int64_t begin = p.off[b], weight = p.off[b + 1] - begin;
+  if (weight > 0) {
     const int rb = (n - s.first) / (2 * p.tok_tile);
-    int64_t off = begin + head * ((p.off[b + 1] - begin) / p.n_heads);
+    int64_t off = begin + head * (weight / p.n_heads);
     for (int i = 0; i < rb; ++i)
       off += static_cast<int64_t>(block_tiles(p, s, i)) * block_weight(s.n, p.tok_tile, i);
-    add(1, total, off, block_tiles(p, s, rb), block_weight(s.n, p.tok_tile, rb), n - s.first - rb * 2 * p.tok_tile);
+    add(1, off, block_tiles(p, s, rb), block_weight(s.n, p.tok_tile, rb), n - s.first - rb * 2 * p.tok_tile);
   }
 
   const float inv = l > 0.f ? 1.f / l : 0.f;

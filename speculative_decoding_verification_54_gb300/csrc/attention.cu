@@ -16,7 +16,7 @@ using namespace specv;
 namespace {
 
 struct AttnLayout {
-  size_t header, off, part_o, part_ml, slab_o, slab_ml, total;
+  size_t header, off, begin, part_o, part_ml, slab_o, slab_ml, total;
 };
 
 // The parts of the rows (one place per row and line) and of the CTAs (one slab
@@ -32,6 +32,7 @@ AttnLayout attn_layout(int B, int N, int n_q_heads, int D) {
   };
   L.header = take(sizeof(WsHeader));
   L.off = take((static_cast<size_t>(B) + 1) * sizeof(int64_t));
+  L.begin = take(2 * (size_t(kAtMaxCtas) + 1) * sizeof(int64_t));
   L.part_o = take(rows * D * sizeof(float));
   L.part_ml = take(rows * sizeof(float2));
   L.slab_o = take(slab_rows * D * sizeof(float));
@@ -281,6 +282,7 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
   const AttnLayout L = attn_layout(B, N, n_q_heads, cache->head_dim);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.off = reinterpret_cast<int64_t*>(ws + L.off);
+  p.begin = reinterpret_cast<int64_t*>(ws + L.begin);
   p.part_o = reinterpret_cast<float*>(ws + L.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
   p.slab_o = reinterpret_cast<float*>(ws + L.slab_o);
