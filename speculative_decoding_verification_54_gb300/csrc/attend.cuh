@@ -62,8 +62,7 @@ constexpr float kAtRise = 8.f;      // log2 of the largest weight
 
 struct AttendParams {
   CUtensorMap tmK, tmV;  // [page, head, slot, dim], boxes of 64 dims x box_rows slots
-  const uint16_t* q;
-  int64_t q_ps, q_hs;
+  CUtensorMap tmQ;       // [position, head, dim], boxes of 64 dims x group heads x tok_tile positions
   uint16_t* out;
   int64_t o_ps, o_hs;
   float* lse;
@@ -188,30 +187,37 @@ __device__ __forceinline__ void st_global_f8(float* q, const float* v) {
 // ---------------------------------------------------------------------------
 // kernel
 // ---------------------------------------------------------------------------
+// What follows the query tiles and the ring in shared memory.
+template <int kSlots>
+struct AtShared {
+  uint64_t kv_full[kSlots], kv_empty[kSlots], part_full[kAtQueue], part_empty[kAtQueue];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], meet[2], done;
+  float2 xch[2][kAtTile];  // the groups' (m, l)
+  AtPart parts[kAtQueue];
+  int64_t warp_sum[kAtThreads / 32], total, off;
+  int seq;
+  uint32_t tmem;
+};
+template <int D>
+constexpr int kAtSlots = kAtRingBytes / (kAtTile * D * 2);
 template <int D>
 constexpr uint32_t at_smem_bytes() {
-  return 2u * kAtTile * D * 2 + kAtRingBytes + 1024u;
+  return 2u * kAtTile * D * 2 + kAtRingBytes + sizeof(AtShared<kAtSlots<D>>);
 }
+static_assert(at_smem_bytes<128>() <= 227 * 1024, "one CTA's shared memory");
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
   constexpr int kHalves = D / 64;                       // 64-dim halves of a tile
   constexpr uint32_t kHalfBytes = kAtTile * 128;        // 16 KB
   constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
-  constexpr int kSlots = kAtRingBytes / kTileBytes;
+  constexpr int kSlots = kAtSlots<D>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  extern __shared__ __align__(1024) uint8_t at_smem_raw[];
-  uint8_t* smem = at_smem_raw + ((1024u - (smem_u32(at_smem_raw) & 1023u)) & 1023u);
-  uint8_t* qbuf = smem;                    // [2] query tiles
-  uint8_t* ring = smem + 2 * kTileBytes;   // [kSlots] key and value tiles
-  __shared__ __align__(8) uint64_t kv_full[kSlots], kv_empty[kSlots];
-  __shared__ __align__(8) uint64_t part_full[kAtQueue], part_empty[kAtQueue];
-  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], o_full[2], meet[2], done;
-  __shared__ AtPart parts[kAtQueue];
-  __shared__ uint32_t tmem_base;
-  __shared__ int64_t s_warp[kAtThreads / 32];
-  __shared__ int64_t s_total, s_off;
-  __shared__ int s_seq;
+  // no static shared memory: the swizzled tiles begin at its (1024-byte aligned) start
+  extern __shared__ __align__(1024) uint8_t at_smem[];
+  uint8_t* const qbuf = at_smem;                   // [2] query tiles
+  uint8_t* const ring = at_smem + 2 * kTileBytes;  // [kSlots] key and value tiles
+  AtShared<kSlots>& sh = *reinterpret_cast<AtShared<kSlots>*>(ring + kAtRingBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* const status = p.batch.status;
   const int cta = static_cast<int>(blockIdx.x);
@@ -219,26 +225,27 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&sh.kv_full[i], 1);
+      mbar_init(&sh.kv_empty[i], 1);
     }
     for (int i = 0; i < kAtQueue; ++i) {
-      mbar_init(&part_full[i], 1);
-      mbar_init(&part_empty[i], 9);  // eight softmax warps and the issuer
+      mbar_init(&sh.part_full[i], 1);
+      mbar_init(&sh.part_empty[i], 9);  // eight softmax warps and the issuer
     }
     for (int g = 0; g < 2; ++g) {
-      mbar_init(&q_full[g], 4);
-      mbar_init(&s_full[g], 1);
-      mbar_init(&p_full[g], 4);
-      mbar_init(&o_full[g], 1);
-      mbar_init(&meet[g], 8);
+      mbar_init(&sh.q_full[g], 1);
+      mbar_init(&sh.q_empty[g], 1);
+      mbar_init(&sh.s_full[g], 1);
+      mbar_init(&sh.p_full[g], 4);
+      mbar_init(&sh.o_full[g], 1);
+      mbar_init(&sh.meet[g], 8);
     }
-    mbar_init(&done, 1);
+    mbar_init(&sh.done, 1);
     fence_mbar_init();
-    s_seq = p.batch.B;
-    s_off = 0;
+    sh.seq = p.batch.B;
+    sh.off = 0;
   }
-  if (warp == 9) tmem_alloc(&tmem_base, 512);
+  if (warp == 9) tmem_alloc(&sh.tmem, 512);
   grid_dep_wait();
 
   // ---- the own-pages line: its weight, and where this CTA's part begins ----
@@ -252,15 +259,15 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       w += one;
     }
     for (int x = 16; x; x >>= 1) w += __shfl_xor_sync(0xffffffffu, w, x);
-    if (lane == 0) s_warp[warp] = w;
+    if (lane == 0) sh.warp_sum[warp] = w;
     __syncthreads();
     if (threadIdx.x == 0) {
       int64_t t = 0;
-      for (int i = 0; i < kAtThreads / 32; ++i) t += s_warp[i];
-      s_total = t;
+      for (int i = 0; i < kAtThreads / 32; ++i) t += sh.warp_sum[i];
+      sh.total = t;
     }
     __syncthreads();
-    const int64_t total = s_total, lo = part_begin(total, own_cta, p.n_ctas);
+    const int64_t total = sh.total, lo = part_begin(total, own_cta, p.n_ctas);
     int64_t before = 0;  // weight of the chunks before this one
     for (int b0 = 0; b0 < p.batch.B; b0 += kAtThreads) {
       const int b = b0 + threadIdx.x;
@@ -271,29 +278,29 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         const int64_t o = __shfl_up_sync(0xffffffffu, inc, x);
         if (lane >= x) inc += o;
       }
-      if (lane == 31) s_warp[warp] = inc;
+      if (lane == 31) sh.warp_sum[warp] = inc;
       __syncthreads();
       int64_t base = before;
-      for (int i = 0; i < warp; ++i) base += s_warp[i];
+      for (int i = 0; i < warp; ++i) base += sh.warp_sum[i];
       const int64_t off = base + inc - one;
       if (b < p.batch.B) {
         if (off <= lo && lo < off + one) {
-          s_seq = b;
-          s_off = off;
+          sh.seq = b;
+          sh.off = off;
         }
         if (cta == 0) {
           p.off[b] = off;
           if (b == p.batch.B - 1) p.off[b + 1] = off + one;
         }
       }
-      for (int i = 0; i < kAtThreads / 32; ++i) before += s_warp[i];
+      for (int i = 0; i < kAtThreads / 32; ++i) before += sh.warp_sum[i];
       __syncthreads();
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = sh.tmem;
   auto tm_s = [&](int g) { return tmem + 128 * g; };
   auto tm_o = [&](int g) { return tmem + 256 + D * g; };
   if (warp >= 8) {
@@ -312,16 +319,34 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       // one tile (keys or values) of 128 entries from `key0` on, of which `len`
       // are live; boxes past them read as zero
       auto load_tile = [&](const CUtensorMap* map, int head, int page, int key0) {
-        if (loaded >= kSlots) ok = ok && mbar_wait(&kv_empty[slot], ((loaded / kSlots) & 1) ^ 1, status, kWaitLimitCycles);
+        if (loaded >= kSlots) ok = ok && mbar_wait(&sh.kv_empty[slot], ((loaded / kSlots) & 1) ^ 1, status, kWaitLimitCycles);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], kTileBytes);
+        if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[slot], kTileBytes);
         __syncwarp();
         if (loads)
           tma_load_4d(smem_u32(ring) + slot * kTileBytes + my_half * kHalfBytes + my_box * box_bytes, map, my_half * 64,
-                      static_cast<uint32_t>(key0 + my_box * p.box_rows) % static_cast<uint32_t>(p.batch.page_size), head, page, &kv_full[slot]);
+                      static_cast<uint32_t>(key0 + my_box * p.box_rows) % static_cast<uint32_t>(p.batch.page_size), head, page, &sh.kv_full[slot]);
         ++loaded;
         if (++slot == kSlots) slot = 0;
+      };
+      // the queries of a part: row tile g of two, or the one tile for each group
+      // that has key tiles
+      uint32_t q_loads[2] = {0, 0};
+      auto load_queries = [&](const AtPart& a) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (a.n1 == 0 && g == 1 && a.t1 - a.t0 < 2) continue;
+          if (q_loads[g] > 0) ok = ok && mbar_wait(&sh.q_empty[g], (q_loads[g] & 1) ^ 1, status, kWaitLimitCycles);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) return;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[g], kHalves * 128u * p.group * p.tok_tile);
+          __syncwarp();
+          if (lane < kHalves)
+            tma_load_3d(smem_u32(qbuf) + g * kTileBytes + lane * kHalfBytes, &p.tmQ, lane * 64, a.head * p.group,
+                        a.first + (a.n1 > 0 && g == 1 ? a.n0 : 0), &sh.q_full[g]);
+          ++q_loads[g];
+        }
       };
       auto page_of = [&](const AtPart& a, int t) {
         const uint32_t key = static_cast<uint32_t>(t) * kAtTile + my_box * p.box_rows;
@@ -337,7 +362,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       auto queue_place = [&]() {
         const int q = queued % kAtQueue;
         if (queued >= kAtQueue)
-          ok = ok && mbar_wait(&part_empty[q], ((queued / kAtQueue) & 1) ^ 1, status, kWaitLimitCycles);
+          ok = ok && mbar_wait(&sh.part_empty[q], ((queued / kAtQueue) & 1) ^ 1, status, kWaitLimitCycles);
         ok = __all_sync(0xffffffffu, ok);
         ++queued;
         return q;
@@ -347,7 +372,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         // the prefix's line is that of one sequence of all new positions
         AtPart a;
         a.line = (turn ^ cta) & 1;
-        const int64_t total = a.line == 0 ? pl.total : s_total;
+        const int64_t total = a.line == 0 ? pl.total : sh.total;
         const int c = a.line == 0 ? cta : own_cta;
         const int64_t lo = part_begin(total, c, p.n_ctas), hi = part_begin(total, c + 1, p.n_ctas);
         if (lane == 0) {
@@ -355,8 +380,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           begin[c] = lo;
           if (c == p.n_ctas - 1) begin[c + 1] = hi;
         }
-        int64_t off = a.line == 0 ? 0 : s_off;
-        a.seq = a.line == 0 ? 0 : s_seq;
+        int64_t off = a.line == 0 ? 0 : sh.off;
+        a.seq = a.line == 0 ? 0 : sh.seq;
 #pragma unroll 1
         for (; off < hi && lo < hi && ok; ++a.seq) {
           SeqSpan s = {0, pl.positions, 0};
@@ -388,8 +413,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
               const int q = queue_place();
               if (!ok) break;
               if (lane == 0) {
-                parts[q] = a;
-                mbar_arrive(&part_full[q]);
+                sh.parts[q] = a;
+                mbar_arrive(&sh.part_full[q]);
               }
               // The order the products want the tiles in: with two row tiles
               // K V K V ...; with one, the groups alternate and the next keys
@@ -401,7 +426,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
               for (int kt = a.t0; kt < a.t1 + lead && ok; ++kt) {
                 const int vt = kt - lead, next = page_of(a, kt + 1);
                 if (kt < a.t1) load_tile(&p.tmK, a.head, page, kt * kAtTile);
-                if (vt >= a.t0 && ok) load_tile(&p.tmV, a.head, lead ? vpage : page, vt * kAtTile);
+                if (kt == a.t0 + lead && ok) load_queries(a);  // after the first keys: the buffers may still be in use
+              if (vt >= a.t0 && ok) load_tile(&p.tmV, a.head, lead ? vpage : page, vt * kAtTile);
                 vpage = page;
                 page = next;
               }
@@ -412,14 +438,17 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       if (ok) {
         const int q = queue_place();
         if (ok && lane == 0) {
-          parts[q].line = -1;
-          mbar_arrive(&part_full[q]);
+          sh.parts[q].line = -1;
+          mbar_arrive(&sh.part_full[q]);
         }
       }
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (q_loads[g] > 0) mbar_wait(&sh.q_full[g], (q_loads[g] & 1) ^ 1, status, kWaitLimitCycles);
       // the copies of the last tiles land before the CTA exits
 #pragma unroll 1
       for (uint32_t i = loaded > kSlots ? loaded - kSlots : 0; i < loaded; ++i)
-        mbar_wait(&kv_full[i % kSlots], (i / kSlots) & 1, status, kWaitLimitCycles);
+        mbar_wait(&sh.kv_full[i % kSlots], (i / kSlots) & 1, status, kWaitLimitCycles);
     } else if (warp == 9) {
       // ---------------- issuer (one thread) ----------------
       if (lane == 0) {
@@ -430,7 +459,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         bool ok = true;
         auto landed = [&](uint32_t i) {
           for (; ok && waited <= i; ++waited)
-            ok = mbar_wait(&kv_full[waited % kSlots], (waited / kSlots) & 1, status, kWaitLimitCycles);
+            ok = mbar_wait(&sh.kv_full[waited % kSlots], (waited / kSlots) & 1, status, kWaitLimitCycles);
           tc_fence_after();
         };
         auto qk = [&](int g, uint32_t i) {
@@ -443,11 +472,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
             const uint64_t step = (k / 4) * (kHalfBytes >> 4) + (k % 4) * 2;
             tc_mma(tm_s(g), ad + step, bd + step, id_qk, k > 0);
           }
-          tc_commit(&s_full[g]);
+          tc_commit(&sh.s_full[g]);
         };
         auto pv = [&](int g, uint32_t i, bool first) {
           landed(i);
-          ok = ok && mbar_wait(&p_full[g], ph_p[g], status, kWaitLimitCycles);
+          ok = ok && mbar_wait(&sh.p_full[g], ph_p[g], status, kWaitLimitCycles);
           if (!ok) return;
           ph_p[g] ^= 1;
           tc_fence_after();
@@ -459,9 +488,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 #pragma unroll 1
         for (int n = 0; ok; ++n) {
           const int q = n % kAtQueue;
-          if (!mbar_wait(&part_full[q], (n / kAtQueue) & 1, status, kWaitLimitCycles)) break;
-          const AtPart a = parts[q];
-          mbar_arrive(&part_empty[q]);
+          if (!mbar_wait(&sh.part_full[q], (n / kAtQueue) & 1, status, kWaitLimitCycles)) break;
+          const AtPart a = sh.parts[q];
+          mbar_arrive(&sh.part_empty[q]);
           if (a.line < 0) break;
           const int tiles = a.t1 - a.t0;
           const bool two = a.n1 > 0;
@@ -472,10 +501,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             if (tile_of(g, 0) >= tiles) continue;
-            ok = ok && mbar_wait(&q_full[g], ph_q[g], status, kWaitLimitCycles);
+            ok = ok && mbar_wait(&sh.q_full[g], ph_q[g], status, kWaitLimitCycles);
             ph_q[g] ^= 1;
             if (ok) qk(g, k_at(tile_of(g, 0)));
-            if (ok && (!two || g == 1)) tc_commit(&kv_empty[k_at(tile_of(g, 0)) % kSlots]);
+            if (ok && (!two || g == 1)) tc_commit(&sh.kv_empty[k_at(tile_of(g, 0)) % kSlots]);
+            if (ok && tile_of(g, 1) >= tiles) tc_commit(&sh.q_empty[g]);
           }
 #pragma unroll 1
           for (int i = 0; i < per && ok; ++i) {
@@ -484,20 +514,21 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
               const int t = tile_of(g, i), next = tile_of(g, i + 1);
               if (t >= tiles || !ok) continue;
               pv(g, v_at(t), i == 0);
-              if (ok && (!two || g == 1)) tc_commit(&kv_empty[v_at(t) % kSlots]);
+              if (ok && (!two || g == 1)) tc_commit(&sh.kv_empty[v_at(t) % kSlots]);
               if (next < tiles) {
                 if (ok) qk(g, k_at(next));
-                if (ok && (!two || g == 1)) tc_commit(&kv_empty[k_at(next) % kSlots]);
+                if (ok && (!two || g == 1)) tc_commit(&sh.kv_empty[k_at(next) % kSlots]);
+                if (ok && tile_of(g, i + 2) >= tiles) tc_commit(&sh.q_empty[g]);
               } else {
-                tc_commit(&o_full[g]);
+                tc_commit(&sh.o_full[g]);
               }
             }
           }
           base += 2 * tiles;
         }
         // nothing is in flight when the TMEM is freed
-        tc_commit(&done);
-        mbar_wait(&done, 0, status, kWaitLimitCycles);
+        tc_commit(&sh.done);
+        mbar_wait(&sh.done, 0, status, kWaitLimitCycles);
       }
     }
   } else {
@@ -505,27 +536,26 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
     // ---------------- softmax groups ----------------
     const int g = warp >> 2, quad = warp & 3, r = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    uint8_t* const my_q = qbuf + g * kTileBytes;
     uint32_t ph_s = 0, ph_o[2] = {0, 0}, ph_meet = 0, base = 0;
     bool ok = true;
     // all eight warps meet (a wait with a limit, unlike a barrier instruction)
     auto meet_all = [&](int i) {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&meet[i]);
-      return __all_sync(0xffffffffu, mbar_wait(&meet[i], ph_meet, status, kWaitLimitCycles)) != 0;
+      if (lane == 0) mbar_arrive(&sh.meet[i]);
+      return __all_sync(0xffffffffu, mbar_wait(&sh.meet[i], ph_meet, status, kWaitLimitCycles)) != 0;
     };
     auto products_done = [&](int o) {
-      const bool got = __all_sync(0xffffffffu, mbar_wait(&o_full[o], ph_o[o], status, kWaitLimitCycles));
+      const bool got = __all_sync(0xffffffffu, mbar_wait(&sh.o_full[o], ph_o[o], status, kWaitLimitCycles));
       ph_o[o] ^= 1;
       return got;
     };
     for (int n = 0; ok; ++n) {
       const int qi = n % kAtQueue;
-      ok = __all_sync(0xffffffffu, mbar_wait(&part_full[qi], (n / kAtQueue) & 1, status, kWaitLimitCycles));
+      ok = __all_sync(0xffffffffu, mbar_wait(&sh.part_full[qi], (n / kAtQueue) & 1, status, kWaitLimitCycles));
       if (!ok) break;
-      const AtPart a = parts[qi];
+      const AtPart a = sh.parts[qi];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&part_empty[qi]);
+      if (lane == 0) mbar_arrive(&sh.part_empty[qi]);
       if (a.line < 0) break;
       const int tiles = a.t1 - a.t0;
       const bool two = a.n1 > 0;
@@ -535,21 +565,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       const bool warp_live = quad * 32 < rows;
       const int tok = first + r / p.group, gq = r % p.group;
       float m = -INFINITY, l = 0.f;
-
-      if (mine > 0) {
-        // queries, rows past the last one zero
-        for (int i = r; i < kAtTile * (D / 8); i += 128) {
-          const int row = i / (D / 8), c = i % (D / 8);
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (row < rows)
-            v = __ldg(reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(first + row / p.group) * p.q_ps +
-                                                     static_cast<int64_t>(a.head * p.group + row % p.group) * p.q_hs) + c);
-          *reinterpret_cast<uint4*>(my_q + (c / 8) * kHalfBytes + row * 128 + ((c % 8) ^ (row % 8)) * 16) = v;
-        }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[g]);
-      }
 
       // entries this row sees: all below `lim`, then the mask's bits from `lim` on
       int lim = a.len;
@@ -565,7 +580,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       }
       for (int i = 0; i < mine && ok; ++i) {
         const int t = a.t0 + (two ? i : 2 * i + g);
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[g], ph_s, status, kWaitLimitCycles));
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[g], ph_s, status, kWaitLimitCycles));
         if (!ok) break;
         ph_s ^= 1;
         tc_fence_after();
@@ -650,7 +665,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         if (live < end) {
           const int i0 = t - a.t0;
           const uint32_t at = base + (two ? 2 * i0 + 1 : min(2 * i0 + 2, 2 * tiles - 1));
-          ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[at % kSlots], (at / kSlots) & 1, status, kWaitLimitCycles));
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.kv_full[at % kSlots], (at / kSlots) & 1, status, kWaitLimitCycles));
           if (!ok) break;
           uint8_t* v = ring + (at % kSlots) * kTileBytes;
           for (int x = r; x < (end - live) * 8 * kHalves; x += 128) {
@@ -661,7 +676,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[g]);
+        if (lane == 0) mbar_arrive(&sh.p_full[g]);
       }
       if (!ok) break;
 
@@ -677,7 +692,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         dst_o = p.slab_o + row * D;
         dst_ml = p.slab_ml + row;
       }
-      float2* xch = reinterpret_cast<float2*>(qbuf);  // [2][128], over the queries once they are read
       // Every phase of both groups' barriers is waited for by both groups (a
       // wait tells neighbouring phases apart, not farther ones); with two row
       // tiles the other group's only after this group's results are out.
@@ -687,10 +701,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       tc_fence_after();
       float f0 = 1.f, f1 = 0.f;
       if (!two) {
-        xch[g * 128 + r] = make_float2(m, l);
+        sh.xch[g][r] = make_float2(m, l);
         ok = meet_all(0);
         if (!ok) break;
-        const float2 o = xch[(g ^ 1) * 128 + r];
+        const float2 o = sh.xch[g ^ 1][r];
         const float mm = fmaxf(m, o.x);
         const float fm = m == -INFINITY ? 0.f : ex2(m - mm), fo = o.x == -INFINITY ? 0.f : ex2(o.x - mm);
         l = g == 0 ? l * fm + o.y * fo : o.y * fo + l * fm;
@@ -735,7 +749,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       tc_fence_before();
       if (two) {
         ok = products_done(g ^ 1);
-      } else {  // O and the queries' buffers are free again once all have read them
+      } else {  // O and the exchanged values are free again once all have read them
         ok = meet_all(1);
         ph_meet ^= 1;
       }

@@ -163,6 +163,23 @@ int launch_append(const AppendParams& p, int interleaved, cudaStream_t s) {
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
+// The queries [position, head, dim] in boxes of one row tile: 64 dims of
+// `group` heads of `positions` positions; past the last position zeros.
+bool encode_queries(CUtensorMap* m, const void* q, const spec_kv_cache* c, int N, int n_q_heads, int64_t pos_stride,
+                    int64_t head_stride, int group, int positions) {
+  EncodeTiledFn enc = encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(n_q_heads),
+                              static_cast<cuuint64_t>(N)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(n_q_heads == 1 ? c->head_dim : head_stride) * 2,
+                                 static_cast<cuuint64_t>(N == 1 ? c->head_dim : pos_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(positions)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, c->dtype == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int D>
 int launch_attend(const AttendParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.batch.N) * p.n_q_heads;
@@ -245,7 +262,7 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
     return e;
   if (prefix_len < 0 || prefix_len > INT32_MAX - kAtTile || (prefix_len > 0 && prefix_table == nullptr) || !(scale > 0.f) || !std::isfinite(scale))
     return SPEC_ERR_INVALID_ARG;
-  if (n_q_heads % cache->n_heads != 0) return SPEC_ERR_INVALID_ARG;
+  if (n_q_heads % cache->n_heads != 0 || q_pos_stride < 0 || q_head_stride < 0) return SPEC_ERR_INVALID_ARG;
   if ((cache->head_dim != 64 && cache->head_dim != 128) || cache->page_size % 8 != 0 ||
       n_q_heads / cache->n_heads > 128)
     return SPEC_ERR_UNSUPPORTED;
@@ -258,12 +275,12 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
   // a box lies inside one page and one key tile
   p.box_rows = 8;
   while (p.box_rows < kAtTile && cache->page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+  p.group = n_q_heads / cache->n_heads;
+  p.tok_tile = kAtTile / p.group;
   if (!encode_pool(&p.tmK, cache->k_pages, cache, p.box_rows) ||
-      !encode_pool(&p.tmV, cache->v_pages, cache, p.box_rows))
+      !encode_pool(&p.tmV, cache->v_pages, cache, p.box_rows) ||
+      !encode_queries(&p.tmQ, q, cache, N, n_q_heads, q_pos_stride, q_head_stride, p.group, p.tok_tile))
     return SPEC_ERR_INVALID_ARG;  // strides beyond what a tensor map takes
-  p.q = static_cast<const uint16_t*>(q);
-  p.q_ps = q_pos_stride;
-  p.q_hs = q_head_stride;
   p.out = static_cast<uint16_t*>(out);
   p.o_ps = out_pos_stride;
   p.o_hs = out_head_stride;
@@ -276,8 +293,6 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
   p.scale_log2 = scale * kLog2e;
   p.n_q_heads = n_q_heads;
   p.n_heads = cache->n_heads;
-  p.group = n_q_heads / cache->n_heads;
-  p.tok_tile = kAtTile / p.group;
   p.n_ctas = sms < kAtMaxCtas ? sms : kAtMaxCtas;
   const AttnLayout L = attn_layout(B, N, n_q_heads, cache->head_dim);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
