@@ -50,11 +50,11 @@
 namespace specv {
 
 constexpr int kAtTile = 128;        // rows of a row tile, keys of a key tile
-constexpr int kAtStep = 64;         // keys of one step of a softmax group
 constexpr int kAtThreads = 384;     // three warpgroups
 // Registers: the launch gives 168 a thread (65,536 / 384, by 8); the softmax
-// groups take 192, the third warpgroup keeps 120: 192 + 192 + 120 = 3 x 168.
-constexpr int kAtSoftmaxRegs = 192, kAtOtherRegs = 120;
+// groups hold a row's 128 scores and take 216, the third warpgroup keeps 72:
+// 216 + 216 + 72 = 3 x 168.
+constexpr int kAtSoftmaxRegs = 216, kAtOtherRegs = 72;
 constexpr int kAtRingBytes = 160 * 1024;
 constexpr int kAtMaxCtas = 160;     // slabs in the workspace
 constexpr int kAtQueue = 4;         // parts queued ahead
@@ -196,7 +196,7 @@ __device__ __forceinline__ void st_global_f8(float* q, const float* v) {
 template <int kSlots>
 struct AtShared {
   uint64_t kv_full[kSlots], kv_empty[kSlots], part_full[kAtQueue], part_empty[kAtQueue];
-  uint64_t q_full[2], q_empty[2], s_full[4], p_full[4], o_done[4], meet[2], done;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], meet[2], done;
   float2 xch[2][kAtTile];  // the groups' (m, l)
   AtPart parts[kAtQueue];
   int64_t warp_sum[kAtThreads / 32], total, off;
@@ -240,11 +240,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
     for (int g = 0; g < 2; ++g) {
       mbar_init(&sh.q_full[g], 1);
       mbar_init(&sh.q_empty[g], 1);
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&sh.s_full[2 * g + b], 1);
-        mbar_init(&sh.p_full[2 * g + b], 4);
-        mbar_init(&sh.o_done[2 * g + b], 1);
-      }
+      mbar_init(&sh.s_full[g], 1);
+      mbar_init(&sh.p_full[g], 4);
+      mbar_init(&sh.o_full[g], 1);
       mbar_init(&sh.meet[g], 8);
     }
     mbar_init(&sh.done, 1);
@@ -308,7 +306,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  auto tm_s = [&](int g, uint32_t u) { return tmem + 128 * g + 64 * (u & 1); };
+  auto tm_s = [&](int g) { return tmem + 128 * g; };
   auto tm_o = [&](int g) { return tmem + 256 + D * g; };
   if (warp >= 8) {
     regs_down<kAtOtherRegs>();
@@ -338,10 +336,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         if (++slot == kSlots) slot = 0;
       };
       // the queries of a part: row tile g of two, or the one tile for each group
+      // that has key tiles
       uint32_t q_loads[2] = {0, 0};
       auto load_queries = [&](const AtPart& a) {
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
+          if (a.n1 == 0 && g == 1 && a.t1 - a.t0 < 2) continue;
           if (q_loads[g] > 0) ok = ok && mbar_wait(&sh.q_empty[g], (q_loads[g] & 1) ^ 1, status, kWaitLimitCycles);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) return;
@@ -421,9 +421,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
                 sh.parts[q] = a;
                 mbar_arrive(&sh.part_full[q]);
               }
-              // The order the products want the tiles in (scores run two halves
-              // of a tile ahead): with two row tiles K V K V ..., with one K0 K1
-              // V0 K2 V1 ... V.
+              // The order the products want the tiles in: with two row tiles
+              // K V K V ...; with one, the groups alternate and the next keys
+              // come before these values: K0 K1 V0 K2 V1 ... V.  Step i loads
+              // the keys of `kt` and the values of `vt`.
               const int lead = a.n1 > 0 ? 0 : 1;
               int page = page_of(a, a.t0), vpage = page;
 #pragma unroll 1
@@ -455,95 +456,92 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         mbar_wait(&sh.kv_full[i % kSlots], (i / kSlots) & 1, status, kWaitLimitCycles);
     } else if (warp == 9) {
       // ---------------- issuer (the whole warp; one thread issues) ----------------
-      constexpr uint32_t id_qk = idesc_f16_f32(kBf16, false, kAtTile, kAtStep);
+      constexpr uint32_t id_qk = idesc_f16_f32(kBf16, false, kAtTile, kAtTile);
       constexpr uint32_t id_pv = idesc_f16_f32(kBf16, true, kAtTile, D);
       const uint32_t utm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint64_t q_desc = smem_desc_k128(smem_u32(qbuf)), k_desc = smem_desc_k128(smem_u32(ring)),
                      v_desc = smem_desc_mn128(smem_u32(ring), kHalfBytes);
       uint32_t base = 0, waited = 0;  // tiles of the ring before this part, tiles known to have landed
-      uint32_t u0 = 0, parts = 0;     // steps of a group before this part; parts so far
+      uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, status, kWaitLimitCycles));
+        return ok;
       };
       auto landed = [&](uint32_t i) {
         for (; ok && waited <= i; ++waited) wait(&sh.kv_full[waited % kSlots], (waited / kSlots) & 1);
-        tc_fence_after();
+        return ok;
       };
-      // scores of group g's step u: the 64 keys from row `row` of ring tile i on;
-      // `free_tile`: the tile's last reader, `free_q`: the queries' last use
-      auto qk = [&](int g, uint32_t u, uint32_t i, int row, bool free_tile, bool free_q) {
-        landed(i);
-        if (!ok) return;
-        const uint64_t ad = q_desc + g * (kTileBytes >> 4);
-        const uint64_t bd = k_desc + (i % kSlots) * (kTileBytes >> 4) + row * (128 >> 4);
-        const uint32_t d = utm + 128 * g + 64 * (u & 1);
-        if (elect_one()) {
+      // group g's scores of ring tile i, in one thread; `free_tile`: the tile's
+      // last reader, `free_q`: the queries' last use
+      auto qk = [&](int g, uint32_t slot, bool free_tile, bool free_q) {
+        const uint64_t ad = q_desc + g * (kTileBytes >> 4), bd = k_desc + slot * (kTileBytes >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t step = (k / 4) * (kHalfBytes >> 4) + (k % 4) * 2;
-            tc_mma(d, ad + step, bd + step, id_qk, k > 0);
-          }
-          tc_commit(&sh.s_full[2 * g + (u & 1)]);
-          if (free_tile) tc_commit(&sh.kv_empty[i % kSlots]);
-          if (free_q) tc_commit(&sh.q_empty[g]);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t step = (k / 4) * (kHalfBytes >> 4) + (k % 4) * 2;
+          tc_mma(utm + 128 * g, ad + step, bd + step, id_qk, k > 0);
         }
-        __syncwarp();
+        tc_commit(&sh.s_full[g]);
+        if (free_tile) tc_commit(&sh.kv_empty[slot]);
+        if (free_q) tc_commit(&sh.q_empty[g]);
       };
-      auto pv = [&](int g, uint32_t u, uint32_t i, int row, bool first, bool free_tile) {
-        landed(i);
-        wait(&sh.p_full[2 * g + (u & 1)], (u >> 1) & 1);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t bd = v_desc + (i % kSlots) * (kTileBytes >> 4) + row * (128 >> 4);
-        const uint32_t d = utm + 256 + D * g, w = utm + 128 * g + 64 * (u & 1);
-        if (elect_one()) {
+      auto pv = [&](int g, uint32_t slot, bool first) {
+        const uint64_t bd = v_desc + slot * (kTileBytes >> 4);
 #pragma unroll
-          for (int k = 0; k < kAtStep / 16; ++k) tc_mma_ts(d, w + 8 * k, bd + k * (2048 >> 4), id_pv, !first || k > 0);
-          tc_commit(&sh.o_done[2 * g + (u & 1)]);
-          if (free_tile) tc_commit(&sh.kv_empty[i % kSlots]);
-        }
-        __syncwarp();
+        for (int k = 0; k < kAtTile / 16; ++k)
+          tc_mma_ts(utm + 256 + D * g, utm + 128 * g + 8 * k, bd + k * (2048 >> 4), id_pv, !first || k > 0);
       };
 #pragma unroll 1
-      for (; ok; ++parts) {
-        const int q = parts % kAtQueue;
-        wait(&sh.part_full[q], (parts / kAtQueue) & 1);
-        if (!ok) break;
+      for (int n = 0; ok; ++n) {
+        const int q = n % kAtQueue;
+        if (!wait(&sh.part_full[q], (n / kAtQueue) & 1)) break;
         const int line = __shfl_sync(0xffffffffu, sh.parts[q].line, 0);
         const int tiles = __shfl_sync(0xffffffffu, sh.parts[q].t1 - sh.parts[q].t0, 0);
         const bool two = __shfl_sync(0xffffffffu, sh.parts[q].n1, 0) > 0;
         if (lane == 0) mbar_arrive(&sh.part_empty[q]);
         if (line < 0) break;
-        const int steps = two ? 2 * tiles : tiles;
-        // both groups are through with a tile after group 1's (last) step on it
-        auto scores = [&](int g, int j) {
-          const int t = two ? j >> 1 : j;
-          qk(g, u0 + j, base + (two ? 2 * t : (t == 0 ? 0 : 2 * t - 1)), (two ? j & 1 : g) * kAtStep,
-             g == 1 && (!two || (j & 1)), j == steps - 1);
-        };
+        const int per = two ? tiles : (tiles + 1) / 2;  // key tiles of group 0
+        auto tile_of = [&](int g, int j) { return two ? j : 2 * j + g; };
+        auto k_at = [&](int t) { return base + (two ? 2 * t : (t == 0 ? 0 : 2 * t - 1)); };
+        auto v_at = [&](int t) { return base + (two ? 2 * t + 1 : min(2 * t + 2, 2 * tiles - 1)); };
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (j >= steps) continue;
-            if (j == 0) wait(&sh.q_full[g], parts & 1);
-            if (ok) scores(g, j);
-          }
+        for (int g = 0; g < 2; ++g) {
+          if (tile_of(g, 0) >= tiles || !ok) continue;
+          const uint32_t i = k_at(tile_of(g, 0));
+          if (!wait(&sh.q_full[g], ph_q[g]) || !landed(i)) continue;
+          ph_q[g] ^= 1;
+          tc_fence_after();
+          if (elect_one()) qk(g, i % kSlots, !two || g == 1, tile_of(g, 1) >= tiles);
+          __syncwarp();
         }
 #pragma unroll 1
-        for (int j = 0; j < steps && ok; ++j) {
+        for (int j = 0; j < per && ok; ++j) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const int t = two ? j >> 1 : j;
-            if (ok)
-              pv(g, u0 + j, base + (two ? 2 * t + 1 : min(2 * t + 2, 2 * tiles - 1)), (two ? j & 1 : g) * kAtStep,
-                 j == 0, g == 1 && (!two || (j & 1)));
-            if (ok && j + 2 < steps) scores(g, j + 2);
+            const int t = tile_of(g, j);
+            if (t >= tiles || !ok) continue;
+            // everything that can be waited for before the weights is, so that
+            // both products follow them without a pause
+            const int next = tile_of(g, j + 1);
+            const bool more = next < tiles;
+            const uint32_t vi = v_at(t), ki = more ? k_at(next) : vi;
+            const uint32_t vslot = vi % kSlots, kslot = ki % kSlots;
+            const bool free_q = tile_of(g, j + 2) >= tiles;
+            if (!landed(vi) || !landed(ki) || !wait(&sh.p_full[g], ph_p[g])) continue;
+            ph_p[g] ^= 1;
+            tc_fence_after();
+            if (elect_one()) {
+              pv(g, vslot, j == 0);
+              if (!two || g == 1) tc_commit(&sh.kv_empty[vslot]);
+              if (more)
+                qk(g, kslot, !two || g == 1, free_q);
+              else
+                tc_commit(&sh.o_full[g]);
+            }
+            __syncwarp();
           }
         }
         base += 2 * tiles;
-        u0 += steps;
       }
       // nothing is in flight when the TMEM is freed
       if (elect_one()) tc_commit(&sh.done);
@@ -555,7 +553,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
     // ---------------- softmax groups ----------------
     const int g = warp >> 2, quad = warp & 3, r = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    uint32_t u0 = 0, ph_meet = 0, base = 0;
+    uint32_t ph_s = 0, ph_o[2] = {0, 0}, ph_meet = 0, base = 0;
     bool ok = true;
     // all eight warps meet (a wait with a limit, unlike a barrier instruction)
     auto meet_all = [&](int i) {
@@ -563,11 +561,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       if (lane == 0) mbar_arrive(&sh.meet[i]);
       return __all_sync(0xffffffffu, mbar_wait(&sh.meet[i], ph_meet, status, kWaitLimitCycles)) != 0;
     };
-    // Group o's product of step u (and all before it).  A wait tells
-    // neighbouring phases apart only: u - 2, the phase before, is complete
-    // wherever this is called, because the scores of u came after it.
-    auto product_done = [&](int o, uint32_t u) {
-      return __all_sync(0xffffffffu, mbar_wait(&sh.o_done[2 * o + (u & 1)], (u >> 1) & 1, status, kWaitLimitCycles)) != 0;
+    auto products_done = [&](int o) {
+      const bool got = __all_sync(0xffffffffu, mbar_wait(&sh.o_full[o], ph_o[o], status, kWaitLimitCycles));
+      ph_o[o] ^= 1;
+      return got;
     };
     for (int n = 0; ok; ++n) {
       const int qi = n % kAtQueue;
@@ -581,7 +578,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       const bool two = a.n1 > 0;
       const int first = a.first + (two && g == 1 ? a.n0 : 0);
       const int rows = (two && g == 1 ? a.n1 : a.n0) * p.group;
-      const int steps = two ? 2 * tiles : tiles;
+      const int mine = two ? tiles : (tiles + 1 - g) / 2;
       const bool warp_live = quad * 32 < rows;
       const int tok = first + r / p.group, gq = r % p.group;
       float m = -INFINITY, l = 0.f;
@@ -598,122 +595,103 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           if (a.seq_n < 64) bits &= (1ull << a.seq_n) - 1;
         }
       }
-      for (int j = 0; j < steps && ok; ++j) {
-        const uint32_t u = u0 + j;
-        const int i = two ? j >> 1 : j, t = a.t0 + i, row0 = (two ? j & 1 : g) * kAtStep;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[2 * g + (u & 1)], (u >> 1) & 1, status, kWaitLimitCycles));
+      // Values past the last entry, in its page, may be anything: zero times that
+      // must be zero.  The tile in question, and its rows live .. end - 1.
+      const int live = a.len % kAtTile, end = (live + p.box_rows - 1) / p.box_rows * p.box_rows;
+      const int ragged = live < end ? a.len / kAtTile : -1;
+      for (int i = 0; i < mine && ok; ++i) {
+        const int t = a.t0 + (two ? i : 2 * i + g);
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[g], ph_s, status, kWaitLimitCycles));
         if (!ok) break;
+        ph_s ^= 1;
         tc_fence_after();
-        // values past the last entry, in its page, may be anything: zero times
-        // that must be zero
-        const int live = static_cast<int>(min(static_cast<int64_t>(kAtTile), a.len - static_cast<int64_t>(t) * kAtTile));
-        const int z0 = max(live, row0), z1 = min((live + p.box_rows - 1) / p.box_rows * p.box_rows, row0 + kAtStep);
-        if (z0 < z1) {
-          const uint32_t at = base + (two ? 2 * i + 1 : min(2 * i + 2, 2 * tiles - 1));
+        if (warp_live) {
+          uint32_t s[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_start(tm_s(g) + lanes + 32 * c, s[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_wait(s[c]);
+          const int left = lim - t * kAtTile;  // len + 127 is below 2^31
+          if (__any_sync(0xffffffffu, left < kAtTile)) {
+            const int below = left < -128 ? -128 : left;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int x = below - 32 * c;  // entries of this run below lim
+              uint32_t see = x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1;
+              if (bits != 0) {
+                if (x >= 0 && x < 32) see |= static_cast<uint32_t>(bits << x);
+                if (x < 0 && x > -64) see |= static_cast<uint32_t>(bits >> -x);
+              }
+#pragma unroll
+              for (int j = 0; j < 32; ++j) s[c][j] = (see >> j) & 1 ? s[c][j] : 0xff800000u;  // -inf
+            }
+          }
+          float tops[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tops[c] = max3(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]), __uint_as_float(s[c][2]));
+#pragma unroll
+            for (int j = 3; j < 31; j += 2) tops[c] = max3(tops[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
+            tops[c] = fmaxf(tops[c], __uint_as_float(s[c][31]));
+          }
+          const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * p.scale_log2;
+          const bool rise = top > m + kAtRise || (m == -INFINITY && top > -INFINITY);
+          if (__any_sync(0xffffffffu, rise)) {
+            const float nm = rise ? top : m;
+            const float al = rise ? ex2(m - nm) : 1.f;  // 0 at a row's first keys
+            l *= al;
+            m = nm;
+            if (i > 0) {  // the last product into O is complete: S came after it
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32_start(tm_o(g) + lanes + 32 * c, o);
+                tmem_ld32_wait(o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+                tmem_st32(tm_o(g) + lanes + 32 * c, o);
+              }
+            }
+          }
+          const float sub = m == -INFINITY ? 0.f : m;
+          const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2), sub2 = f32x2(-sub, -sub);
+          uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              // 16-bit weights for the product with V, half a step off at most;
+              // the sum keeps them in 32 bits
+              float e0, e1;
+              f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1])), scale2, sub2),
+                          e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum[j % 4] = add_f32x2(sum[j % 4], f32x2(e0, e1));
+              w[j] = Pack16<T>::pack(e0, e1);
+            }
+            tmem_st16(tm_s(g) + lanes + 16 * c, w);
+          }
+          float l0, l1;
+          f32x2_split(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), l0, l1);
+          l += l0 + l1;
+          tmem_st_wait();
+        }
+        if (t == ragged) {
+          const uint32_t at = base + (two ? 2 * (t - a.t0) + 1 : min(2 * (t - a.t0) + 2, 2 * tiles - 1));
           ok = __all_sync(0xffffffffu, mbar_wait(&sh.kv_full[at % kSlots], (at / kSlots) & 1, status, kWaitLimitCycles));
           if (!ok) break;
           uint8_t* v = ring + (at % kSlots) * kTileBytes;
-          for (int x = r; x < (z1 - z0) * 8 * kHalves; x += 128) {
-            const int row = z0 + x / (8 * kHalves), c = x % (8 * kHalves);
+          for (int x = r; x < (end - live) * 8 * kHalves; x += 128) {
+            const int row = live + x / (8 * kHalves), c = x % (8 * kHalves);
             *reinterpret_cast<uint4*>(v + (c / 8) * kHalfBytes + row * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_async_shared();
         }
-        auto weights_ready = [&]() {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_full[2 * g + (u & 1)]);
-        };
-        if (!warp_live) {
-          weights_ready();
-          continue;
-        }
-        const uint32_t ts = tm_s(g, u) + lanes;
-        uint32_t s[2][32];
-        tmem_ld32_start(ts, s[0]);
-        tmem_ld32_start(ts + 32, s[1]);
-        tmem_ld32_wait(s[0]);
-        tmem_ld32_wait(s[1]);
-        const int64_t left = static_cast<int64_t>(lim) - static_cast<int64_t>(t) * kAtTile - row0;
-        if (__any_sync(0xffffffffu, left < kAtStep)) {
-          const int below = left < -64 ? -64 : left > 64 ? 64 : static_cast<int>(left);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int x = below - 32 * c;  // entries of this run below lim
-            uint32_t see = x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1;
-            if (bits != 0) {
-              if (x >= 0 && x < 32) see |= static_cast<uint32_t>(bits << x);
-              if (x < 0 && x > -64) see |= static_cast<uint32_t>(bits >> -x);
-            }
-#pragma unroll
-            for (int k = 0; k < 32; ++k) s[c][k] = (see >> k) & 1 ? s[c][k] : 0xff800000u;  // -inf
-          }
-        }
-        // The weights against the reference m: 16-bit values for the product
-        // with V, half a step off at most; their sum stays in 32 bits.
-        const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
-        auto weights = [&]() {
-          const float sub = m == -INFINITY ? 0.f : -m;
-          const uint64_t sub2 = f32x2(sub, sub);
-          uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t w[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float e0, e1;
-              f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), scale2, sub2),
-                          e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              sum[k % 4] = add_f32x2(sum[k % 4], f32x2(e0, e1));
-              w[k] = Pack16<T>::pack(e0, e1);
-            }
-            tmem_st16(ts + 16 * c, w);
-          }
-          float l0, l1;
-          f32x2_split(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), l0, l1);
-          return l0 + l1;
-        };
-        // They go ahead with the reference so far while the step's maximum is
-        // found beside them, and are done again in the few steps where the
-        // reference has to rise.
-        float now = weights();
-        float tops[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t* x = &s[c / 2][16 * (c % 2)];
-          tops[c] = __uint_as_float(x[0]);
-#pragma unroll
-          for (int k = 1; k < 15; k += 2) tops[c] = max3(tops[c], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-          tops[c] = fmaxf(tops[c], __uint_as_float(x[15]));
-        }
-        const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * p.scale_log2;
-        const bool rise = top > m + kAtRise || (m == -INFINITY && top > -INFINITY);
-        if (__any_sync(0xffffffffu, rise)) {
-          const float nm = rise ? top : m;
-          const float al = rise ? ex2(m - nm) : 1.f;  // 0 at a row's first keys
-          l *= al;
-          m = nm;
-          if (j > 0) {
-            ok = product_done(g, u - 1);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32_start(tm_o(g) + lanes + 32 * c, o);
-              tmem_ld32_wait(o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-              tmem_st32(tm_o(g) + lanes + 32 * c, o);
-            }
-          }
-          now = weights();
-        }
-        l += now;
-        tmem_st_wait();
-        weights_ready();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[g]);
       }
       if (!ok) break;
 
@@ -729,8 +707,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         dst_o = p.slab_o + row * D;
         dst_ml = p.slab_ml + row;
       }
-      // the last products; with one row tile both groups'
-      ok = product_done(g, u0 + steps - 1) && (two || product_done(g ^ 1, u0 + steps - 1));
+      // Every phase of both groups' barriers is waited for by both groups (a
+      // wait tells neighbouring phases apart, not farther ones); with two row
+      // tiles the other group's only after this group's results are out.
+      ok = products_done(two ? g : 0);
+      if (!two && tiles > 1) ok = products_done(1) && ok;
       if (!ok) break;
       tc_fence_after();
       float f0 = 1.f, f1 = 0.f;
@@ -766,9 +747,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
             const int col = g * (D / 2) + 32 * c;
             float v[32], x[32];
             tmem_ld32(tm_o(0) + lanes + col, v);
-            tmem_ld32(tm_o(1) + lanes + col, x);
+            if (tiles > 1) {
+              tmem_ld32(tm_o(1) + lanes + col, x);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = v[j] * f0 + x[j] * f1;
+              for (int j = 0; j < 32; ++j) v[j] = v[j] * f0 + x[j] * f1;
+            }
             if (mine_to_write) {
 #pragma unroll
               for (int j = 0; j < 32; j += 8)
@@ -779,11 +762,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         if (mine_to_write && (two || g == 0)) *dst_ml = make_float2(m, l);
       }
       tc_fence_before();
-      if (!two) {  // O and the exchanged values are free again once all have read them
+      if (two) {
+        ok = products_done(g ^ 1);
+      } else {  // O and the exchanged values are free again once all have read them
         ok = meet_all(1);
         ph_meet ^= 1;
       }
-      u0 += steps;
       base += 2 * tiles;
     }
   }
@@ -794,96 +778,146 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------------------
-// join: one warp per row adds its parts
+// join: one warp per position and key head adds the parts of its rows (one per
+// query head: they share the items, so what finds the parts is done once)
 // ---------------------------------------------------------------------------
+// The parts that hold tiles of one item, from part c0 on: bit i of `parts` is
+// part c0 + i, `first` those that begin the item (their rows' own places).
+struct ItemParts {
+  int c0;
+  unsigned parts, first;
+  int tile_row;  // of the position's first row, in a slab
+  bool more;     // the item goes on after part c0 + 31
+};
+
+// An item of `tiles` tiles of weight w from `off` on, in a line of weight W.
+__device__ __forceinline__ ItemParts find_parts(const AttendParams& p, int line, int64_t W, int64_t off, int tiles,
+                                                int w, int pos, int c_from, int lane) {
+  ItemParts r;
+  r.tile_row = pos % p.tok_tile * p.group + (w == 2 ? pos / p.tok_tile * kAtTile : 0);
+  // part c begins at W * c / n, so `off` lies in part ((off + 1) n - 1) / W; one
+  // early for the rounding of fp32
+  r.c0 = c_from >= 0 ? c_from
+                     : max(0, static_cast<int>((static_cast<float>(off + 1) * p.n_ctas - 1.f) / static_cast<float>(W)) - 1);
+  const int64_t* begin = p.begin + line * (p.n_ctas + 1);
+  const int c = r.c0 + lane;
+  int t0 = 0, t1 = 0;
+  if (c < p.n_ctas) {
+    t0 = tiles_before(begin[c], off, w, tiles);
+    t1 = tiles_before(begin[c + 1], off, w, tiles);
+  }
+  r.parts = __ballot_sync(0xffffffffu, t0 < t1);
+  r.first = __ballot_sync(0xffffffffu, t0 == 0);
+  r.more = r.c0 + 32 < p.n_ctas && __shfl_sync(0xffffffffu, t1, 31) < tiles;
+  return r;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p) {
   constexpr int kPer = D / 32;  // dims of a lane
   const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int n = static_cast<int>(row / p.n_q_heads), hq = static_cast<int>(row % p.n_q_heads);
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int n = static_cast<int>(id / p.n_heads), head = static_cast<int>(id % p.n_heads);
   grid_dep_launch();
   grid_dep_wait();
   if (n >= p.batch.N) return;
   const int b = find_seq(p.batch.q_indptr, p.batch.B, n, lane);
   if (b < 0) return;
   const SeqSpan s = seq_span(p.batch, b);
+  const int64_t begin = p.off[b], weight = p.off[b + 1] - begin, total = p.off[p.batch.B];
   if (n < s.first || n >= s.first + s.n) return;
-  const int head = hq / p.group, gq = hq % p.group;
 
-  float o[kPer] = {}, m = -INFINITY, l = 0.f;
-  // adds the parts of one item: `tiles` tiles of weight w from `off` on; `pos`
-  // is the row's position in the item's block
-  auto add = [&](int line, int64_t off, int tiles, int w, int pos) {
-    if (tiles == 0) return;
-    const int tile_row = pos % p.tok_tile * p.group + gq + (w == 2 ? pos / p.tok_tile * 128 : 0);
-    const int64_t* begin = p.begin + line * (p.n_ctas + 1);
-    for (int c0 = 0; c0 < p.n_ctas; c0 += 32) {
-      // lane i: whether part c0 + i holds tiles of the item, and the item's first
-      const int c = c0 + lane;
-      int t0 = 0, t1 = 0;
-      if (c < p.n_ctas) {
-        t0 = tiles_before(begin[c], off, w, tiles);
-        t1 = tiles_before(begin[c + 1], off, w, tiles);
-      }
-      unsigned parts = __ballot_sync(0xffffffffu, t0 < t1);
-      const unsigned firsts = __ballot_sync(0xffffffffu, t0 == 0);
-      while (parts != 0u) {
-        // up to four parts' loads in flight, added in ascending order
-        float x[4][kPer];
-        float2 ml[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          ml[k] = make_float2(-INFINITY, 0.f);
-          if (parts == 0u) continue;
-          const int i = __ffs(parts) - 1;
-          parts &= parts - 1;
-          const bool first = (firsts >> i) & 1;
-          const int cta = line == 0 ? c0 + i : p.n_ctas - 1 - (c0 + i);
-          const int64_t at = first ? (static_cast<int64_t>(line) * p.batch.N + n) * p.n_q_heads + hq
-                                   : (static_cast<int64_t>(cta) * 2 + line) * 256 + tile_row;
-          ml[k] = (first ? p.part_ml : p.slab_ml)[at];
-          const float* src = (first ? p.part_o : p.slab_o) + at * D + lane * kPer;
-          if (kPer == 4)
-            *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(src);
-          else
-            *reinterpret_cast<float2*>(x[k]) = *reinterpret_cast<const float2*>(src);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (ml[k].x == -INFINITY) continue;  // nothing seen: its O is not looked at
-          const float mm = fmaxf(m, ml[k].x);
-          const float fo = m == -INFINITY ? 0.f : ex2(m - mm), fx = ex2(ml[k].x - mm);
-          m = mm;
-          l = l * fo + ml[k].y * fx;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) o[i] = o[i] * fo + x[k][i] * fx;
-        }
-      }
-    }
-  };
+  // the position's item in each line
+  int64_t off[2] = {0, 0}, W[2] = {1, 1};
+  int tiles[2] = {0, 0}, w[2] = {1, 1}, pos[2] = {0, 0};
   if (p.prefix_len > 0) {
     const PrefixLine pl = prefix_line(p);
     const int rb = n / (2 * p.tok_tile);
-    add(0, head * pl.per_head + rb * 2LL * pl.tiles, pl.tiles, block_weight(pl.positions, p.tok_tile, rb),
-        n - rb * 2 * p.tok_tile);
+    off[0] = head * pl.per_head + rb * 2LL * pl.tiles;
+    W[0] = pl.total;
+    tiles[0] = pl.tiles;
+    w[0] = block_weight(pl.positions, p.tok_tile, rb);
+    pos[0] = n - rb * 2 * p.tok_tile;
   }
-  const int64_t begin = p.off[b], weight = p.off[b + 1] - begin;
   if (weight > 0) {
     const int rb = (n - s.first) / (2 * p.tok_tile);
-    int64_t off = begin + head * (weight / p.n_heads);
-    for (int i = 0; i < rb; ++i)
-      off += static_cast<int64_t>(block_tiles(p, s, i)) * block_weight(s.n, p.tok_tile, i);
-    add(1, off, block_tiles(p, s, rb), block_weight(s.n, p.tok_tile, rb), n - s.first - rb * 2 * p.tok_tile);
+    off[1] = begin;
+    int64_t own = 0;  // one head's weight, and the blocks before this one
+    for (int i = 0; i * 2 * p.tok_tile < s.n; ++i) {
+      const int64_t x = static_cast<int64_t>(block_tiles(p, s, i)) * block_weight(s.n, p.tok_tile, i);
+      own += x;
+      if (i < rb) off[1] += x;
+    }
+    off[1] += head * own;
+    W[1] = total;
+    tiles[1] = block_tiles(p, s, rb);
+    w[1] = block_weight(s.n, p.tok_tile, rb);
+    pos[1] = n - s.first - rb * 2 * p.tok_tile;
+  }
+  ItemParts ip[2];
+#pragma unroll
+  for (int line = 0; line < 2; ++line) {
+    ip[line].parts = 0u;
+    if (tiles[line] > 0) ip[line] = find_parts(p, line, W[line], off[line], tiles[line], w[line], pos[line], -1, lane);
   }
 
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint16_t* dst = p.out + n * p.o_ps + hq * p.o_hs + lane * kPer;
+  for (int gq = 0; gq < p.group; ++gq) {
+    const int hq = head * p.group + gq;
+    float o[kPer] = {}, m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPer; i += 2)
-    *reinterpret_cast<uint32_t*>(dst + i) = Pack16<T>::pack(o[i] * inv, o[i + 1] * inv);
-  if (lane == 0 && p.lse != nullptr)
-    p.lse[static_cast<int64_t>(n) * p.n_q_heads + hq] = l > 0.f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+    for (int line = 0; line < 2; ++line) {
+      if (tiles[line] == 0) continue;
+      ItemParts at = ip[line];
+      const int64_t own_row = (static_cast<int64_t>(line) * p.batch.N + n) * p.n_q_heads + hq;
+      while (true) {
+        unsigned left = at.parts;
+        while (left != 0u) {
+          // up to four parts' loads in flight, added in ascending order
+          float x[4][kPer];
+          float2 ml[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (left == 0u) continue;
+            const int i = __ffs(left) - 1;
+            left &= left - 1;
+            const bool first = (at.first >> i) & 1;
+            const int c = at.c0 + i;
+            const int64_t row = first ? own_row
+                                      : (static_cast<int64_t>(line == 0 ? c : p.n_ctas - 1 - c) * 2 + line) * 256 +
+                                            at.tile_row + gq;
+            ml[k] = (first ? p.part_ml : p.slab_ml)[row];
+            const float* src = (first ? p.part_o : p.slab_o) + row * D + lane * kPer;
+            if (kPer == 4)
+              *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(src);
+            else
+              *reinterpret_cast<float2*>(x[k]) = *reinterpret_cast<const float2*>(src);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (ml[k].x == -INFINITY) continue;  // nothing seen: its O is not looked at
+            const float mm = fmaxf(m, ml[k].x);
+            const float fo = m == -INFINITY ? 0.f : ex2(m - mm), fx = ex2(ml[k].x - mm);
+            m = mm;
+            l = l * fo + ml[k].y * fx;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) o[i] = o[i] * fo + x[k][i] * fx;
+          }
+        }
+        if (!at.more) break;
+        at = find_parts(p, line, W[line], off[line], tiles[line], w[line], pos[line], at.c0 + 32, lane);
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint16_t* dst = p.out + n * p.o_ps + hq * p.o_hs + lane * kPer;
+    if (kPer == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(Pack16<T>::pack(o[0] * inv, o[1] * inv),
+                                                  Pack16<T>::pack(o[kPer - 2] * inv, o[kPer - 1] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = Pack16<T>::pack(o[0] * inv, o[1] * inv);
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[static_cast<int64_t>(n) * p.n_q_heads + hq] = l > 0.f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+  }
 }
 
 }  // namespace specv

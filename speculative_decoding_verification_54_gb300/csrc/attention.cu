@@ -182,7 +182,7 @@ bool encode_queries(CUtensorMap* m, const void* q, const spec_kv_cache* c, int N
 
 template <typename T, int D>
 int launch_attend(const AttendParams& p, cudaStream_t s) {
-  const int64_t rows = static_cast<int64_t>(p.batch.N) * p.n_q_heads;
+  const int64_t rows = static_cast<int64_t>(p.batch.N) * p.n_heads;
   if (launch_pdl(attend_kernel<T, D>, dim3(p.n_ctas), dim3(kAtThreads), at_smem_bytes<D>(), s, p) != cudaSuccess ||
       launch_pdl(attend_join_kernel<T, D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, p) != cudaSuccess)
     return SPEC_ERR_CUDA;
