@@ -75,8 +75,8 @@ struct AttendParams {
   int n_q_heads, n_heads, group;
   int tok_tile;      // positions of a row tile: 128 / group
   int n_ctas;
-  int64_t* off;      // [B + 1] where each sequence begins in the own-pages line
   int64_t* begin;    // [2][n_ctas + 1] where the parts begin in each line
+  int4* part_meta;   // [2][N * n_q_heads] RowItem of each row
   float* part_o;     // [2][N * n_q_heads][D]
   float2* part_ml;   // [2][N * n_q_heads]
   float* slab_o;     // [n_ctas][2][256][D]
@@ -112,6 +112,16 @@ __device__ __forceinline__ int64_t seq_head_weight(const AttendParams& p, const 
   return w;
 }
 
+// The rows of the blocks that see no key at all (fewer entries than new
+// positions, which the status word reports): the join finds no parts there.
+__device__ __noinline__ void no_tiles(const AttendParams& p, const SeqSpan& s) {
+  for (int i = 0; i < s.n; ++i) {
+    if (block_tiles(p, s, i / (2 * p.tok_tile)) > 0) continue;
+    for (int h = 0; h < p.n_q_heads; ++h)
+      p.part_meta[(static_cast<int64_t>(p.batch.N) + s.first + i) * p.n_q_heads + h] = make_int4(-1, 0, 0, 0);
+  }
+}
+
 struct PrefixLine {
   int positions, blocks, tiles;
   int64_t per_head, total;
@@ -129,8 +139,12 @@ __device__ __forceinline__ PrefixLine prefix_line(const AttendParams& p) {
 }
 
 // Part c of n of a line of weight W begins at W * c / n; tiles belong to the
-// part that their first unit of weight lies in.
-__device__ __forceinline__ int64_t part_begin(int64_t W, int c, int n) { return W * c / n; }
+// part that their first unit of weight lies in.  (The 64-bit division takes
+// some hundred clocks, before the first load of a CTA.)
+__device__ __forceinline__ int64_t part_begin(int64_t W, int c, int n) {
+  if (W < (1 << 24)) return static_cast<uint32_t>(W) * static_cast<uint32_t>(c) / static_cast<uint32_t>(n);  // n <= 160
+  return W * c / n;
+}
 __device__ __forceinline__ int tiles_before(int64_t x, int64_t off, int w, int tiles) {
   if (x <= off) return 0;
   const int64_t t = w == 2 ? (x - off + 1) >> 1 : x - off;
@@ -139,6 +153,9 @@ __device__ __forceinline__ int tiles_before(int64_t x, int64_t off, int w, int t
 
 // A part of an item, as the scheduler queues it.
 struct AtPart {
+  int64_t off;        // the item's place in its line
+  int tiles, w;       // all its key tiles, their weight
+  int last;           // for the part with the first tile: the last part that holds any
   int line;           // 0 prefix, 1 own pages, -1 no more
   int head, first;    // key head, first position
   int n0, n1;         // positions of the two row tiles (n1 = 0: one tile)
@@ -147,6 +164,16 @@ struct AtPart {
   int seq_first, seq_n;
   int seq;
 };
+
+// What the join needs of a row's item, written with the item's first tile:
+// x: the parts that hold its first and last tile, and the row's place in their
+// slabs (8 bits each), or -1: no tiles.  y: 2 * tiles + (weight 2 ? 1 : 0).
+// z, w: the item's place in its line.
+__device__ __forceinline__ int4 row_item(const AtPart& a, int part, int slab_row) {
+  return make_int4(part | a.last << 8 | slab_row << 16, 2 * a.tiles + (a.w == 2), static_cast<int>(a.off),
+                   static_cast<int>(a.off >> 32));
+}
+
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -255,29 +282,26 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 
   // ---- the own-pages line: its weight, and where this CTA's part begins ----
   const int own_cta = p.n_ctas - 1 - cta;  // mirrored, so that short lines meet on different CTAs
-  int64_t first_weight = 0;
   {
-    int64_t w = 0;
-    for (int b = threadIdx.x; b < p.batch.B; b += kAtThreads) {
-      const int64_t one = seq_head_weight(p, seq_span(p.batch, b)) * p.n_heads;
-      if (b == static_cast<int>(threadIdx.x)) first_weight = one;
-      w += one;
+    int64_t total = 0;
+    if (p.batch.B > kAtThreads) {  // several chunks: their sum first
+      int64_t w = 0;
+      for (int b = threadIdx.x; b < p.batch.B; b += kAtThreads) w += seq_head_weight(p, seq_span(p.batch, b)) * p.n_heads;
+      for (int x = 16; x; x >>= 1) w += __shfl_xor_sync(0xffffffffu, w, x);
+      if (lane == 0) sh.warp_sum[warp] = w;
+      __syncthreads();
+      for (int i = 0; i < kAtThreads / 32; ++i) total += sh.warp_sum[i];
+      __syncthreads();
     }
-    for (int x = 16; x; x >>= 1) w += __shfl_xor_sync(0xffffffffu, w, x);
-    if (lane == 0) sh.warp_sum[warp] = w;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int64_t t = 0;
-      for (int i = 0; i < kAtThreads / 32; ++i) t += sh.warp_sum[i];
-      sh.total = t;
-    }
-    __syncthreads();
-    const int64_t total = sh.total, lo = part_begin(total, own_cta, p.n_ctas);
     int64_t before = 0;  // weight of the chunks before this one
     for (int b0 = 0; b0 < p.batch.B; b0 += kAtThreads) {
       const int b = b0 + threadIdx.x;
       int64_t one = 0;
-      if (b < p.batch.B) one = b0 == 0 ? first_weight : seq_head_weight(p, seq_span(p.batch, b)) * p.n_heads;
+      if (b < p.batch.B) {
+        const SeqSpan s = seq_span(p.batch, b);
+        one = seq_head_weight(p, s) * p.n_heads;
+        if (cta == 0 && s.kv < s.n) no_tiles(p, s);
+      }
       int64_t inc = one;
       for (int x = 1; x < 32; x <<= 1) {
         const int64_t o = __shfl_up_sync(0xffffffffu, inc, x);
@@ -286,21 +310,20 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       if (lane == 31) sh.warp_sum[warp] = inc;
       __syncthreads();
       int64_t base = before;
-      for (int i = 0; i < warp; ++i) base += sh.warp_sum[i];
-      const int64_t off = base + inc - one;
-      if (b < p.batch.B) {
-        if (off <= lo && lo < off + one) {
-          sh.seq = b;
-          sh.off = off;
-        }
-        if (cta == 0) {
-          p.off[b] = off;
-          if (b == p.batch.B - 1) p.off[b + 1] = off + one;
-        }
+      for (int i = 0; i < kAtThreads / 32; ++i) {
+        const int64_t x = sh.warp_sum[i];
+        if (i < warp) base += x;
+        before += x;
       }
-      for (int i = 0; i < kAtThreads / 32; ++i) before += sh.warp_sum[i];
-      __syncthreads();
+      if (p.batch.B <= kAtThreads) total = before;
+      const int64_t off = base + inc - one, lo = part_begin(total, own_cta, p.n_ctas);
+      if (b < p.batch.B && off <= lo && lo < off + one) {
+        sh.seq = b;
+        sh.off = off;
+      }
+      if (b0 + kAtThreads < p.batch.B) __syncthreads();
     }
+    if (threadIdx.x == 0) sh.total = total;
   }
   tc_fence_before();
   __syncthreads();
@@ -408,10 +431,16 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
             for (int at = 0; at < s.n && ok; at += 2 * p.tok_tile) {
               const int rb = at / (2 * p.tok_tile);
               const int tiles = a.line == 0 ? pl.tiles : block_tiles(p, s, rb), w = block_weight(s.n, p.tok_tile, rb);
+              a.off = off;
+              a.tiles = tiles;
+              a.w = w;
               a.t0 = tiles_before(lo, off, w, tiles);
               a.t1 = tiles_before(hi, off, w, tiles);
               off += static_cast<int64_t>(tiles) * w;
               if (a.t0 >= a.t1) continue;
+              // the part that the item's last tile begins in
+              a.last = c;
+              if (a.t0 == 0 && a.t1 < tiles) a.last = static_cast<int>(((off - w + 1) * p.n_ctas - 1) / total);
               a.first = s.first + at;
               a.n0 = min(p.tok_tile, s.n - at);
               a.n1 = min(p.tok_tile, s.n - at - a.n0);
@@ -698,12 +727,15 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       // ---- the part's results ----
       float* dst_o;
       float2* dst_ml;
+      int4* dst_meta = nullptr;
+      const int slab_row = (two ? g * 128 : 0) + r;
       if (a.t0 == 0) {
         const int64_t row = (static_cast<int64_t>(a.line) * p.batch.N + tok) * p.n_q_heads + a.head * p.group + gq;
         dst_o = p.part_o + row * D;
         dst_ml = p.part_ml + row;
+        dst_meta = p.part_meta + row;
       } else {
-        const int64_t row = (static_cast<int64_t>(cta) * 2 + a.line) * 256 + (two ? g * 128 : 0) + r;
+        const int64_t row = (static_cast<int64_t>(cta) * 2 + a.line) * 256 + slab_row;
         dst_o = p.slab_o + row * D;
         dst_ml = p.slab_ml + row;
       }
@@ -759,7 +791,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
             }
           }
         }
-        if (mine_to_write && (two || g == 0)) *dst_ml = make_float2(m, l);
+        if (mine_to_write && (two || g == 0)) {
+          *dst_ml = make_float2(m, l);
+          if (a.t0 == 0) *dst_meta = row_item(a, a.line == 0 ? cta : own_cta, slab_row);
+        }
       }
       tc_fence_before();
       if (two) {
@@ -778,146 +813,90 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------------------
-// join: one warp per position and key head adds the parts of its rows (one per
-// query head: they share the items, so what finds the parts is done once)
+// join: one warp per row adds the row's parts.  Each line's first part says
+// where the others are, so a row whose items were not split takes one round of
+// loads.
 // ---------------------------------------------------------------------------
-// The parts that hold tiles of one item, from part c0 on: bit i of `parts` is
-// part c0 + i, `first` those that begin the item (their rows' own places).
-struct ItemParts {
-  int c0;
-  unsigned parts, first;
-  int tile_row;  // of the position's first row, in a slab
-  bool more;     // the item goes on after part c0 + 31
-};
-
-// An item of `tiles` tiles of weight w from `off` on, in a line of weight W.
-__device__ __forceinline__ ItemParts find_parts(const AttendParams& p, int line, int64_t W, int64_t off, int tiles,
-                                                int w, int pos, int c_from, int lane) {
-  ItemParts r;
-  r.tile_row = pos % p.tok_tile * p.group + (w == 2 ? pos / p.tok_tile * kAtTile : 0);
-  // part c begins at W * c / n, so `off` lies in part ((off + 1) n - 1) / W; one
-  // early for the rounding of fp32
-  r.c0 = c_from >= 0 ? c_from
-                     : max(0, static_cast<int>((static_cast<float>(off + 1) * p.n_ctas - 1.f) / static_cast<float>(W)) - 1);
-  const int64_t* begin = p.begin + line * (p.n_ctas + 1);
-  const int c = r.c0 + lane;
-  int t0 = 0, t1 = 0;
-  if (c < p.n_ctas) {
-    t0 = tiles_before(begin[c], off, w, tiles);
-    t1 = tiles_before(begin[c + 1], off, w, tiles);
-  }
-  r.parts = __ballot_sync(0xffffffffu, t0 < t1);
-  r.first = __ballot_sync(0xffffffffu, t0 == 0);
-  r.more = r.c0 + 32 < p.n_ctas && __shfl_sync(0xffffffffu, t1, 31) < tiles;
-  return r;
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p) {
   constexpr int kPer = D / 32;  // dims of a lane
   const int lane = threadIdx.x & 31;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int n = static_cast<int>(id / p.n_heads), head = static_cast<int>(id % p.n_heads);
+  const int64_t rows = static_cast<int64_t>(p.batch.N) * p.n_q_heads;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   grid_dep_launch();
   grid_dep_wait();
-  if (n >= p.batch.N) return;
-  const int b = find_seq(p.batch.q_indptr, p.batch.B, n, lane);
-  if (b < 0) return;
-  const SeqSpan s = seq_span(p.batch, b);
-  const int64_t begin = p.off[b], weight = p.off[b + 1] - begin, total = p.off[p.batch.B];
-  if (n < s.first || n >= s.first + s.n) return;
+  if (row >= rows) return;
+  const int n = static_cast<int>(row / p.n_q_heads), hq = static_cast<int>(row - static_cast<int64_t>(n) * p.n_q_heads);
 
-  // the position's item in each line
-  int64_t off[2] = {0, 0}, W[2] = {1, 1};
-  int tiles[2] = {0, 0}, w[2] = {1, 1}, pos[2] = {0, 0};
-  if (p.prefix_len > 0) {
-    const PrefixLine pl = prefix_line(p);
-    const int rb = n / (2 * p.tok_tile);
-    off[0] = head * pl.per_head + rb * 2LL * pl.tiles;
-    W[0] = pl.total;
-    tiles[0] = pl.tiles;
-    w[0] = block_weight(pl.positions, p.tok_tile, rb);
-    pos[0] = n - rb * 2 * p.tok_tile;
-  }
-  if (weight > 0) {
-    const int rb = (n - s.first) / (2 * p.tok_tile);
-    off[1] = begin;
-    int64_t own = 0;  // one head's weight, and the blocks before this one
-    for (int i = 0; i * 2 * p.tok_tile < s.n; ++i) {
-      const int64_t x = static_cast<int64_t>(block_tiles(p, s, i)) * block_weight(s.n, p.tok_tile, i);
-      own += x;
-      if (i < rb) off[1] += x;
-    }
-    off[1] += head * own;
-    W[1] = total;
-    tiles[1] = block_tiles(p, s, rb);
-    w[1] = block_weight(s.n, p.tok_tile, rb);
-    pos[1] = n - s.first - rb * 2 * p.tok_tile;
-  }
-  ItemParts ip[2];
+  auto load = [&](const float* src, float (&x)[kPer]) {
+    if (kPer == 4)
+      *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+    else
+      *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+  };
+  float x[2][kPer];
+  float2 ml[2];
+  int4 item[2];
 #pragma unroll
   for (int line = 0; line < 2; ++line) {
-    ip[line].parts = 0u;
-    if (tiles[line] > 0) ip[line] = find_parts(p, line, W[line], off[line], tiles[line], w[line], pos[line], -1, lane);
+    item[line] = make_int4(-1, 0, 0, 0);
+    if (line == 0 && p.prefix_len == 0) continue;
+    item[line] = p.part_meta[line * rows + row];
+    ml[line] = p.part_ml[line * rows + row];
+    load(p.part_o + (line * rows + row) * D + lane * kPer, x[line]);
   }
+  if (n >= new_positions(p.batch)) return;  // padding
 
-  for (int gq = 0; gq < p.group; ++gq) {
-    const int hq = head * p.group + gq;
-    float o[kPer] = {}, m = -INFINITY, l = 0.f;
+  float o[kPer] = {}, m = -INFINITY, l = 0.f;
+  auto add = [&](const float2& a, const float (&v)[kPer]) {
+    if (a.x == -INFINITY) return;  // nothing seen: its O is not looked at
+    const float mm = fmaxf(m, a.x);
+    const float fo = m == -INFINITY ? 0.f : ex2(m - mm), fx = ex2(a.x - mm);
+    m = mm;
+    l = l * fo + a.y * fx;
 #pragma unroll
-    for (int line = 0; line < 2; ++line) {
-      if (tiles[line] == 0) continue;
-      ItemParts at = ip[line];
-      const int64_t own_row = (static_cast<int64_t>(line) * p.batch.N + n) * p.n_q_heads + hq;
-      while (true) {
-        unsigned left = at.parts;
-        while (left != 0u) {
-          // up to four parts' loads in flight, added in ascending order
-          float x[4][kPer];
-          float2 ml[4];
+    for (int i = 0; i < kPer; ++i) o[i] = o[i] * fo + v[i] * fx;
+  };
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            ml[k] = make_float2(-INFINITY, 0.f);
-            if (left == 0u) continue;
-            const int i = __ffs(left) - 1;
-            left &= left - 1;
-            const bool first = (at.first >> i) & 1;
-            const int c = at.c0 + i;
-            const int64_t row = first ? own_row
-                                      : (static_cast<int64_t>(line == 0 ? c : p.n_ctas - 1 - c) * 2 + line) * 256 +
-                                            at.tile_row + gq;
-            ml[k] = (first ? p.part_ml : p.slab_ml)[row];
-            const float* src = (first ? p.part_o : p.slab_o) + row * D + lane * kPer;
-            if (kPer == 4)
-              *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(src);
-            else
-              *reinterpret_cast<float2*>(x[k]) = *reinterpret_cast<const float2*>(src);
-          }
+  for (int line = 0; line < 2; ++line) {
+    if (item[line].x < 0) continue;
+    add(ml[line], x[line]);
+    const int first = item[line].x & 255, last = min(item[line].x >> 8 & 255, p.n_ctas - 1);
+    const int slab_row = item[line].x >> 16 & 255, tiles = item[line].y >> 1, w = 1 + (item[line].y & 1);
+    const int64_t off = static_cast<int64_t>(item[line].w) << 32 | static_cast<uint32_t>(item[line].z);
+    const int64_t* begin = p.begin + line * (p.n_ctas + 1);
+    for (int c0 = first + 1; c0 <= last; c0 += 32) {
+      // lane i: whether part c0 + i holds a tile's beginning
+      const int c = c0 + lane;
+      const bool has = c <= last && tiles_before(begin[c], off, w, tiles) < tiles_before(begin[c + 1], off, w, tiles);
+      unsigned parts = __ballot_sync(0xffffffffu, has);
+      while (parts != 0u) {
+        // up to four parts' loads in flight, added in ascending order
+        float v[4][kPer];
+        float2 a[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (ml[k].x == -INFINITY) continue;  // nothing seen: its O is not looked at
-            const float mm = fmaxf(m, ml[k].x);
-            const float fo = m == -INFINITY ? 0.f : ex2(m - mm), fx = ex2(ml[k].x - mm);
-            m = mm;
-            l = l * fo + ml[k].y * fx;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) o[i] = o[i] * fo + x[k][i] * fx;
-          }
+        for (int k = 0; k < 4; ++k) {
+          a[k] = make_float2(-INFINITY, 0.f);
+          if (parts == 0u) continue;
+          const int part = c0 + __ffs(parts) - 1;
+          parts &= parts - 1;
+          const int64_t at = (static_cast<int64_t>(line == 0 ? part : p.n_ctas - 1 - part) * 2 + line) * 256 + slab_row;
+          a[k] = p.slab_ml[at];
+          load(p.slab_o + at * D + lane * kPer, v[k]);
         }
-        if (!at.more) break;
-        at = find_parts(p, line, W[line], off[line], tiles[line], w[line], pos[line], at.c0 + 32, lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) add(a[k], v[k]);
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t* dst = p.out + n * p.o_ps + hq * p.o_hs + lane * kPer;
-    if (kPer == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(Pack16<T>::pack(o[0] * inv, o[1] * inv),
-                                                  Pack16<T>::pack(o[kPer - 2] * inv, o[kPer - 1] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(dst) = Pack16<T>::pack(o[0] * inv, o[1] * inv);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[static_cast<int64_t>(n) * p.n_q_heads + hq] = l > 0.f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
   }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint16_t* dst = p.out + n * p.o_ps + hq * p.o_hs + lane * kPer;
+  if (kPer == 4)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(Pack16<T>::pack(o[0] * inv, o[1] * inv), Pack16<T>::pack(o[kPer - 2] * inv, o[kPer - 1] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = Pack16<T>::pack(o[0] * inv, o[1] * inv);
+  if (lane == 0 && p.lse != nullptr) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
 }
 
 }  // namespace specv

@@ -16,7 +16,7 @@ using namespace specv;
 namespace {
 
 struct AttnLayout {
-  size_t header, off, begin, part_o, part_ml, slab_o, slab_ml, total;
+  size_t header, begin, part_meta, part_o, part_ml, slab_o, slab_ml, total;
 };
 
 // The parts of the rows (one place per row and line) and of the CTAs (one slab
@@ -31,8 +31,8 @@ AttnLayout attn_layout(int B, int N, int n_q_heads, int D) {
     return at;
   };
   L.header = take(sizeof(WsHeader));
-  L.off = take((static_cast<size_t>(B) + 1) * sizeof(int64_t));
   L.begin = take(2 * (size_t(kAtMaxCtas) + 1) * sizeof(int64_t));
+  L.part_meta = take(rows * sizeof(int4));
   L.part_o = take(rows * D * sizeof(float));
   L.part_ml = take(rows * sizeof(float2));
   L.slab_o = take(slab_rows * D * sizeof(float));
@@ -182,7 +182,7 @@ bool encode_queries(CUtensorMap* m, const void* q, const spec_kv_cache* c, int N
 
 template <typename T, int D>
 int launch_attend(const AttendParams& p, cudaStream_t s) {
-  const int64_t rows = static_cast<int64_t>(p.batch.N) * p.n_heads;
+  const int64_t rows = static_cast<int64_t>(p.batch.N) * p.n_q_heads;
   if (launch_pdl(attend_kernel<T, D>, dim3(p.n_ctas), dim3(kAtThreads), at_smem_bytes<D>(), s, p) != cudaSuccess ||
       launch_pdl(attend_join_kernel<T, D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, p) != cudaSuccess)
     return SPEC_ERR_CUDA;
@@ -296,8 +296,8 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
   p.n_ctas = sms < kAtMaxCtas ? sms : kAtMaxCtas;
   const AttnLayout L = attn_layout(B, N, n_q_heads, cache->head_dim);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.off = reinterpret_cast<int64_t*>(ws + L.off);
   p.begin = reinterpret_cast<int64_t*>(ws + L.begin);
+  p.part_meta = reinterpret_cast<int4*>(ws + L.part_meta);
   p.part_o = reinterpret_cast<float*>(ws + L.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
   p.slab_o = reinterpret_cast<float*>(ws + L.slab_o);
