@@ -33,7 +33,8 @@
 //   warp 9          issues the products: S = Q K^T (both operands
 //                   from shared memory) and O += P V (P from TMEM, where the
 //                   softmax group wrote it over S; V's rows are K).
-//   warps 10, 11    only fill their warpgroup.
+//   warp 10         loads the queries of each part (TMA).
+//   warp 11         only fills its warpgroup.
 // TMEM: S0 S1 (128 columns each) and O0 O1 (D columns each).
 //
 // The reference m of a row rises only when a tile's maximum passes it by more
@@ -58,6 +59,7 @@ constexpr int kAtSoftmaxRegs = 216, kAtOtherRegs = 72;
 constexpr int kAtRingBytes = 160 * 1024;
 constexpr int kAtMaxCtas = 160;     // slabs in the workspace
 constexpr int kAtQueue = 4;         // parts queued ahead
+constexpr int kAtFixed = 3;         // a part's fixed cost in key tiles
 constexpr float kAtRise = 8.f;      // log2 of the largest weight
 
 struct AttendParams {
@@ -99,16 +101,22 @@ __device__ __forceinline__ int block_tiles(const AttendParams& p, const SeqSpan&
   return last <= 0 ? 0 : static_cast<int>((last + kAtTile - 1) / kAtTile);
 }
 
-// Row tiles of the block: its weight per key tile.
+// Row tiles of the block: its weight per key tile.  A part's fixed cost
+// (queries, first scores, results) measured about three tiles', so an item
+// weighs three tiles more than it has, all on its first tile.
 __device__ __forceinline__ int block_weight(int positions, int tok_tile, int rb) {
   return positions - rb * 2 * tok_tile > tok_tile ? 2 : 1;
+}
+
+__device__ __forceinline__ int64_t item_weight(int tiles, int w) {
+  return tiles == 0 ? 0 : static_cast<int64_t>(tiles + kAtFixed) * w;
 }
 
 // Weight of one key head's items of a sequence.
 __device__ __forceinline__ int64_t seq_head_weight(const AttendParams& p, const SeqSpan& s) {
   int64_t w = 0;
   for (int rb = 0; rb * 2 * p.tok_tile < s.n; ++rb)
-    w += static_cast<int64_t>(block_tiles(p, s, rb)) * block_weight(s.n, p.tok_tile, rb);
+    w += item_weight(block_tiles(p, s, rb), block_weight(s.n, p.tok_tile, rb));
   return w;
 }
 
@@ -131,9 +139,9 @@ __device__ __forceinline__ PrefixLine prefix_line(const AttendParams& p) {
   L.positions = new_positions(p.batch);
   L.tiles = (p.prefix_len + kAtTile - 1) / kAtTile;
   L.blocks = (L.positions + 2 * p.tok_tile - 1) / (2 * p.tok_tile);
-  L.per_head = L.blocks > 0
-                   ? static_cast<int64_t>(L.tiles) * (2 * (L.blocks - 1) + block_weight(L.positions, p.tok_tile, L.blocks - 1))
-                   : 0;
+  L.per_head = L.blocks > 0 ? (L.blocks - 1) * item_weight(L.tiles, 2) +
+                                  item_weight(L.tiles, block_weight(L.positions, p.tok_tile, L.blocks - 1))
+                            : 0;
   L.total = L.per_head * p.n_heads;
   return L;
 }
@@ -145,10 +153,11 @@ __device__ __forceinline__ int64_t part_begin(int64_t W, int c, int n) {
   if (W < (1 << 24)) return static_cast<uint32_t>(W) * static_cast<uint32_t>(c) / static_cast<uint32_t>(n);  // n <= 160
   return W * c / n;
 }
+// Tile t of an item begins at its `off` (t = 0) or at off + (t + kAtFixed) w.
 __device__ __forceinline__ int tiles_before(int64_t x, int64_t off, int w, int tiles) {
-  if (x <= off) return 0;
-  const int64_t t = w == 2 ? (x - off + 1) >> 1 : x - off;
-  return t < tiles ? static_cast<int>(t) : tiles;
+  if (x <= off || tiles == 0) return 0;
+  const int64_t t = (w == 2 ? (x - off + 1) >> 1 : x - off) - kAtFixed;
+  return t < 1 ? 1 : t < tiles ? static_cast<int>(t) : tiles;
 }
 
 // A part of an item, as the scheduler queues it.
@@ -262,7 +271,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
     }
     for (int i = 0; i < kAtQueue; ++i) {
       mbar_init(&sh.part_full[i], 1);
-      mbar_init(&sh.part_empty[i], 9);  // eight softmax warps and the issuer
+      mbar_init(&sh.part_empty[i], 10);  // eight softmax warps, the issuer, the queries' warp
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&sh.q_full[g], 1);
@@ -358,24 +367,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         ++loaded;
         if (++slot == kSlots) slot = 0;
       };
-      // the queries of a part: row tile g of two, or the one tile for each group
-      // that has key tiles
-      uint32_t q_loads[2] = {0, 0};
-      auto load_queries = [&](const AtPart& a) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (a.n1 == 0 && g == 1 && a.t1 - a.t0 < 2) continue;
-          if (q_loads[g] > 0) ok = ok && mbar_wait(&sh.q_empty[g], (q_loads[g] & 1) ^ 1, status, kWaitLimitCycles);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) return;
-          if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[g], kHalves * 128u * p.group * p.tok_tile);
-          __syncwarp();
-          if (lane < kHalves)
-            tma_load_3d(smem_u32(qbuf) + g * kTileBytes + lane * kHalfBytes, &p.tmQ, lane * 64, a.head * p.group,
-                        a.first + (a.n1 > 0 && g == 1 ? a.n0 : 0), &sh.q_full[g]);
-          ++q_loads[g];
-        }
-      };
       auto page_of = [&](const AtPart& a, int t) {
         const uint32_t key = static_cast<uint32_t>(t) * kAtTile + my_box * p.box_rows;
         if (!loads || t >= a.t1 || key >= static_cast<uint32_t>(a.len)) return p.n_pages;  // the copy fills zeros
@@ -436,7 +427,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
               a.w = w;
               a.t0 = tiles_before(lo, off, w, tiles);
               a.t1 = tiles_before(hi, off, w, tiles);
-              off += static_cast<int64_t>(tiles) * w;
+              off += item_weight(tiles, w);
               if (a.t0 >= a.t1) continue;
               // the part that the item's last tile begins in
               a.last = c;
@@ -460,8 +451,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
               for (int kt = a.t0; kt < a.t1 + lead && ok; ++kt) {
                 const int vt = kt - lead, next = page_of(a, kt + 1);
                 if (kt < a.t1) load_tile(&p.tmK, a.head, page, kt * kAtTile);
-                if (kt == a.t0 + lead && ok) load_queries(a);  // after the first keys: the buffers may still be in use
-              if (vt >= a.t0 && ok) load_tile(&p.tmV, a.head, lead ? vpage : page, vt * kAtTile);
+                if (vt >= a.t0 && ok) load_tile(&p.tmV, a.head, lead ? vpage : page, vt * kAtTile);
                 vpage = page;
                 page = next;
               }
@@ -476,9 +466,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           mbar_arrive(&sh.part_full[q]);
         }
       }
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-        if (q_loads[g] > 0) mbar_wait(&sh.q_full[g], (q_loads[g] & 1) ^ 1, status, kWaitLimitCycles);
       // the copies of the last tiles land before the CTA exits
 #pragma unroll 1
       for (uint32_t i = loaded > kSlots ? loaded - kSlots : 0; i < loaded; ++i)
@@ -576,6 +563,39 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       if (elect_one()) tc_commit(&sh.done);
       __syncwarp();
       mbar_wait(&sh.done, 0, status, kWaitLimitCycles);
+    } else if (warp == 10) {
+      // ---------------- queries (their own warp: the buffers come free late, and keys must not wait) ----------------
+      uint32_t loads[2] = {0, 0};
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, status, kWaitLimitCycles));
+        return ok;
+      };
+#pragma unroll 1
+      for (int n = 0; ok; ++n) {
+        const int q = n % kAtQueue;
+        if (!wait(&sh.part_full[q], (n / kAtQueue) & 1)) break;
+        const int line = sh.parts[q].line, tiles = sh.parts[q].t1 - sh.parts[q].t0, head = sh.parts[q].head,
+                  first = sh.parts[q].first, n0 = sh.parts[q].n0, n1 = sh.parts[q].n1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.part_empty[q]);
+        if (line < 0) break;
+        // row tile g of two, or the one tile for each group that has key tiles
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (n1 == 0 && g == 1 && tiles < 2) continue;
+          if (loads[g] > 0 && !wait(&sh.q_empty[g], (loads[g] & 1) ^ 1)) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[g], kHalves * 128u * p.group * p.tok_tile);
+          __syncwarp();
+          if (lane < kHalves)
+            tma_load_3d(smem_u32(qbuf) + g * kTileBytes + lane * kHalfBytes, &p.tmQ, lane * 64, head * p.group,
+                        first + (n1 > 0 && g == 1 ? n0 : 0), &sh.q_full[g]);
+          ++loads[g];
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g)  // the last copies land before the CTA exits
+        if (loads[g] > 0) mbar_wait(&sh.q_full[g], (loads[g] & 1) ^ 1, status, kWaitLimitCycles);
     }
   } else {
     regs_up<kAtSoftmaxRegs>();
