@@ -103,20 +103,25 @@ __device__ __forceinline__ int block_tiles(const AttendParams& p, const SeqSpan&
 
 // Row tiles of the block: its weight per key tile.  A part's fixed cost
 // (queries, first scores, results) measured about three tiles', so an item
-// weighs three tiles more than it has, all on its first tile.
+// weighs three tiles more than it has, all on its first tile -- where the CTAs
+// have several tiles each (decode_b64: 84 us with it, 87 without); where they
+// have few, the tiles alone are dealt out, which uses more CTAs (candidates_d64:
+// 28 us against 31.5).
 __device__ __forceinline__ int block_weight(int positions, int tok_tile, int rb) {
   return positions - rb * 2 * tok_tile > tok_tile ? 2 : 1;
 }
 
-__device__ __forceinline__ int64_t item_weight(int tiles, int w) {
-  return tiles == 0 ? 0 : static_cast<int64_t>(tiles + kAtFixed) * w;
+__device__ __forceinline__ int64_t item_weight(int tiles, int w, int fixed) {
+  return tiles == 0 ? 0 : static_cast<int64_t>(tiles + fixed) * w;
 }
+// The fixed cost that counts in a line whose tiles alone weigh W0.
+__device__ __forceinline__ int line_fixed(int64_t W0, int n_ctas) { return W0 < 6LL * n_ctas ? 0 : kAtFixed; }
 
 // Weight of one key head's items of a sequence.
-__device__ __forceinline__ int64_t seq_head_weight(const AttendParams& p, const SeqSpan& s) {
+__device__ __forceinline__ int64_t seq_head_weight(const AttendParams& p, const SeqSpan& s, int fixed) {
   int64_t w = 0;
   for (int rb = 0; rb * 2 * p.tok_tile < s.n; ++rb)
-    w += item_weight(block_tiles(p, s, rb), block_weight(s.n, p.tok_tile, rb));
+    w += item_weight(block_tiles(p, s, rb), block_weight(s.n, p.tok_tile, rb), fixed);
   return w;
 }
 
@@ -131,7 +136,7 @@ __device__ __noinline__ void no_tiles(const AttendParams& p, const SeqSpan& s) {
 }
 
 struct PrefixLine {
-  int positions, blocks, tiles;
+  int positions, blocks, tiles, fixed;
   int64_t per_head, total;
 };
 __device__ __forceinline__ PrefixLine prefix_line(const AttendParams& p) {
@@ -139,9 +144,9 @@ __device__ __forceinline__ PrefixLine prefix_line(const AttendParams& p) {
   L.positions = new_positions(p.batch);
   L.tiles = (p.prefix_len + kAtTile - 1) / kAtTile;
   L.blocks = (L.positions + 2 * p.tok_tile - 1) / (2 * p.tok_tile);
-  L.per_head = L.blocks > 0 ? (L.blocks - 1) * item_weight(L.tiles, 2) +
-                                  item_weight(L.tiles, block_weight(L.positions, p.tok_tile, L.blocks - 1))
-                            : 0;
+  const int row_tiles = L.blocks > 0 ? 2 * (L.blocks - 1) + block_weight(L.positions, p.tok_tile, L.blocks - 1) : 0;
+  L.fixed = line_fixed(static_cast<int64_t>(L.tiles) * row_tiles * p.n_heads, p.n_ctas);
+  L.per_head = item_weight(L.tiles, row_tiles, L.fixed);
   L.total = L.per_head * p.n_heads;
   return L;
 }
@@ -153,10 +158,10 @@ __device__ __forceinline__ int64_t part_begin(int64_t W, int c, int n) {
   if (W < (1 << 24)) return static_cast<uint32_t>(W) * static_cast<uint32_t>(c) / static_cast<uint32_t>(n);  // n <= 160
   return W * c / n;
 }
-// Tile t of an item begins at its `off` (t = 0) or at off + (t + kAtFixed) w.
-__device__ __forceinline__ int tiles_before(int64_t x, int64_t off, int w, int tiles) {
+// Tile t of an item begins at its `off` (t = 0) or at off + (t + fixed) w.
+__device__ __forceinline__ int tiles_before(int64_t x, int64_t off, int w, int fixed, int tiles) {
   if (x <= off || tiles == 0) return 0;
-  const int64_t t = (w == 2 ? (x - off + 1) >> 1 : x - off) - kAtFixed;
+  const int64_t t = (w == 2 ? (x - off + 1) >> 1 : x - off) - fixed;
   return t < 1 ? 1 : t < tiles ? static_cast<int>(t) : tiles;
 }
 
@@ -164,6 +169,7 @@ __device__ __forceinline__ int tiles_before(int64_t x, int64_t off, int w, int t
 struct AtPart {
   int64_t off;        // the item's place in its line
   int tiles, w;       // all its key tiles, their weight
+  int fixed;          // the fixed cost that counts in the line
   int last;           // for the part with the first tile: the last part that holds any
   int line;           // 0 prefix, 1 own pages, -1 no more
   int head, first;    // key head, first position
@@ -176,10 +182,10 @@ struct AtPart {
 
 // What the join needs of a row's item, written with the item's first tile:
 // x: the parts that hold its first and last tile, and the row's place in their
-// slabs (8 bits each), or -1: no tiles.  y: 2 * tiles + (weight 2 ? 1 : 0).
+// slabs (8 bits each), or -1: no tiles.  y: 8 * tiles + 2 * fixed + weight - 1.
 // z, w: the item's place in its line.
 __device__ __forceinline__ int4 row_item(const AtPart& a, int part, int slab_row) {
-  return make_int4(part | a.last << 8 | slab_row << 16, 2 * a.tiles + (a.w == 2), static_cast<int>(a.off),
+  return make_int4(part | a.last << 8 | slab_row << 16, 8 * a.tiles + 2 * a.fixed + a.w - 1, static_cast<int>(a.off),
                    static_cast<int>(a.off >> 32));
 }
 
@@ -235,8 +241,8 @@ struct AtShared {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], meet[2], done;
   float2 xch[2][kAtTile];  // the groups' (m, l)
   AtPart parts[kAtQueue];
-  int64_t warp_sum[kAtThreads / 32], total, off;
-  int seq;
+  int64_t warp_sum[kAtThreads / 32], warp_sum1[kAtThreads / 32], total, off;
+  int seq, fixed;
   uint32_t tmem;
 };
 template <int D>
@@ -292,47 +298,85 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   // ---- the own-pages line: its weight, and where this CTA's part begins ----
   const int own_cta = p.n_ctas - 1 - cta;  // mirrored, so that short lines meet on different CTAs
   {
-    int64_t total = 0;
-    if (p.batch.B > kAtThreads) {  // several chunks: their sum first
-      int64_t w = 0;
-      for (int b = threadIdx.x; b < p.batch.B; b += kAtThreads) w += seq_head_weight(p, seq_span(p.batch, b)) * p.n_heads;
-      for (int x = 16; x; x >>= 1) w += __shfl_xor_sync(0xffffffffu, w, x);
-      if (lane == 0) sh.warp_sum[warp] = w;
+    // the weight of the tiles alone and of an item's fixed tile go side by side
+    // until the first sum says which fixed cost counts
+    int64_t total = 0, total1 = 0;
+    if (p.batch.B > kAtThreads) {  // several chunks: their sums first
+      int64_t w = 0, w1 = 0;
+      for (int b = threadIdx.x; b < p.batch.B; b += kAtThreads) {
+        const SeqSpan s = seq_span(p.batch, b);
+        const int64_t x = seq_head_weight(p, s, 0);
+        w += x * p.n_heads;
+        w1 += (seq_head_weight(p, s, 1) - x) * p.n_heads;
+      }
+      for (int x = 16; x; x >>= 1) {
+        w += __shfl_xor_sync(0xffffffffu, w, x);
+        w1 += __shfl_xor_sync(0xffffffffu, w1, x);
+      }
+      if (lane == 0) {
+        sh.warp_sum[warp] = w;
+        sh.warp_sum1[warp] = w1;
+      }
       __syncthreads();
-      for (int i = 0; i < kAtThreads / 32; ++i) total += sh.warp_sum[i];
+      for (int i = 0; i < kAtThreads / 32; ++i) {
+        total += sh.warp_sum[i];
+        total1 += sh.warp_sum1[i];
+      }
       __syncthreads();
     }
-    int64_t before = 0;  // weight of the chunks before this one
+    int64_t before = 0, before1 = 0;  // of the chunks before this one
+    int fixed = 0;
     for (int b0 = 0; b0 < p.batch.B; b0 += kAtThreads) {
       const int b = b0 + threadIdx.x;
-      int64_t one = 0;
+      int64_t one = 0, one1 = 0;
       if (b < p.batch.B) {
         const SeqSpan s = seq_span(p.batch, b);
-        one = seq_head_weight(p, s) * p.n_heads;
+        const int64_t x = seq_head_weight(p, s, 0);
+        one = x * p.n_heads;
+        one1 = (seq_head_weight(p, s, 1) - x) * p.n_heads;
         if (cta == 0 && s.kv < s.n) no_tiles(p, s);
       }
-      int64_t inc = one;
+      int64_t inc = one, inc1 = one1;
       for (int x = 1; x < 32; x <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, inc, x);
-        if (lane >= x) inc += o;
+        const int64_t o = __shfl_up_sync(0xffffffffu, inc, x), o1 = __shfl_up_sync(0xffffffffu, inc1, x);
+        if (lane >= x) {
+          inc += o;
+          inc1 += o1;
+        }
       }
-      if (lane == 31) sh.warp_sum[warp] = inc;
+      if (lane == 31) {
+        sh.warp_sum[warp] = inc;
+        sh.warp_sum1[warp] = inc1;
+      }
       __syncthreads();
-      int64_t base = before;
+      int64_t base = before, base1 = before1;
       for (int i = 0; i < kAtThreads / 32; ++i) {
-        const int64_t x = sh.warp_sum[i];
-        if (i < warp) base += x;
+        const int64_t x = sh.warp_sum[i], x1 = sh.warp_sum1[i];
+        if (i < warp) {
+          base += x;
+          base1 += x1;
+        }
         before += x;
+        before1 += x1;
       }
-      if (p.batch.B <= kAtThreads) total = before;
-      const int64_t off = base + inc - one, lo = part_begin(total, own_cta, p.n_ctas);
-      if (b < p.batch.B && off <= lo && lo < off + one) {
+      if (p.batch.B <= kAtThreads) {
+        total = before;
+        total1 = before1;
+      }
+      fixed = line_fixed(total, p.n_ctas);
+      const int64_t mine = one + fixed * one1, off = base + inc + fixed * (base1 + inc1) - mine;
+      const int64_t lo = part_begin(total + fixed * total1, own_cta, p.n_ctas);
+      if (b < p.batch.B && off <= lo && lo < off + mine) {
         sh.seq = b;
         sh.off = off;
       }
       if (b0 + kAtThreads < p.batch.B) __syncthreads();
     }
-    if (threadIdx.x == 0) sh.total = total;
+    total += fixed * total1;
+    if (threadIdx.x == 0) {
+      sh.total = total;
+      sh.fixed = fixed;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -391,6 +435,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         // the prefix's line is that of one sequence of all new positions
         AtPart a;
         a.line = (turn ^ cta) & 1;
+        a.fixed = a.line == 0 ? pl.fixed : sh.fixed;
         const int64_t total = a.line == 0 ? pl.total : sh.total;
         const int c = a.line == 0 ? cta : own_cta;
         const int64_t lo = part_begin(total, c, p.n_ctas), hi = part_begin(total, c + 1, p.n_ctas);
@@ -407,7 +452,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           int64_t hw = pl.per_head;
           if (a.line == 1) {
             s = seq_span(p.batch, a.seq);
-            hw = seq_head_weight(p, s);
+            hw = seq_head_weight(p, s, a.fixed);
           }
           a.len = a.line == 0 ? p.prefix_len : static_cast<int>(s.kv);
           a.old = a.line == 0 ? a.len : a.len - s.n;
@@ -425,9 +470,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
               a.off = off;
               a.tiles = tiles;
               a.w = w;
-              a.t0 = tiles_before(lo, off, w, tiles);
-              a.t1 = tiles_before(hi, off, w, tiles);
-              off += item_weight(tiles, w);
+              a.t0 = tiles_before(lo, off, w, a.fixed, tiles);
+              a.t1 = tiles_before(hi, off, w, a.fixed, tiles);
+              off += item_weight(tiles, w, a.fixed);
               if (a.t0 >= a.t1) continue;
               // the part that the item's last tile begins in
               a.last = c;
@@ -882,13 +927,15 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     if (item[line].x < 0) continue;
     add(ml[line], x[line]);
     const int first = item[line].x & 255, last = min(item[line].x >> 8 & 255, p.n_ctas - 1);
-    const int slab_row = item[line].x >> 16 & 255, tiles = item[line].y >> 1, w = 1 + (item[line].y & 1);
+    const int slab_row = item[line].x >> 16 & 255, tiles = item[line].y >> 3, w = 1 + (item[line].y & 1),
+              fixed = item[line].y >> 1 & 3;
     const int64_t off = static_cast<int64_t>(item[line].w) << 32 | static_cast<uint32_t>(item[line].z);
     const int64_t* begin = p.begin + line * (p.n_ctas + 1);
     for (int c0 = first + 1; c0 <= last; c0 += 32) {
       // lane i: whether part c0 + i holds a tile's beginning
       const int c = c0 + lane;
-      const bool has = c <= last && tiles_before(begin[c], off, w, tiles) < tiles_before(begin[c + 1], off, w, tiles);
+      const bool has = c <= last && tiles_before(begin[c], off, w, fixed, tiles) <
+                                        tiles_before(begin[c + 1], off, w, fixed, tiles);
       unsigned parts = __ballot_sync(0xffffffffu, has);
       while (parts != 0u) {
         // up to four parts' loads in flight, added in ascending order
