@@ -58,6 +58,7 @@ constexpr int kAtThreads = 384;     // three warpgroups
 constexpr int kAtSoftmaxRegs = 216, kAtOtherRegs = 72;
 constexpr int kAtRingBytes = 160 * 1024;
 constexpr int kAtMaxCtas = 160;     // slabs in the workspace
+constexpr int kScanWarps = 8;       // the softmax warps add up the sequences' work
 constexpr int kAtQueue = 4;         // parts queued ahead
 constexpr int kAtFixed = 3;         // a part's fixed cost in key tiles
 constexpr float kAtRise = 8.f;      // log2 of the largest weight
@@ -224,6 +225,10 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+__device__ __forceinline__ void named_sync(int id, int nthreads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
 // 32-byte global store (eight fp32; the address 32-byte aligned)
 __device__ __forceinline__ void st_global_f8(float* q, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(q), "f"(v[0]), "f"(v[1]), "f"(v[2]),
@@ -238,7 +243,7 @@ __device__ __forceinline__ void st_global_f8(float* q, const float* v) {
 template <int kSlots>
 struct AtShared {
   uint64_t kv_full[kSlots], kv_empty[kSlots], part_full[kAtQueue], part_empty[kAtQueue];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], meet[2], done;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], meet[2], done, scanned;
   float2 xch[2][kAtTile];  // the groups' (m, l)
   AtPart parts[kAtQueue];
   int64_t warp_sum[kAtThreads / 32], warp_sum1[kAtThreads / 32], total, off;
@@ -288,100 +293,18 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       mbar_init(&sh.meet[g], 8);
     }
     mbar_init(&sh.done, 1);
+    mbar_init(&sh.scanned, kScanWarps);
     fence_mbar_init();
     sh.seq = p.batch.B;
     sh.off = 0;
   }
   if (warp == 9) tmem_alloc(&sh.tmem, 512);
-  grid_dep_wait();
-
-  // ---- the own-pages line: its weight, and where this CTA's part begins ----
-  const int own_cta = p.n_ctas - 1 - cta;  // mirrored, so that short lines meet on different CTAs
-  {
-    // the weight of the tiles alone and of an item's fixed tile go side by side
-    // until the first sum says which fixed cost counts
-    int64_t total = 0, total1 = 0;
-    if (p.batch.B > kAtThreads) {  // several chunks: their sums first
-      int64_t w = 0, w1 = 0;
-      for (int b = threadIdx.x; b < p.batch.B; b += kAtThreads) {
-        const SeqSpan s = seq_span(p.batch, b);
-        const int64_t x = seq_head_weight(p, s, 0);
-        w += x * p.n_heads;
-        w1 += (seq_head_weight(p, s, 1) - x) * p.n_heads;
-      }
-      for (int x = 16; x; x >>= 1) {
-        w += __shfl_xor_sync(0xffffffffu, w, x);
-        w1 += __shfl_xor_sync(0xffffffffu, w1, x);
-      }
-      if (lane == 0) {
-        sh.warp_sum[warp] = w;
-        sh.warp_sum1[warp] = w1;
-      }
-      __syncthreads();
-      for (int i = 0; i < kAtThreads / 32; ++i) {
-        total += sh.warp_sum[i];
-        total1 += sh.warp_sum1[i];
-      }
-      __syncthreads();
-    }
-    int64_t before = 0, before1 = 0;  // of the chunks before this one
-    int fixed = 0;
-    for (int b0 = 0; b0 < p.batch.B; b0 += kAtThreads) {
-      const int b = b0 + threadIdx.x;
-      int64_t one = 0, one1 = 0;
-      if (b < p.batch.B) {
-        const SeqSpan s = seq_span(p.batch, b);
-        const int64_t x = seq_head_weight(p, s, 0);
-        one = x * p.n_heads;
-        one1 = (seq_head_weight(p, s, 1) - x) * p.n_heads;
-        if (cta == 0 && s.kv < s.n) no_tiles(p, s);
-      }
-      int64_t inc = one, inc1 = one1;
-      for (int x = 1; x < 32; x <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, inc, x), o1 = __shfl_up_sync(0xffffffffu, inc1, x);
-        if (lane >= x) {
-          inc += o;
-          inc1 += o1;
-        }
-      }
-      if (lane == 31) {
-        sh.warp_sum[warp] = inc;
-        sh.warp_sum1[warp] = inc1;
-      }
-      __syncthreads();
-      int64_t base = before, base1 = before1;
-      for (int i = 0; i < kAtThreads / 32; ++i) {
-        const int64_t x = sh.warp_sum[i], x1 = sh.warp_sum1[i];
-        if (i < warp) {
-          base += x;
-          base1 += x1;
-        }
-        before += x;
-        before1 += x1;
-      }
-      if (p.batch.B <= kAtThreads) {
-        total = before;
-        total1 = before1;
-      }
-      fixed = line_fixed(total, p.n_ctas);
-      const int64_t mine = one + fixed * one1, off = base + inc + fixed * (base1 + inc1) - mine;
-      const int64_t lo = part_begin(total + fixed * total1, own_cta, p.n_ctas);
-      if (b < p.batch.B && off <= lo && lo < off + mine) {
-        sh.seq = b;
-        sh.off = off;
-      }
-      if (b0 + kAtThreads < p.batch.B) __syncthreads();
-    }
-    total += fixed * total1;
-    if (threadIdx.x == 0) {
-      sh.total = total;
-      sh.fixed = fixed;
-    }
-  }
+  const int own_cta = p.n_ctas - 1 - cta;  // the own-pages line is mirrored, so that short lines meet on different CTAs
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  grid_dep_wait();
   auto tm_s = [&](int g) { return tmem + 128 * g; };
   auto tm_o = [&](int g) { return tmem + 256 + D * g; };
   if (warp >= 8) {
@@ -435,6 +358,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         // the prefix's line is that of one sequence of all new positions
         AtPart a;
         a.line = (turn ^ cta) & 1;
+        if (a.line == 1) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.scanned, 0, status, kWaitLimitCycles));
+          if (!ok) break;
+        }
         a.fixed = a.line == 0 ? pl.fixed : sh.fixed;
         const int64_t total = a.line == 0 ? pl.total : sh.total;
         const int c = a.line == 0 ? cta : own_cta;
@@ -645,8 +572,94 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   } else {
     regs_up<kAtSoftmaxRegs>();
     // ---------------- softmax groups ----------------
+    // ---- first, beside the producer's start on the prefix: the own-pages line's
+    // weight, and where this CTA's part of it begins ----
+    {
+      // the weight of the tiles alone and of an item's fixed tile go side by side
+      // until the first sum says which fixed cost counts
+      int64_t total = 0, total1 = 0;
+      if (p.batch.B > kScanWarps * 32) {  // several chunks: their sums first
+        int64_t w = 0, w1 = 0;
+        for (int b = threadIdx.x; b < p.batch.B; b += kScanWarps * 32) {
+          const SeqSpan s = seq_span(p.batch, b);
+          const int64_t x = seq_head_weight(p, s, 0);
+          w += x * p.n_heads;
+          w1 += (seq_head_weight(p, s, 1) - x) * p.n_heads;
+        }
+        for (int x = 16; x; x >>= 1) {
+          w += __shfl_xor_sync(0xffffffffu, w, x);
+          w1 += __shfl_xor_sync(0xffffffffu, w1, x);
+        }
+        if (lane == 0) {
+          sh.warp_sum[warp] = w;
+          sh.warp_sum1[warp] = w1;
+        }
+        named_sync(1, kScanWarps * 32);
+        for (int i = 0; i < kScanWarps; ++i) {
+          total += sh.warp_sum[i];
+          total1 += sh.warp_sum1[i];
+        }
+        named_sync(1, kScanWarps * 32);
+      }
+      int64_t before = 0, before1 = 0;  // of the chunks before this one
+      int fixed = 0;
+      for (int b0 = 0; b0 < p.batch.B; b0 += kScanWarps * 32) {
+        const int b = b0 + threadIdx.x;
+        int64_t one = 0, one1 = 0;
+        if (b < p.batch.B) {
+          const SeqSpan s = seq_span(p.batch, b);
+          const int64_t x = seq_head_weight(p, s, 0);
+          one = x * p.n_heads;
+          one1 = (seq_head_weight(p, s, 1) - x) * p.n_heads;
+          if (cta == 0 && s.kv < s.n) no_tiles(p, s);
+        }
+        int64_t inc = one, inc1 = one1;
+        for (int x = 1; x < 32; x <<= 1) {
+          const int64_t o = __shfl_up_sync(0xffffffffu, inc, x), o1 = __shfl_up_sync(0xffffffffu, inc1, x);
+          if (lane >= x) {
+            inc += o;
+            inc1 += o1;
+          }
+        }
+        if (lane == 31) {
+          sh.warp_sum[warp] = inc;
+          sh.warp_sum1[warp] = inc1;
+        }
+        named_sync(1, kScanWarps * 32);
+        int64_t base = before, base1 = before1;
+        for (int i = 0; i < kScanWarps; ++i) {
+          const int64_t x = sh.warp_sum[i], x1 = sh.warp_sum1[i];
+          if (i < warp) {
+            base += x;
+            base1 += x1;
+          }
+          before += x;
+          before1 += x1;
+        }
+        if (p.batch.B <= kScanWarps * 32) {
+          total = before;
+          total1 = before1;
+        }
+        fixed = line_fixed(total, p.n_ctas);
+        const int64_t mine = one + fixed * one1, off = base + inc + fixed * (base1 + inc1) - mine;
+        const int64_t lo = part_begin(total + fixed * total1, own_cta, p.n_ctas);
+        if (b < p.batch.B && off <= lo && lo < off + mine) {
+          sh.seq = b;
+          sh.off = off;
+        }
+        if (b0 + kScanWarps * 32 < p.batch.B) named_sync(1, kScanWarps * 32);
+      }
+      total += fixed * total1;
+      if (threadIdx.x == 0) {
+        sh.total = total;
+        sh.fixed = fixed;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.scanned);
+    }
     const int g = warp >> 2, quad = warp & 3, r = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const int row_tok = r / p.group, row_head = r % p.group;
     uint32_t ph_s = 0, ph_o[2] = {0, 0}, ph_meet = 0, base = 0;
     bool ok = true;
     // all eight warps meet (a wait with a limit, unlike a barrier instruction)
@@ -674,7 +687,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       const int rows = (two && g == 1 ? a.n1 : a.n0) * p.group;
       const int mine = two ? tiles : (tiles + 1 - g) / 2;
       const bool warp_live = quad * 32 < rows;
-      const int tok = first + r / p.group, gq = r % p.group;
+      const int tok = first + row_tok, gq = row_head;
       float m = -INFINITY, l = 0.f;
 
       // entries this row sees: all below `lim`, then the mask's bits from `lim` on
@@ -691,8 +704,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       }
       // Values past the last entry, in its page, may be anything: zero times that
       // must be zero.  The tile in question, and its rows live .. end - 1.
-      const int live = a.len % kAtTile, end = (live + p.box_rows - 1) / p.box_rows * p.box_rows;
-      const int ragged = live < end ? a.len / kAtTile : -1;
+      const int live = a.len & (kAtTile - 1), end = (live + p.box_rows - 1) & -p.box_rows;  // box_rows: a power of two
+      const int ragged = live < end ? a.len >> 7 : -1;
       for (int i = 0; i < mine && ok; ++i) {
         const int t = a.t0 + (two ? i : 2 * i + g);
         ok = __all_sync(0xffffffffu, mbar_wait(&sh.s_full[g], ph_s, status, kWaitLimitCycles));
