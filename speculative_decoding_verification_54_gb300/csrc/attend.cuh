@@ -27,14 +27,13 @@
 //                   one, the groups share its rows and alternate key tiles
 //                   (their halves are joined at the end of the part), so that
 //                   exponentials of one overlap products of the other.
-//   warp 8          the scheduler and producer: finds the CTA's parts, queues
-//                   them for the others and loads key and value tiles (TMA,
-//                   one box per run of a page and 64 dims) into a ring.
+//   warp 8          the scheduler: finds the CTA's parts, queues them for the
+//                   others and loads their queries (TMA).
 //   warp 9          issues the products: S = Q K^T (both operands
 //                   from shared memory) and O += P V (P from TMEM, where the
 //                   softmax group wrote it over S; V's rows are K).
-//   warp 10         loads the queries of each part (TMA).
-//   warp 11         only fills its warpgroup.
+//   warps 10, 11    load key and value tiles into a ring (TMA, one box per run
+//                   of a page and 64 dims).
 // TMEM: S0 S1 (128 columns each) and O0 O1 (D columns each).
 //
 // The reference m of a row rises only when a tile's maximum passes it by more
@@ -282,7 +281,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
     }
     for (int i = 0; i < kAtQueue; ++i) {
       mbar_init(&sh.part_full[i], 1);
-      mbar_init(&sh.part_empty[i], 10);  // eight softmax warps, the issuer, the queries' warp
+      mbar_init(&sh.part_empty[i], 11);  // eight softmax warps, the issuer, the two loaders
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&sh.q_full[g], 1);
@@ -310,40 +309,32 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   if (warp >= 8) {
     regs_down<kAtOtherRegs>();
     if (warp == 8) {
-      // ---------------- scheduler and producer (the whole warp) ----------------
+      // ---------------- scheduler (the whole warp): parts, and their queries ----------------
       const PrefixLine pl = prefix_line(p);
-      const int n_boxes = kAtTile / p.box_rows;
-      const int my_box = lane % n_boxes, my_half = lane / n_boxes;
-      const bool loads = my_half < kHalves;
-      const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
-      int slot = 0, queued = 0;
-      uint32_t loaded = 0;  // tiles, for the ring's phases
+      int queued = 0;
+      uint32_t q_loads[2] = {0, 0};
       bool ok = true;
-
-      // one tile (keys or values) of 128 entries from `key0` on, of which `len`
-      // are live; boxes past them read as zero
-      auto load_tile = [&](const CUtensorMap* map, int head, int page, int key0) {
-        if (loaded >= kSlots) ok = ok && mbar_wait(&sh.kv_empty[slot], ((loaded / kSlots) & 1) ^ 1, status, kWaitLimitCycles);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[slot], kTileBytes);
-        __syncwarp();
-        if (loads)
-          tma_load_4d(smem_u32(ring) + slot * kTileBytes + my_half * kHalfBytes + my_box * box_bytes, map, my_half * 64,
-                      static_cast<uint32_t>(key0 + my_box * p.box_rows) % static_cast<uint32_t>(p.batch.page_size), head, page, &sh.kv_full[slot]);
-        ++loaded;
-        if (++slot == kSlots) slot = 0;
+      // The queries of a part whose first positions are `first`: row tile g of
+      // two, or (-1) none for a group without key tiles.
+      auto load_queries = [&](int head, int first0, int first1) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int first = g == 0 ? first0 : first1;
+          if (first < 0) continue;
+          if (q_loads[g] > 0)
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&sh.q_empty[g], (q_loads[g] & 1) ^ 1, status, kWaitLimitCycles));
+          if (!ok) return;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[g], kHalves * 128u * p.group * p.tok_tile);
+          __syncwarp();
+          if (lane < kHalves)
+            tma_load_3d(smem_u32(qbuf) + g * kTileBytes + lane * kHalfBytes, &p.tmQ, lane * 64, head * p.group, first,
+                        &sh.q_full[g]);
+          ++q_loads[g];
+        }
       };
-      auto page_of = [&](const AtPart& a, int t) {
-        const uint32_t key = static_cast<uint32_t>(t) * kAtTile + my_box * p.box_rows;
-        if (!loads || t >= a.t1 || key >= static_cast<uint32_t>(a.len)) return p.n_pages;  // the copy fills zeros
-        const uint32_t i = key / static_cast<uint32_t>(p.batch.page_size);
-        const int page = a.line == 0 ? p.prefix_table[i]
-                                     : p.batch.block_table[static_cast<int64_t>(a.seq) * p.batch.table_width + i];
-        if (page >= 0 && page < p.n_pages) return page;
-        atomicOr(status, kStatusBadCache);
-        return p.n_pages;
-      };
+      // After the first part the queries come one part behind the queue: their
+      // buffers come free late, and the key and value loads need not wait.
+      int late_head = 0, late0 = -1, late1 = -1;
       // a free place of the queue
       auto queue_place = [&]() {
         const int q = queued % kAtQueue;
@@ -413,24 +404,20 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
                 sh.parts[q] = a;
                 mbar_arrive(&sh.part_full[q]);
               }
-              // The order the products want the tiles in: with two row tiles
-              // K V K V ...; with one, the groups alternate and the next keys
-              // come before these values: K0 K1 V0 K2 V1 ... V.  Step i loads
-              // the keys of `kt` and the values of `vt`.
-              const int lead = a.n1 > 0 ? 0 : 1;
-              int page = page_of(a, a.t0), vpage = page;
-#pragma unroll 1
-              for (int kt = a.t0; kt < a.t1 + lead && ok; ++kt) {
-                const int vt = kt - lead, next = page_of(a, kt + 1);
-                if (kt < a.t1) load_tile(&p.tmK, a.head, page, kt * kAtTile);
-                if (vt >= a.t0 && ok) load_tile(&p.tmV, a.head, lead ? vpage : page, vt * kAtTile);
-                vpage = page;
-                page = next;
+              const int first1 = a.n1 > 0 ? a.first + a.n0 : a.t1 - a.t0 > 1 ? a.first : -1;
+              if (queued == 1) {
+                load_queries(a.head, a.first, first1);
+              } else {
+                if (late0 >= 0) load_queries(late_head, late0, late1);
+                late_head = a.head;
+                late0 = a.first;
+                late1 = first1;
               }
             }
           }
         }
       }
+      if (ok && late0 >= 0) load_queries(late_head, late0, late1);
       if (ok) {
         const int q = queue_place();
         if (ok && lane == 0) {
@@ -438,10 +425,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           mbar_arrive(&sh.part_full[q]);
         }
       }
-      // the copies of the last tiles land before the CTA exits
-#pragma unroll 1
-      for (uint32_t i = loaded > kSlots ? loaded - kSlots : 0; i < loaded; ++i)
-        mbar_wait(&sh.kv_full[i % kSlots], (i / kSlots) & 1, status, kWaitLimitCycles);
+#pragma unroll
+      for (int g = 0; g < 2; ++g)  // the last copies land before the CTA exits
+        if (q_loads[g] > 0) mbar_wait(&sh.q_full[g], (q_loads[g] & 1) ^ 1, status, kWaitLimitCycles);
     } else if (warp == 9) {
       // ---------------- issuer (the whole warp; one thread issues) ----------------
       constexpr uint32_t id_qk = idesc_f16_f32(kBf16, false, kAtTile, kAtTile);
@@ -535,39 +521,73 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       if (elect_one()) tc_commit(&sh.done);
       __syncwarp();
       mbar_wait(&sh.done, 0, status, kWaitLimitCycles);
-    } else if (warp == 10) {
-      // ---------------- queries (their own warp: the buffers come free late, and keys must not wait) ----------------
-      uint32_t loads[2] = {0, 0};
+    } else {
+      // ---------------- key loads (warp 10) and value loads (warp 11) ----------------
+      // One box a lane: a run of a page's slots, 64 dims.  (One warp for both
+      // could not keep up with pages of 16: 3,300 clocks a key tile.)
+      const bool values = warp == 11;
+      const CUtensorMap* const map = values ? &p.tmV : &p.tmK;
+      const int n_boxes = kAtTile / p.box_rows;
+      const int my_box = lane % n_boxes, my_half = lane / n_boxes;
+      const bool loads = my_half < kHalves;
+      const uint32_t my_dst = smem_u32(ring) + my_half * kHalfBytes + my_box * p.box_rows * 128;
+      const uint32_t page_size = p.batch.page_size;
+      uint32_t base = 0, last = 0;  // tiles of the ring before this part; 1 + the last one this warp put in slot `lane`
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, status, kWaitLimitCycles));
-        return ok;
-      };
 #pragma unroll 1
       for (int n = 0; ok; ++n) {
         const int q = n % kAtQueue;
-        if (!wait(&sh.part_full[q], (n / kAtQueue) & 1)) break;
-        const int line = sh.parts[q].line, tiles = sh.parts[q].t1 - sh.parts[q].t0, head = sh.parts[q].head,
-                  first = sh.parts[q].first, n0 = sh.parts[q].n0, n1 = sh.parts[q].n1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh.part_full[q], (n / kAtQueue) & 1, status, kWaitLimitCycles));
+        if (!ok) break;
+        const int line = sh.parts[q].line, head = sh.parts[q].head, t0 = sh.parts[q].t0, tiles = sh.parts[q].t1 - t0,
+                  len = sh.parts[q].len, seq = sh.parts[q].seq;
+        const bool two = sh.parts[q].n1 > 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.part_empty[q]);
         if (line < 0) break;
-        // row tile g of two, or the one tile for each group that has key tiles
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (n1 == 0 && g == 1 && tiles < 2) continue;
-          if (loads[g] > 0 && !wait(&sh.q_empty[g], (loads[g] & 1) ^ 1)) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[g], kHalves * 128u * p.group * p.tok_tile);
+        const int32_t* const table =
+            line == 0 ? p.prefix_table : p.batch.block_table + static_cast<int64_t>(seq) * p.batch.table_width;
+        // the page of this lane's box in the part's tile i, loaded three tiles
+        // ahead; past the entries n_pages, where the copy fills zeros
+        auto page_at = [&](int i) {
+          const uint32_t key = static_cast<uint32_t>(t0 + i) * kAtTile + my_box * p.box_rows;
+          return loads && i < tiles && key < static_cast<uint32_t>(len) ? table[key / page_size] : p.n_pages;
+        };
+        int page0 = page_at(0), page1 = page_at(1), page2 = page_at(2);
+#pragma unroll 1
+        for (int i = 0; i < tiles; ++i) {
+          // the order the products want the tiles in: with two row tiles
+          // K V K V ...; with one the groups alternate and the next keys come
+          // before these values: K0 K1 V0 K2 V1 ... V
+          const uint32_t at = base + (values ? (two ? 2 * i + 1 : min(2 * i + 2, 2 * tiles - 1))
+                                             : (two ? 2 * i : (i == 0 ? 0 : 2 * i - 1)));
+          const uint32_t slot = at % kSlots, use = at / kSlots;
+          int page = page0;
+          page0 = page1;
+          page1 = page2;
+          page2 = page_at(i + 3);
+          const uint32_t key = static_cast<uint32_t>(t0 + i) * kAtTile + my_box * p.box_rows;
+          if (page < 0 || page >= p.n_pages) {
+            if (loads && key < static_cast<uint32_t>(len)) atomicOr(status, kStatusBadCache);
+            page = p.n_pages;
+          }
+          const int at_slot = static_cast<int>(key % page_size);
+          if (use > 0)
+            ok = __all_sync(0xffffffffu, mbar_wait(&sh.kv_empty[slot], (use & 1) ^ 1, status, kWaitLimitCycles));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[slot], kTileBytes);
           __syncwarp();
-          if (lane < kHalves)
-            tma_load_3d(smem_u32(qbuf) + g * kTileBytes + lane * kHalfBytes, &p.tmQ, lane * 64, head * p.group,
-                        first + (n1 > 0 && g == 1 ? n0 : 0), &sh.q_full[g]);
-          ++loads[g];
+          if (loads) tma_load_4d(my_dst + slot * kTileBytes, map, my_half * 64, at_slot, head, page, &sh.kv_full[slot]);
+          if (lane == static_cast<int>(slot)) last = at + 1;
         }
+        base += 2 * tiles;
       }
-#pragma unroll
-      for (int g = 0; g < 2; ++g)  // the last copies land before the CTA exits
-        if (loads[g] > 0) mbar_wait(&sh.q_full[g], (loads[g] & 1) ^ 1, status, kWaitLimitCycles);
+      // Copies land before the CTA exits: the issuer waits for every tile, unless
+      // a wait ran out.  (Only then: a slot that the other loader has filled since
+      // is past the phase waited for here.)
+      if (!ok && lane < kSlots && last > 0)
+        mbar_wait(&sh.kv_full[lane], ((last - 1) / kSlots) & 1, status, kWaitLimitCycles);
+      __syncwarp();
     }
   } else {
     regs_up<kAtSoftmaxRegs>();
