@@ -244,7 +244,14 @@ int spec_kv_append(const spec_kv_cache* cache, const void* q, int64_t q_pos_stri
   p.n_q_heads = n_q_heads;
   p.D = D;
   p.half = rot_dim / 2;
-  p.tile = N <= 1024 ? 1 : 4;
+  // Positions a CTA takes: as few as fill the GPU once with three CTAs an SM,
+  // at most 24 (32,768 positions of 256 dims: 24 a CTA 196 us, 8 203 us, 4 216
+  // us, 2 251 us; a position's look-ups cost as much as streaming some 30 KB),
+  // and no more than 32 KB of cosines and sines.
+  p.tile = (N + 3 * kAppendSms - 1) / (3 * kAppendSms);
+  const int most = p.half > 0 ? 32 * 1024 / (p.half * static_cast<int>(sizeof(float2))) : kAppendMaxTile;
+  if (p.tile > most) p.tile = most;
+  if (p.tile > kAppendMaxTile) p.tile = kAppendMaxTile;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cache->dtype == SPEC_BF16 ? launch_append<__nv_bfloat16>(p, interleaved, s)
                                    : launch_append<__half>(p, interleaved, s);

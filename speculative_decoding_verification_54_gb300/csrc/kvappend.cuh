@@ -15,20 +15,23 @@
 // GB300's fp64 rate; this is three integer products.
 //
 // Layout.  A CTA takes a few positions.  Its threads first put the cosines and
-// sines of those positions into shared memory, once for all heads; then thread
-// i owns the 16-byte vector i % (D/8) of every head it visits, so it reads its
-// 8 pairs from shared memory once per position and streams the heads.  The
-// other half of a (f, f + rot/2) pair is a second load of the same row, from
-// L1.  Bound by the copies: q, k, v read once, written once.
+// sines of those positions into shared memory, once for all heads; then each
+// thread owns two 16-byte vectors of every head it visits, the two that turn
+// together where pairs are (f, f + rot/2), so that it reads its 8 pairs'
+// cosines once per position and every vector once, and streams the heads.
+// Bound by the copies: q, k, v read once, written once.
 #pragma once
 
 #include "paged.cuh"
 
 namespace specv {
 
+// 256 threads, three CTAs an SM, two heads a thread in flight: 203 us on 32,768
+// positions of 256 dims; four heads 218, four CTAs 215, two CTAs with four heads 254.
 constexpr int kAppendThreads = 256;
-constexpr int kAppendMaxTile = 8;   // positions a CTA takes, at most
-constexpr int kAppendBatch = 4;     // heads a thread has in flight
+constexpr int kAppendMaxTile = 24;   // positions a CTA takes, at most
+constexpr int kAppendBatch = 2;     // heads a thread has in flight
+constexpr int kAppendSms = 152;      // GB300's; the tile size goes by it
 
 struct AppendParams {
   const uint16_t *q, *k, *v;
@@ -41,6 +44,12 @@ struct AppendParams {
   const int32_t* axis;
   int64_t position_base;
   int n_axes, n_q_heads, D, half, tile;  // half = rot_dim / 2
+
+  // row `row` of position n: query heads, then key heads, then value heads
+  __device__ __forceinline__ const uint16_t* row_src(int64_t n, int row) const {
+    const int Hk = cache.n_heads, k0 = row - n_q_heads;
+    return k0 < 0 ? q + n * q_ps + row * q_hs : k0 < Hk ? k + n * k_ps + k0 * k_hs : v + n * v_ps + (k0 - Hk) * v_hs;
+  }
 };
 
 template <typename T>
@@ -77,8 +86,78 @@ __device__ __forceinline__ float2 unit_of(int64_t position, uint64_t turn64) {
   return cs;
 }
 
+// a 16-byte vector that is read once: past L1
+__device__ __forceinline__ uint4 ld_once(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  Pack16<T>::unpack(v.x, x[0], x[1]);
+  Pack16<T>::unpack(v.y, x[2], x[3]);
+  Pack16<T>::unpack(v.z, x[4], x[5]);
+  Pack16<T>::unpack(v.w, x[6], x[7]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(Pack16<T>::pack(x[0], x[1]), Pack16<T>::pack(x[2], x[3]), Pack16<T>::pack(x[4], x[5]),
+                    Pack16<T>::pack(x[6], x[7]));
+}
+
+// dims e of x and of y are pair e
+template <typename T>
+__device__ __forceinline__ void turn_pair(uint4& xv, uint4& yv, const float* c, const float* s) {
+  float x[8], y[8], u[8], w[8];
+  unpack8<T>(xv, x);
+  unpack8<T>(yv, y);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    u[e] = fmaf(y[e], -s[e], x[e] * c[e]);
+    w[e] = fmaf(x[e], s[e], y[e] * c[e]);
+  }
+  xv = pack8<T>(u);
+  yv = pack8<T>(w);
+}
+
+// dims 2e and 2e + 1 of x are pair e; from dim `end` on x stays
+template <typename T>
+__device__ __forceinline__ void turn_neighbours(uint4& xv, const float* c, const float* s, int end) {
+  float x[8];
+  unpack8<T>(xv, x);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (2 * e >= end) continue;
+    const float u = fmaf(x[2 * e + 1], -s[e], x[2 * e] * c[e]);
+    x[2 * e + 1] = fmaf(x[2 * e], s[e], x[2 * e + 1] * c[e]);
+    x[2 * e] = u;
+  }
+  xv = pack8<T>(x);
+}
+
+// dims d and d + half are a pair, `half` no multiple of 8: the others one by
+// one.  A dim past rot_dim keeps its bits.
+template <typename T>
+__device__ __forceinline__ void turn_scattered(uint4& xv, const uint16_t* row, const float2* cs, int d0, int half) {
+  float x[8];
+  unpack8<T>(xv, x);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int d = d0 + e;
+    if (d >= 2 * half) continue;
+    const bool first = d < half;
+    const float2 a = cs[first ? d : d - half];
+    const float y = Pack16<T>::up(row[first ? d + half : d - half]);
+    x[e] = fmaf(y, first ? -a.y : a.y, x[e] * a.x);
+  }
+  xv = pack8<T>(x);
+}
+
 template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ float2 ap_units[];  // [tile][half]
   __shared__ int64_t s_dst[kAppendMaxTile];   // element offset of the entry in the pools, -1: not written
   __shared__ int64_t s_entry[kAppendMaxTile];
@@ -137,88 +216,69 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     __syncthreads();
   }
 
-  // ---- the heads: thread i owns vector i % vpr of each row it visits ----
-  const int vpr = p.D >> 3, rpi = kAppendThreads / vpr;
-  const int j = tid % vpr, r0 = tid / vpr;
+  // ---- the heads: thread i owns unit i % upr of each row it visits ----
+  const int vpr = p.D >> 3, upr = (vpr + 1) >> 1, rpi = kAppendThreads / upr;
+  const int u = tid % upr, r0 = tid / upr;
   if (r0 >= rpi) return;
   const int Hq = p.n_q_heads, Hk = p.cache.n_heads, rows = Hq + 2 * Hk;
-  const int d0 = 8 * j, rot = 2 * p.half;
-  const bool turned = d0 < rot;
-  const bool whole = (p.half & 7) == 0;  // the other halves of this vector's pairs are one vector too
+  const int hv = p.half >> 3, rot = 2 * p.half;
+  // the pairs of a vector are all in one other vector: the unit is the two
+  const bool paired = !kInterleaved && (p.half & 7) == 0 && u < hv;
+  const int v0 = paired ? u : !kInterleaved && (p.half & 7) == 0 ? 2 * hv + 2 * (u - hv) : 2 * u;
+  const int v1 = paired ? u + hv : v0 + 1;
+  const bool two = v1 < vpr;
+  const int d0 = 8 * v0, d1 = 8 * v1;
   for (int t = 0; t < tile; ++t) {
     if (!s_live[t]) continue;
     const int64_t n = n0 + t, dst0 = s_dst[t];
-    // this vector's cosines, and sines with the sign of the other half's term;
-    // dims that are not rotated take cos 1, sin 0
+    const float2* cs = ap_units + t * p.half;
+    // a pair of vectors turns by its 8 angles; neighbours have 4 each
     float c[8], s[8];
+    if (paired || (kInterleaved && d0 < rot)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int d = d0 + e;
-      const int f = kInterleaved ? d >> 1 : (d < p.half ? d : d - p.half);
-      const bool first = kInterleaved ? (d & 1) == 0 : d < p.half;
-      float2 u = make_float2(1.f, 0.f);
-      if (d < rot) u = ap_units[t * p.half + f];
-      c[e] = u.x;
-      s[e] = first ? -u.y : u.y;
+      for (int e = 0; e < 8; ++e) {
+        const int f = kInterleaved ? (d0 >> 1) + e : d0 + e;
+        const float2 x = f < p.half ? cs[f] : make_float2(1.f, 0.f);
+        c[e] = x.x;
+        s[e] = x.y;
+      }
     }
     for (int row0 = r0; row0 < rows; row0 += kAppendBatch * rpi) {
-      uint4 own[kAppendBatch], other[kAppendBatch];
-      const uint16_t* src[kAppendBatch];
+      uint4 a[kAppendBatch], b[kAppendBatch];
 #pragma unroll
       for (int i = 0; i < kAppendBatch; ++i) {
         const int row = row0 + i * rpi;
-        own[i] = other[i] = make_uint4(0, 0, 0, 0);
-        src[i] = nullptr;
         if (row >= rows) continue;
-        src[i] = row < Hq        ? p.q + n * p.q_ps + row * p.q_hs
-                 : row < Hq + Hk ? p.k + n * p.k_ps + (row - Hq) * p.k_hs
-                                 : p.v + n * p.v_ps + (row - Hq - Hk) * p.v_hs;
-        own[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + d0));
-        if (!kInterleaved && turned && whole && row < Hq + Hk)
-          other[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + (d0 < p.half ? d0 + p.half : d0 - p.half)));
+        const uint16_t* src = p.row_src(n, row);
+        a[i] = ld_once(src + d0);
+        if (two) b[i] = ld_once(src + d1);
       }
 #pragma unroll
       for (int i = 0; i < kAppendBatch; ++i) {
         const int row = row0 + i * rpi;
         if (row >= rows) continue;
-        uint4 w = own[i];
-        if (turned && row < Hq + Hk) {
-          float x[8], y[8];
-          Pack16<T>::unpack(own[i].x, x[0], x[1]);
-          Pack16<T>::unpack(own[i].y, x[2], x[3]);
-          Pack16<T>::unpack(own[i].z, x[4], x[5]);
-          Pack16<T>::unpack(own[i].w, x[6], x[7]);
-          if (kInterleaved) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
-          } else if (whole) {
-            Pack16<T>::unpack(other[i].x, y[0], y[1]);
-            Pack16<T>::unpack(other[i].y, y[2], y[3]);
-            Pack16<T>::unpack(other[i].z, y[4], y[5]);
-            Pack16<T>::unpack(other[i].w, y[6], y[7]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int d = d0 + e;
-              y[e] = d < rot ? Pack16<T>::up(__ldg(src[i] + (d < p.half ? d + p.half : d - p.half))) : 0.f;
-            }
+        uint4 x = a[i], y = b[i];
+        if (row < Hq + Hk) {
+          if (paired) {
+            turn_pair<T>(x, y, c, s);
+          } else if (kInterleaved) {
+            if (d0 < rot) turn_neighbours<T>(x, c, s, rot - d0);
+            if (two && d1 < rot) turn_neighbours<T>(y, c + 4, s + 4, rot - d1);
+          } else if (d0 < rot && (p.half & 7) != 0) {
+            turn_scattered<T>(x, p.row_src(n, row), cs, d0, p.half);
+            if (two) turn_scattered<T>(y, p.row_src(n, row), cs, d1, p.half);
           }
-          // a dim past rot_dim keeps its bits: cos 1, sin 0, and its partner
-          // (which may be infinite) left out
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = d0 + e < rot ? fmaf(y[e], s[e], x[e] * c[e]) : x[e];
-          w.x = Pack16<T>::pack(x[0], x[1]);
-          w.y = Pack16<T>::pack(x[2], x[3]);
-          w.z = Pack16<T>::pack(x[4], x[5]);
-          w.w = Pack16<T>::pack(x[6], x[7]);
         }
+        uint16_t* dst;
         if (row < Hq) {
-          *reinterpret_cast<uint4*>(p.q_out + (n * Hq + row) * p.D + d0) = w;
-        } else if (dst0 >= 0) {
+          dst = p.q_out + (n * Hq + row) * p.D;
+        } else {
+          if (dst0 < 0) continue;
           const bool is_k = row < Hq + Hk;
-          uint16_t* pool = is_k ? p.cache.k : p.cache.v;
-          *reinterpret_cast<uint4*>(pool + dst0 + (row - Hq - (is_k ? 0 : Hk)) * p.cache.head_stride + d0) = w;
+          dst = (is_k ? p.cache.k : p.cache.v) + dst0 + (row - Hq - (is_k ? 0 : Hk)) * p.cache.head_stride;
         }
+        *reinterpret_cast<uint4*>(dst + d0) = x;
+        if (two) *reinterpret_cast<uint4*>(dst + d1) = y;
       }
     }
   }
