@@ -434,6 +434,8 @@ def make_kv_cache(k_pages, v_pages) -> SpecKvCache:
                         page_size, n_heads, head_dim, codes[k_pages.dtype])
     cache.tensors = (k_pages, v_pages)
     cache.address = ctypes.addressof(cache)
+    # what every call compares with, read once
+    cache.expected = (k_pages.dtype, n_heads, head_dim, page_size, k_pages.device.index)
     return cache
 
 
@@ -447,6 +449,16 @@ def spec_attention_workspace_bytes(B: int, N: int, n_q_heads: int, head_dim: int
 def make_attention_workspace(B: int, N: int, n_q_heads: int, head_dim: int, device="cuda"):
     """Allocate (torch) and zero a workspace for spec_kv_append and spec_prefix_attention."""
     return _aligned_zeros(spec_attention_workspace_bytes(B, N, n_q_heads, head_dim), device)
+
+
+def _call_stream(stream, device_index):
+    """The caller's stream, or PyTorch's current one (its raw handle: building
+    the Stream object costs as much as the launch)."""
+    if stream is not None:
+        return _stream(stream)
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device_index) if raw is not None else torch.cuda.current_stream(device_index).cuda_stream
 
 
 def _positions_first(name, cache, *tensors):
@@ -489,34 +501,60 @@ def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspa
     no rotation); positions int32 [n_axes, N] and axis int32 [rot_dim / 2], or
     None for position_base + the entry's index."""
     import torch
-    _positions_first("spec_kv_append", cache, q, k, v, q_out)
-    B = _batch_checks("spec_kv_append", q_indptr, block_table, kv_len)
-    n_axes, rot = 1, 0
+    dt, n_heads, D, _, device = cache.expected
+    i32, q_shape, k_shape = torch.int32, q.shape, k.shape
+    # one pass over what has to hold; which one does not is found out after
+    if not (q.dtype is dt and k.dtype is dt and v.dtype is dt and q_out.dtype is dt
+            and len(q_shape) == 3 and q_shape[2] == D and k_shape == (q_shape[0], n_heads, D) and v.shape == k_shape
+            and q_out.shape == q_shape and q_out.is_contiguous()
+            and q_indptr.dtype is i32 and kv_len.dtype is i32 and block_table.dtype is i32
+            and kv_len.dim() == 1 and q_indptr.shape == (kv_len.shape[0] + 1,)
+            and block_table.dim() == 2 and block_table.shape[0] == kv_len.shape[0]
+            and q_indptr.is_contiguous() and kv_len.is_contiguous() and block_table.is_contiguous()
+            and q.is_cuda and k.is_cuda and v.is_cuda and q_out.is_cuda and q_indptr.is_cuda and kv_len.is_cuda
+            and block_table.is_cuda and workspace.is_cuda and device is not None):
+        _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspace)
+    q_stride, k_stride, v_stride = q.stride(), k.stride(), v.stride()
+    if q_stride[2] != 1 or k_stride[2] != 1 or v_stride[2] != 1:
+        _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspace)
+    n_axes, rot, freq, pos, ax = 1, 0, None, None, None
     if inv_freq is not None:
         rot = 2 * inv_freq.shape[0]
-        if inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
+        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise SpecVerifyError(SPEC_ERR_INVALID_ARG, "spec_kv_append: inv_freq must be contiguous float32")
+        freq = inv_freq.data_ptr()
     if positions is not None:
         n_axes = positions.shape[0]
-        if positions.dtype != torch.int32 or tuple(positions.shape) != (n_axes, q.shape[0]) \
+        if positions.dtype is not i32 or tuple(positions.shape) != (n_axes, q_shape[0]) \
                 or not positions.is_contiguous():
             raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_kv_append: positions {positions.dtype} "
-                                  f"{tuple(positions.shape)}, expected contiguous int32 [n_axes, {q.shape[0]}]")
-    if axis is not None and (axis.dtype != torch.int32 or 2 * axis.numel() != rot or not axis.is_contiguous()):
-        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_kv_append: axis {axis.dtype} {tuple(axis.shape)}, expected "
-                              f"contiguous int32 [{rot // 2}]")
-    n_heads = cache.n_heads
+                                  f"{tuple(positions.shape)}, expected contiguous int32 [n_axes, {q_shape[0]}]")
+        pos = positions.data_ptr()
+    if axis is not None:
+        if axis.dtype is not i32 or 2 * axis.numel() != rot or not axis.is_contiguous():
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_kv_append: axis {axis.dtype} {tuple(axis.shape)}, "
+                                  f"expected contiguous int32 [{rot // 2}]")
+        ax = axis.data_ptr()
+    _on_gpu("spec_kv_append", inv_freq, positions, axis)
+    lib = _lib or load()
+    code = lib.spec_kv_append(
+        cache.address, q.data_ptr(), q_stride[0], q_stride[1], k.data_ptr(), k_stride[0], k_stride[1], v.data_ptr(),
+        v_stride[0], v_stride[1], q_shape[1], q_shape[0], q_indptr.data_ptr(), kv_len.shape[0], block_table.data_ptr(),
+        block_table.shape[1], kv_len.data_ptr(), freq, pos, n_axes, ax, rot, 1 if interleaved else 0, position_base,
+        q_out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _call_stream(stream, device))
+    if code != SPEC_OK:
+        _check(code, "spec_kv_append")
+
+
+def _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspace):
+    name, n_heads = "spec_kv_append", cache.n_heads
+    _positions_first(name, cache, q, k, v, q_out)
+    _batch_checks(name, q_indptr, block_table, kv_len)
     if k.shape[1] != n_heads or v.shape[1] != n_heads or q_out.shape != q.shape or not q_out.is_contiguous():
-        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_kv_append: q {tuple(q.shape)}, k {tuple(k.shape)}, "
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: q {tuple(q.shape)}, k {tuple(k.shape)}, "
                               f"v {tuple(v.shape)}, q_out {tuple(q_out.shape)}, {n_heads} cache heads")
-    _on_gpu("spec_kv_append", cache.tensors[0], cache.tensors[1], q, k, v, q_out, q_indptr, block_table, kv_len,
-            inv_freq, positions, axis, workspace)
-    _check(load().spec_kv_append(
-        cache.address, q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-        v.stride(0), v.stride(1), q.shape[1], q.shape[0], q_indptr.data_ptr(), B, block_table.data_ptr(),
-        block_table.shape[1], kv_len.data_ptr(), _ptr(inv_freq), _ptr(positions), n_axes, _ptr(axis), rot,
-        1 if interleaved else 0, position_base, q_out.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
-        _stream(stream)), "spec_kv_append")
+    _on_gpu(name, cache.tensors[0], cache.tensors[1], q, k, v, q_out, q_indptr, block_table, kv_len, workspace)
+    raise SpecVerifyError(SPEC_ERR_INVALID_ARG, name)
 
 
 def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspace, prefix_table=None, prefix_len=0,
@@ -529,28 +567,53 @@ def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspac
     position sees new entry j) or None for a chain; scale defaults to
     D ** -0.5; lse float32 [N, n_q_heads] or None.  The rest as spec_kv_append."""
     import torch
-    _positions_first("spec_prefix_attention", cache, q, out)
-    B = _batch_checks("spec_prefix_attention", q_indptr, block_table, kv_len)
-    N, n_q_heads, D = q.shape
+    dt, n_heads, D, page_size, device = cache.expected
+    i32, q_shape = torch.int32, q.shape
+    if not (q.dtype is dt and out.dtype is dt and len(q_shape) == 3 and q_shape[2] == D and out.shape == q_shape
+            and q_indptr.dtype is i32 and kv_len.dtype is i32 and block_table.dtype is i32
+            and kv_len.dim() == 1 and q_indptr.shape == (kv_len.shape[0] + 1,)
+            and block_table.dim() == 2 and block_table.shape[0] == kv_len.shape[0]
+            and q_indptr.is_contiguous() and kv_len.is_contiguous() and block_table.is_contiguous()
+            and q.is_cuda and out.is_cuda and q_indptr.is_cuda and kv_len.is_cuda and block_table.is_cuda
+            and workspace.is_cuda and device is not None):
+        _refuse_attention(cache, q, out, q_indptr, block_table, kv_len, workspace)
+    q_stride, out_stride = q.stride(), out.stride()
+    if q_stride[2] != 1 or out_stride[2] != 1:
+        _refuse_attention(cache, q, out, q_indptr, block_table, kv_len, workspace)
+    N, n_q_heads = q_shape[0], q_shape[1]
+    shared = mask = stats = None
+    if prefix_len > 0:
+        if prefix_table is None or prefix_table.dtype is not i32 or prefix_table.dim() != 1 \
+                or not prefix_table.is_contiguous() or prefix_table.shape[0] * page_size < prefix_len:
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: prefix_table does not hold the pages "
+                                  f"of {prefix_len} entries")
+        shared = prefix_table.data_ptr()
+    if draft_mask is not None:
+        if draft_mask.dtype is not torch.int64 or draft_mask.shape != (N,) or not draft_mask.is_contiguous():
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: draft_mask {draft_mask.dtype} "
+                                  f"{tuple(draft_mask.shape)}, expected contiguous int64 [{N}]")
+        mask = draft_mask.data_ptr()
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (N, n_q_heads) or not lse.is_contiguous():
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: lse {lse.dtype} {tuple(lse.shape)}, "
+                                  f"expected contiguous float32 [{N}, {n_q_heads}]")
+        stats = lse.data_ptr()
+    _on_gpu("spec_prefix_attention", prefix_table, draft_mask, lse)
+    lib = _lib or load()
+    code = lib.spec_prefix_attention(
+        cache.address, q.data_ptr(), q_stride[0], q_stride[1], n_q_heads, N, q_indptr.data_ptr(), kv_len.shape[0],
+        shared, prefix_len, block_table.data_ptr(), block_table.shape[1], kv_len.data_ptr(), mask,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), out_stride[0], out_stride[1], stats,
+        workspace.data_ptr(), workspace.nbytes, _call_stream(stream, device))
+    if code != SPEC_OK:
+        _check(code, "spec_prefix_attention")
+
+
+def _refuse_attention(cache, q, out, q_indptr, block_table, kv_len, workspace):
+    name = "spec_prefix_attention"
+    _positions_first(name, cache, q, out)
+    _batch_checks(name, q_indptr, block_table, kv_len)
     if out.shape != q.shape:
-        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: q {tuple(q.shape)}, out {tuple(out.shape)}")
-    if prefix_len > 0 and (prefix_table is None or prefix_table.dtype != torch.int32 or prefix_table.dim() != 1
-                           or not prefix_table.is_contiguous()
-                           or prefix_table.shape[0] * cache.page_size < prefix_len):
-        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: prefix_table does not hold the pages of "
-                              f"{prefix_len} entries")
-    if draft_mask is not None and (draft_mask.dtype != torch.int64 or tuple(draft_mask.shape) != (N,)
-                                   or not draft_mask.is_contiguous()):
-        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: draft_mask {draft_mask.dtype} "
-                              f"{tuple(draft_mask.shape)}, expected contiguous int64 [{N}]")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (N, n_q_heads)
-                            or not lse.is_contiguous()):
-        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: lse {lse.dtype} {tuple(lse.shape)}, "
-                              f"expected contiguous float32 [{N}, {n_q_heads}]")
-    _on_gpu("spec_prefix_attention", cache.tensors[0], cache.tensors[1], q, out, q_indptr, block_table, kv_len,
-            prefix_table, draft_mask, lse, workspace)
-    _check(load().spec_prefix_attention(
-        cache.address, q.data_ptr(), q.stride(0), q.stride(1), n_q_heads, N, q_indptr.data_ptr(), B,
-        _ptr(prefix_table), prefix_len, block_table.data_ptr(), block_table.shape[1], kv_len.data_ptr(),
-        _ptr(draft_mask), D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1),
-        _ptr(lse), workspace.data_ptr(), _nbytes(workspace), _stream(stream)), "spec_prefix_attention")
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: q {tuple(q.shape)}, out {tuple(out.shape)}")
+    _on_gpu(name, cache.tensors[0], cache.tensors[1], q, out, q_indptr, block_table, kv_len, workspace)
+    raise SpecVerifyError(SPEC_ERR_INVALID_ARG, name)
