@@ -6,20 +6,18 @@
 // and values are read once per row block and not once per sequence; over the
 // sequences' own pages the rows of one sequence are.  An item is a block of
 // up to two row tiles (128 rows each: whole positions) against all tiles of
-// 128 keys that its rows see.  The items' key tiles, weighted by their row
-// tiles, form two lines, one over the prefix and one over the own pages, and
-// CTA c takes the c-th equal part of each: lengths are read on the device, so
-// nothing is planned on the host, and one sequence or one head fills the GPU
-// as well as many.  Even CTAs begin with their prefix part (bound by the
-// tensor cores), odd ones with their own-pages part (bound by HBM), so the two
-// overlap.
+// 128 keys that its rows see.  The items' key tiles, weighted by what they
+// cost, form one line, the prefix's items first, and CTA c takes its c-th equal
+// part: lengths are read on the device, so nothing is planned on the host, and
+// one sequence or one head fills the GPU as well as many.  CTAs bound by the
+// tensor cores (prefix) and CTAs bound by HBM (own pages) run side by side.
 //
 // A part of an item leaves, per row, the unnormalised output, its reference
 // exponent m and the sum l: O = sum_t 2^(s_t - m) v_t, l = sum_t 2^(s_t - m)
 // with s in units of log2.  The part that holds an item's first tile writes to
-// the row's own place, any other to its CTA's slab (it is the CTA's first in
-// that line); attend_join_kernel adds a row's parts in a fixed order, so
-// results do not depend on timing.
+// the row's own place, any other to its CTA's slab (it is the CTA's first
+// part); attend_join_kernel adds a row's parts in a fixed order, so results do
+// not depend on timing.
 //
 // One CTA per SM:
 //   warps 0-3, 4-7  softmax groups 0 and 1, one thread a row.  With two row
@@ -59,7 +57,7 @@ constexpr int kAtRingBytes = 160 * 1024;
 constexpr int kAtMaxCtas = 160;     // slabs in the workspace
 constexpr int kScanWarps = 8;       // the softmax warps add up the sequences' work
 constexpr int kAtQueue = 4;         // parts queued ahead
-constexpr int kAtFixed = 3;         // a part's fixed cost in key tiles
+constexpr int kAtFixed = 15;        // weight of a part's fixed cost
 constexpr float kAtRise = 8.f;      // log2 of the largest weight
 
 struct AttendParams {
@@ -77,12 +75,12 @@ struct AttendParams {
   int n_q_heads, n_heads, group;
   int tok_tile;      // positions of a row tile: 128 / group
   int n_ctas;
-  int64_t* begin;    // [2][n_ctas + 1] where the parts begin in each line
+  int64_t* begin;    // [n_ctas + 1] where the CTAs' parts begin
   int4* part_meta;   // [2][N * n_q_heads] RowItem of each row
   float* part_o;     // [2][N * n_q_heads][D]
   float2* part_ml;   // [2][N * n_q_heads]
-  float* slab_o;     // [n_ctas][2][256][D]
-  float2* slab_ml;   // [n_ctas][2][256]
+  float* slab_o;     // [n_ctas][256][D]
+  float2* slab_ml;   // [n_ctas][256]
 };
 
 // ---------------------------------------------------------------------------
@@ -101,27 +99,29 @@ __device__ __forceinline__ int block_tiles(const AttendParams& p, const SeqSpan&
   return last <= 0 ? 0 : static_cast<int>((last + kAtTile - 1) / kAtTile);
 }
 
-// Row tiles of the block: its weight per key tile.  A part's fixed cost
-// (queries, first scores, results) measured about three tiles', so an item
-// weighs three tiles more than it has, all on its first tile -- where the CTAs
-// have several tiles each (decode_b64: 84 us with it, 87 without); where they
-// have few, the tiles alone are dealt out, which uses more CTAs (candidates_d64:
-// 28 us against 31.5).
-__device__ __forceinline__ int block_weight(int positions, int tok_tile, int rb) {
+// Row tiles of a block.
+__device__ __forceinline__ int block_rows(int positions, int tok_tile, int rb) {
   return positions - rb * 2 * tok_tile > tok_tile ? 2 : 1;
 }
 
-__device__ __forceinline__ int64_t item_weight(int tiles, int w, int fixed) {
-  return tiles == 0 ? 0 : static_cast<int64_t>(tiles + fixed) * w;
+// Weights are in units of some 400 clocks: a key tile took 3,250 with two row
+// tiles and 2,000 with one.  A part's queries, first scores and results took
+// some 6,000: an item weighs that much more, all on its first tile, where the
+// CTAs have several tiles each; where they have few the tiles alone are dealt
+// out, which uses more CTAs (candidates_d64: 28 us against 31.5).
+__device__ __forceinline__ int tile_weight(int row_tiles) { return row_tiles == 2 ? 8 : 5; }
+__device__ __forceinline__ int fixed_weight(int64_t tiles_alone, int n_ctas) {
+  return tiles_alone < 30LL * n_ctas ? 0 : kAtFixed;
 }
-// The fixed cost that counts in a line whose tiles alone weigh W0.
-__device__ __forceinline__ int line_fixed(int64_t W0, int n_ctas) { return W0 < 6LL * n_ctas ? 0 : kAtFixed; }
+__device__ __forceinline__ int64_t item_weight(int tiles, int row_tiles, int fixed) {
+  return tiles == 0 ? 0 : static_cast<int64_t>(tiles) * tile_weight(row_tiles) + fixed;
+}
 
 // Weight of one key head's items of a sequence.
 __device__ __forceinline__ int64_t seq_head_weight(const AttendParams& p, const SeqSpan& s, int fixed) {
   int64_t w = 0;
   for (int rb = 0; rb * 2 * p.tok_tile < s.n; ++rb)
-    w += item_weight(block_tiles(p, s, rb), block_weight(s.n, p.tok_tile, rb), fixed);
+    w += item_weight(block_tiles(p, s, rb), block_rows(s.n, p.tok_tile, rb), fixed);
   return w;
 }
 
@@ -135,40 +135,49 @@ __device__ __noinline__ void no_tiles(const AttendParams& p, const SeqSpan& s) {
   }
 }
 
-struct PrefixLine {
-  int positions, blocks, tiles, fixed;
-  int64_t per_head, total;
+// The prefix's items: the same for each head.
+struct PrefixItems {
+  int positions, blocks, tiles;
+  int64_t tiles_alone;  // weight of one head's, without fixed cost
+  __device__ __forceinline__ int64_t per_head(int fixed) const {
+    return tiles == 0 ? 0 : tiles_alone + static_cast<int64_t>(blocks) * fixed;
+  }
 };
-__device__ __forceinline__ PrefixLine prefix_line(const AttendParams& p) {
-  PrefixLine L;
+__device__ __forceinline__ PrefixItems prefix_items(const AttendParams& p) {
+  PrefixItems L;
   L.positions = new_positions(p.batch);
   L.tiles = (p.prefix_len + kAtTile - 1) / kAtTile;
   L.blocks = (L.positions + 2 * p.tok_tile - 1) / (2 * p.tok_tile);
-  const int row_tiles = L.blocks > 0 ? 2 * (L.blocks - 1) + block_weight(L.positions, p.tok_tile, L.blocks - 1) : 0;
-  L.fixed = line_fixed(static_cast<int64_t>(L.tiles) * row_tiles * p.n_heads, p.n_ctas);
-  L.per_head = item_weight(L.tiles, row_tiles, L.fixed);
-  L.total = L.per_head * p.n_heads;
+  L.tiles_alone = L.blocks == 0 ? 0
+                                : static_cast<int64_t>(L.tiles) *
+                                      ((L.blocks - 1) * tile_weight(2) +
+                                       tile_weight(block_rows(L.positions, p.tok_tile, L.blocks - 1)));
   return L;
 }
 
-// Part c of n of a line of weight W begins at W * c / n; tiles belong to the
+// Part c of n of the line of weight W begins at W * c / n; tiles belong to the
 // part that their first unit of weight lies in.  (The 64-bit division takes
 // some hundred clocks, before the first load of a CTA.)
 __device__ __forceinline__ int64_t part_begin(int64_t W, int c, int n) {
   if (W < (1 << 24)) return static_cast<uint32_t>(W) * static_cast<uint32_t>(c) / static_cast<uint32_t>(n);  // n <= 160
   return W * c / n;
 }
-// Tile t of an item begins at its `off` (t = 0) or at off + (t + fixed) w.
-__device__ __forceinline__ int tiles_before(int64_t x, int64_t off, int w, int fixed, int tiles) {
+// Tile t of an item begins at its `off` (t = 0) or at off + fixed + t * weight:
+// the tiles that begin before x.
+__device__ __forceinline__ int tiles_before(int64_t x, int64_t off, int row_tiles, int fixed, int tiles) {
   if (x <= off || tiles == 0) return 0;
-  const int64_t t = (w == 2 ? (x - off + 1) >> 1 : x - off) - fixed;
-  return t < 1 ? 1 : t < tiles ? static_cast<int>(t) : tiles;
+  const int64_t y = x - off - fixed;
+  if (y <= 0) return 1;
+  if (y >= static_cast<int64_t>(tiles) * 8) return tiles;
+  const uint32_t z = static_cast<uint32_t>(y);
+  const int t = static_cast<int>(row_tiles == 2 ? (z + 7) / 8 : (z + 4) / 5);
+  return min(t, tiles);
 }
 
 // A part of an item, as the scheduler queues it.
 struct AtPart {
-  int64_t off;        // the item's place in its line
-  int tiles, w;       // all its key tiles, their weight
+  int64_t off;        // the item's place in the line
+  int tiles, w;       // all its key tiles, its row tiles
   int fixed;          // the fixed cost that counts in the line
   int last;           // for the part with the first tile: the last part that holds any
   int line;           // 0 prefix, 1 own pages, -1 no more
@@ -182,10 +191,10 @@ struct AtPart {
 
 // What the join needs of a row's item, written with the item's first tile:
 // x: the parts that hold its first and last tile, and the row's place in their
-// slabs (8 bits each), or -1: no tiles.  y: 8 * tiles + 2 * fixed + weight - 1.
-// z, w: the item's place in its line.
+// slabs (8 bits each), or -1: no tiles.  y: 4 * tiles, 2 where the fixed cost counts, row tiles - 1.
+// z, w: the item's place in the line.
 __device__ __forceinline__ int4 row_item(const AtPart& a, int part, int slab_row) {
-  return make_int4(part | a.last << 8 | slab_row << 16, 8 * a.tiles + 2 * a.fixed + a.w - 1, static_cast<int>(a.off),
+  return make_int4(part | a.last << 8 | slab_row << 16, 4 * a.tiles + (a.fixed > 0 ? 2 : 0) + a.w - 1, static_cast<int>(a.off),
                    static_cast<int>(a.off >> 32));
 }
 
@@ -245,7 +254,7 @@ struct AtShared {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], meet[2], done, scanned;
   float2 xch[2][kAtTile];  // the groups' (m, l)
   AtPart parts[kAtQueue];
-  int64_t warp_sum[kAtThreads / 32], warp_sum1[kAtThreads / 32], total, off;
+  int64_t warp_sum[kScanWarps], warp_sum1[kScanWarps], total, prefix, off;
   int seq, fixed;
   uint32_t tmem;
 };
@@ -298,7 +307,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
     sh.off = 0;
   }
   if (warp == 9) tmem_alloc(&sh.tmem, 512);
-  const int own_cta = p.n_ctas - 1 - cta;  // the own-pages line is mirrored, so that short lines meet on different CTAs
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -310,7 +318,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
     regs_down<kAtOtherRegs>();
     if (warp == 8) {
       // ---------------- scheduler (the whole warp): parts, and their queries ----------------
-      const PrefixLine pl = prefix_line(p);
+      const PrefixItems pl = prefix_items(p);
       int queued = 0;
       uint32_t q_loads[2] = {0, 0};
       bool ok = true;
@@ -344,30 +352,26 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         ++queued;
         return q;
       };
+      ok = __all_sync(0xffffffffu, mbar_wait(&sh.scanned, 0, status, kWaitLimitCycles));
+      AtPart a;
+      a.fixed = sh.fixed;
+      const int64_t total = sh.total, prefix = sh.prefix;
+      const int64_t lo = part_begin(total, cta, p.n_ctas), hi = part_begin(total, cta + 1, p.n_ctas);
+      if (ok && lane == 0) {
+        p.begin[cta] = lo;
+        if (cta == p.n_ctas - 1) p.begin[cta + 1] = hi;
+      }
 #pragma unroll 1
-      for (int turn = 0; turn < 2 && ok; ++turn) {
-        // the prefix's line is that of one sequence of all new positions
-        AtPart a;
-        a.line = (turn ^ cta) & 1;
-        if (a.line == 1) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&sh.scanned, 0, status, kWaitLimitCycles));
-          if (!ok) break;
-        }
-        a.fixed = a.line == 0 ? pl.fixed : sh.fixed;
-        const int64_t total = a.line == 0 ? pl.total : sh.total;
-        const int c = a.line == 0 ? cta : own_cta;
-        const int64_t lo = part_begin(total, c, p.n_ctas), hi = part_begin(total, c + 1, p.n_ctas);
-        if (lane == 0) {
-          int64_t* const begin = p.begin + a.line * (p.n_ctas + 1);
-          begin[c] = lo;
-          if (c == p.n_ctas - 1) begin[c + 1] = hi;
-        }
+      for (a.line = 0; a.line < 2 && ok; ++a.line) {
+        // the prefix is like one sequence of all new positions
+        if (a.line == 0 ? lo >= prefix : hi <= prefix) continue;
         int64_t off = a.line == 0 ? 0 : sh.off;
         a.seq = a.line == 0 ? 0 : sh.seq;
 #pragma unroll 1
-        for (; off < hi && lo < hi && ok; ++a.seq) {
+        for (; off < hi && lo < hi && a.seq < p.batch.B && ok; ++a.seq) {
+          if (a.line == 0 && a.seq > 0) break;
           SeqSpan s = {0, pl.positions, 0};
-          int64_t hw = pl.per_head;
+          int64_t hw = pl.per_head(a.fixed);
           if (a.line == 1) {
             s = seq_span(p.batch, a.seq);
             hw = seq_head_weight(p, s, a.fixed);
@@ -384,7 +388,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 #pragma unroll 1
             for (int at = 0; at < s.n && ok; at += 2 * p.tok_tile) {
               const int rb = at / (2 * p.tok_tile);
-              const int tiles = a.line == 0 ? pl.tiles : block_tiles(p, s, rb), w = block_weight(s.n, p.tok_tile, rb);
+              const int tiles = a.line == 0 ? pl.tiles : block_tiles(p, s, rb), w = block_rows(s.n, p.tok_tile, rb);
               a.off = off;
               a.tiles = tiles;
               a.w = w;
@@ -393,8 +397,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
               off += item_weight(tiles, w, a.fixed);
               if (a.t0 >= a.t1) continue;
               // the part that the item's last tile begins in
-              a.last = c;
-              if (a.t0 == 0 && a.t1 < tiles) a.last = static_cast<int>(((off - w + 1) * p.n_ctas - 1) / total);
+              a.last = cta;
+              if (a.t0 == 0 && a.t1 < tiles)
+                a.last = static_cast<int>(((off - tile_weight(w) + 1) * p.n_ctas - 1) / total);
               a.first = s.first + at;
               a.n0 = min(p.tok_tile, s.n - at);
               a.n1 = min(p.tok_tile, s.n - at - a.n0);
@@ -592,11 +597,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   } else {
     regs_up<kAtSoftmaxRegs>();
     // ---------------- softmax groups ----------------
-    // ---- first, beside the producer's start on the prefix: the own-pages line's
-    // weight, and where this CTA's part of it begins ----
+    // ---- first: the line's weight, and where this CTA's part of the own pages begins ----
     {
-      // the weight of the tiles alone and of an item's fixed tile go side by side
-      // until the first sum says which fixed cost counts
+      const PrefixItems pl = prefix_items(p);
+      const int64_t prefix0 = pl.tiles_alone * p.n_heads, prefix1 = pl.tiles > 0 ? static_cast<int64_t>(pl.blocks) * p.n_heads : 0;
+      int64_t prefix = 0, sum = 0;
+      // the weight of the tiles alone and the number of items go side by side
+      // until the whole sum says which fixed cost counts
       int64_t total = 0, total1 = 0;
       if (p.batch.B > kScanWarps * 32) {  // several chunks: their sums first
         int64_t w = 0, w1 = 0;
@@ -660,18 +667,20 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           total = before;
           total1 = before1;
         }
-        fixed = line_fixed(total, p.n_ctas);
-        const int64_t mine = one + fixed * one1, off = base + inc + fixed * (base1 + inc1) - mine;
-        const int64_t lo = part_begin(total + fixed * total1, own_cta, p.n_ctas);
-        if (b < p.batch.B && off <= lo && lo < off + mine) {
+        fixed = fixed_weight(prefix0 + total, p.n_ctas);
+        prefix = prefix0 + fixed * prefix1;
+        sum = prefix + total + fixed * total1;
+        const int64_t mine = one + fixed * one1, off = prefix + base + inc + fixed * (base1 + inc1) - mine;
+        const int64_t from = max(part_begin(sum, cta, p.n_ctas), prefix);
+        if (b < p.batch.B && off <= from && from < off + mine) {
           sh.seq = b;
           sh.off = off;
         }
         if (b0 + kScanWarps * 32 < p.batch.B) named_sync(1, kScanWarps * 32);
       }
-      total += fixed * total1;
       if (threadIdx.x == 0) {
-        sh.total = total;
+        sh.total = sum;
+        sh.prefix = prefix;
         sh.fixed = fixed;
       }
       __syncwarp();
@@ -833,7 +842,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         dst_ml = p.part_ml + row;
         dst_meta = p.part_meta + row;
       } else {
-        const int64_t row = (static_cast<int64_t>(cta) * 2 + a.line) * 256 + slab_row;
+        const int64_t row = static_cast<int64_t>(cta) * 256 + slab_row;
         dst_o = p.slab_o + row * D;
         dst_ml = p.slab_ml + row;
       }
@@ -891,7 +900,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         }
         if (mine_to_write && (two || g == 0)) {
           *dst_ml = make_float2(m, l);
-          if (a.t0 == 0) *dst_meta = row_item(a, a.line == 0 ? cta : own_cta, slab_row);
+          if (a.t0 == 0) *dst_meta = row_item(a, cta, slab_row);
         }
       }
       tc_fence_before();
@@ -911,7 +920,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------------------
-// join: one warp per row adds the row's parts.  Each line's first part says
+// join: one warp per row adds the row's parts.  Each item's first part says
 // where the others are, so a row whose items were not split takes one round of
 // loads.
 // ---------------------------------------------------------------------------
@@ -960,10 +969,10 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     if (item[line].x < 0) continue;
     add(ml[line], x[line]);
     const int first = item[line].x & 255, last = min(item[line].x >> 8 & 255, p.n_ctas - 1);
-    const int slab_row = item[line].x >> 16 & 255, tiles = item[line].y >> 3, w = 1 + (item[line].y & 1),
-              fixed = item[line].y >> 1 & 3;
+    const int slab_row = item[line].x >> 16 & 255, tiles = item[line].y >> 2, w = 1 + (item[line].y & 1),
+              fixed = item[line].y & 2 ? kAtFixed : 0;
     const int64_t off = static_cast<int64_t>(item[line].w) << 32 | static_cast<uint32_t>(item[line].z);
-    const int64_t* begin = p.begin + line * (p.n_ctas + 1);
+    const int64_t* const begin = p.begin;
     for (int c0 = first + 1; c0 <= last; c0 += 32) {
       // lane i: whether part c0 + i holds a tile's beginning
       const int c = c0 + lane;
@@ -980,7 +989,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
           if (parts == 0u) continue;
           const int part = c0 + __ffs(parts) - 1;
           parts &= parts - 1;
-          const int64_t at = (static_cast<int64_t>(line == 0 ? part : p.n_ctas - 1 - part) * 2 + line) * 256 + slab_row;
+          const int64_t at = static_cast<int64_t>(part) * 256 + slab_row;
           a[k] = p.slab_ml[at];
           load(p.slab_o + at * D + lane * kPer, v[k]);
         }

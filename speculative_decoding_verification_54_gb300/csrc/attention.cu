@@ -19,11 +19,11 @@ struct AttnLayout {
   size_t header, begin, part_meta, part_o, part_ml, slab_o, slab_ml, total;
 };
 
-// The parts of the rows (one place per row and line) and of the CTAs (one slab
-// per CTA and line): at most two row tiles each.
+// The parts of the rows (one place per row for the prefix, one for its own
+// pages) and of the CTAs (one slab each, two row tiles).
 AttnLayout attn_layout(int B, int N, int n_q_heads, int D) {
   AttnLayout L;
-  const size_t rows = 2 * static_cast<size_t>(N) * n_q_heads, slab_rows = size_t(kAtMaxCtas) * 2 * 2 * kAtTile;
+  const size_t rows = 2 * static_cast<size_t>(N) * n_q_heads, slab_rows = size_t(kAtMaxCtas) * 2 * kAtTile;
   size_t off = 0;
   auto take = [&off](size_t bytes) {
     const size_t at = off;
@@ -31,7 +31,7 @@ AttnLayout attn_layout(int B, int N, int n_q_heads, int D) {
     return at;
   };
   L.header = take(sizeof(WsHeader));
-  L.begin = take(2 * (size_t(kAtMaxCtas) + 1) * sizeof(int64_t));
+  L.begin = take((size_t(kAtMaxCtas) + 1) * sizeof(int64_t));
   L.part_meta = take(rows * sizeof(int4));
   L.part_o = take(rows * D * sizeof(float));
   L.part_ml = take(rows * sizeof(float2));
