@@ -55,7 +55,6 @@ constexpr int kAtThreads = 384;     // three warpgroups
 constexpr int kAtSoftmaxRegs = 216, kAtOtherRegs = 72;
 constexpr int kAtRingBytes = 160 * 1024;
 constexpr int kAtMaxCtas = 160;     // slabs in the workspace
-constexpr int kScanWarps = 8;       // the softmax warps add up the sequences' work
 constexpr int kAtQueue = 4;         // parts queued ahead
 constexpr int kAtFixed = 15;        // weight of a part's fixed cost
 constexpr float kAtRise = 8.f;      // log2 of the largest weight
@@ -117,11 +116,20 @@ __device__ __forceinline__ int64_t item_weight(int tiles, int row_tiles, int fix
   return tiles == 0 ? 0 : static_cast<int64_t>(tiles) * tile_weight(row_tiles) + fixed;
 }
 
-// Weight of one key head's items of a sequence.
-__device__ __forceinline__ int64_t seq_head_weight(const AttendParams& p, const SeqSpan& s, int fixed) {
-  int64_t w = 0;
-  for (int rb = 0; rb * 2 * p.tok_tile < s.n; ++rb)
-    w += item_weight(block_tiles(p, s, rb), block_rows(s.n, p.tok_tile, rb), fixed);
+// One key head's items of a sequence: the weight of their tiles alone, and how
+// many there are.
+struct SeqWeight {
+  int64_t tiles_alone;
+  int items;
+  __device__ __forceinline__ int64_t per_head(int fixed) const { return tiles_alone + static_cast<int64_t>(items) * fixed; }
+};
+__device__ __forceinline__ SeqWeight seq_weight(const AttendParams& p, const SeqSpan& s) {
+  SeqWeight w = {0, 0};
+  for (int rb = 0; rb * 2 * p.tok_tile < s.n; ++rb) {
+    const int tiles = block_tiles(p, s, rb);
+    w.tiles_alone += static_cast<int64_t>(tiles) * tile_weight(block_rows(s.n, p.tok_tile, rb));
+    w.items += tiles > 0;
+  }
   return w;
 }
 
@@ -233,10 +241,6 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-__device__ __forceinline__ void named_sync(int id, int nthreads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
 // 32-byte global store (eight fp32; the address 32-byte aligned)
 __device__ __forceinline__ void st_global_f8(float* q, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(q), "f"(v[0]), "f"(v[1]), "f"(v[2]),
@@ -251,11 +255,9 @@ __device__ __forceinline__ void st_global_f8(float* q, const float* v) {
 template <int kSlots>
 struct AtShared {
   uint64_t kv_full[kSlots], kv_empty[kSlots], part_full[kAtQueue], part_empty[kAtQueue];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], meet[2], done, scanned;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], meet[2], done;
   float2 xch[2][kAtTile];  // the groups' (m, l)
   AtPart parts[kAtQueue];
-  int64_t warp_sum[kScanWarps], warp_sum1[kScanWarps], total, prefix, off;
-  int seq, fixed;
   uint32_t tmem;
 };
 template <int D>
@@ -301,10 +303,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       mbar_init(&sh.meet[g], 8);
     }
     mbar_init(&sh.done, 1);
-    mbar_init(&sh.scanned, kScanWarps);
     fence_mbar_init();
-    sh.seq = p.batch.B;
-    sh.off = 0;
   }
   if (warp == 9) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
@@ -352,11 +351,54 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         ++queued;
         return q;
       };
-      ok = __all_sync(0xffffffffu, mbar_wait(&sh.scanned, 0, status, kWaitLimitCycles));
+      // the line: the weight of the tiles alone and the number of items side by
+      // side, until their sum says which fixed cost counts
       AtPart a;
-      a.fixed = sh.fixed;
-      const int64_t total = sh.total, prefix = sh.prefix;
+      SeqWeight first = {0, 0};  // of sequence `lane`
+      int64_t own = 0, own_items = 0;
+      for (int b = lane; b < p.batch.B; b += 32) {
+        const SeqSpan s = seq_span(p.batch, b);
+        const SeqWeight w = seq_weight(p, s);
+        if (b == lane) first = w;
+        own += w.tiles_alone * p.n_heads;
+        own_items += static_cast<int64_t>(w.items) * p.n_heads;
+        if (cta == 0 && s.kv < s.n) no_tiles(p, s);
+      }
+#pragma unroll
+      for (int x = 16; x; x >>= 1) {
+        own += __shfl_xor_sync(0xffffffffu, own, x);
+        own_items += __shfl_xor_sync(0xffffffffu, own_items, x);
+      }
+      a.fixed = fixed_weight(pl.tiles_alone * p.n_heads + own, p.n_ctas);
+      const int64_t prefix = pl.per_head(a.fixed) * p.n_heads, total = prefix + own + own_items * a.fixed;
       const int64_t lo = part_begin(total, cta, p.n_ctas), hi = part_begin(total, cta + 1, p.n_ctas);
+      // the sequence that this CTA's part of the own pages begins in
+      int own_seq = p.batch.B;
+      int64_t own_off = prefix;
+      if (lo < hi && hi > prefix) {
+        const int64_t from = max(lo, prefix);
+#pragma unroll 1
+        for (int b0 = 0; b0 < p.batch.B; b0 += 32) {
+          const int b = b0 + lane;
+          int64_t mine = 0;
+          if (b < p.batch.B)
+            mine = (b0 == 0 ? first : seq_weight(p, seq_span(p.batch, b))).per_head(a.fixed) * p.n_heads;
+          int64_t inc = mine;
+#pragma unroll
+          for (int x = 1; x < 32; x <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, inc, x);
+            if (lane >= x) inc += o;
+          }
+          const int64_t off = own_off + inc - mine;
+          const unsigned here = __ballot_sync(0xffffffffu, off <= from && from < off + mine);
+          if (here != 0u) {
+            own_seq = b0 + __ffs(here) - 1;
+            own_off = __shfl_sync(0xffffffffu, off, __ffs(here) - 1);
+            break;
+          }
+          own_off += __shfl_sync(0xffffffffu, inc, 31);
+        }
+      }
       if (ok && lane == 0) {
         p.begin[cta] = lo;
         if (cta == p.n_ctas - 1) p.begin[cta + 1] = hi;
@@ -365,8 +407,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       for (a.line = 0; a.line < 2 && ok; ++a.line) {
         // the prefix is like one sequence of all new positions
         if (a.line == 0 ? lo >= prefix : hi <= prefix) continue;
-        int64_t off = a.line == 0 ? 0 : sh.off;
-        a.seq = a.line == 0 ? 0 : sh.seq;
+        int64_t off = a.line == 0 ? 0 : own_off;
+        a.seq = a.line == 0 ? 0 : own_seq;
 #pragma unroll 1
         for (; off < hi && lo < hi && a.seq < p.batch.B && ok; ++a.seq) {
           if (a.line == 0 && a.seq > 0) break;
@@ -374,7 +416,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           int64_t hw = pl.per_head(a.fixed);
           if (a.line == 1) {
             s = seq_span(p.batch, a.seq);
-            hw = seq_head_weight(p, s, a.fixed);
+            hw = seq_weight(p, s).per_head(a.fixed);
           }
           a.len = a.line == 0 ? p.prefix_len : static_cast<int>(s.kv);
           a.old = a.line == 0 ? a.len : a.len - s.n;
@@ -597,95 +639,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   } else {
     regs_up<kAtSoftmaxRegs>();
     // ---------------- softmax groups ----------------
-    // ---- first: the line's weight, and where this CTA's part of the own pages begins ----
-    {
-      const PrefixItems pl = prefix_items(p);
-      const int64_t prefix0 = pl.tiles_alone * p.n_heads, prefix1 = pl.tiles > 0 ? static_cast<int64_t>(pl.blocks) * p.n_heads : 0;
-      int64_t prefix = 0, sum = 0;
-      // the weight of the tiles alone and the number of items go side by side
-      // until the whole sum says which fixed cost counts
-      int64_t total = 0, total1 = 0;
-      if (p.batch.B > kScanWarps * 32) {  // several chunks: their sums first
-        int64_t w = 0, w1 = 0;
-        for (int b = threadIdx.x; b < p.batch.B; b += kScanWarps * 32) {
-          const SeqSpan s = seq_span(p.batch, b);
-          const int64_t x = seq_head_weight(p, s, 0);
-          w += x * p.n_heads;
-          w1 += (seq_head_weight(p, s, 1) - x) * p.n_heads;
-        }
-        for (int x = 16; x; x >>= 1) {
-          w += __shfl_xor_sync(0xffffffffu, w, x);
-          w1 += __shfl_xor_sync(0xffffffffu, w1, x);
-        }
-        if (lane == 0) {
-          sh.warp_sum[warp] = w;
-          sh.warp_sum1[warp] = w1;
-        }
-        named_sync(1, kScanWarps * 32);
-        for (int i = 0; i < kScanWarps; ++i) {
-          total += sh.warp_sum[i];
-          total1 += sh.warp_sum1[i];
-        }
-        named_sync(1, kScanWarps * 32);
-      }
-      int64_t before = 0, before1 = 0;  // of the chunks before this one
-      int fixed = 0;
-      for (int b0 = 0; b0 < p.batch.B; b0 += kScanWarps * 32) {
-        const int b = b0 + threadIdx.x;
-        int64_t one = 0, one1 = 0;
-        if (b < p.batch.B) {
-          const SeqSpan s = seq_span(p.batch, b);
-          const int64_t x = seq_head_weight(p, s, 0);
-          one = x * p.n_heads;
-          one1 = (seq_head_weight(p, s, 1) - x) * p.n_heads;
-          if (cta == 0 && s.kv < s.n) no_tiles(p, s);
-        }
-        int64_t inc = one, inc1 = one1;
-        for (int x = 1; x < 32; x <<= 1) {
-          const int64_t o = __shfl_up_sync(0xffffffffu, inc, x), o1 = __shfl_up_sync(0xffffffffu, inc1, x);
-          if (lane >= x) {
-            inc += o;
-            inc1 += o1;
-          }
-        }
-        if (lane == 31) {
-          sh.warp_sum[warp] = inc;
-          sh.warp_sum1[warp] = inc1;
-        }
-        named_sync(1, kScanWarps * 32);
-        int64_t base = before, base1 = before1;
-        for (int i = 0; i < kScanWarps; ++i) {
-          const int64_t x = sh.warp_sum[i], x1 = sh.warp_sum1[i];
-          if (i < warp) {
-            base += x;
-            base1 += x1;
-          }
-          before += x;
-          before1 += x1;
-        }
-        if (p.batch.B <= kScanWarps * 32) {
-          total = before;
-          total1 = before1;
-        }
-        fixed = fixed_weight(prefix0 + total, p.n_ctas);
-        prefix = prefix0 + fixed * prefix1;
-        sum = prefix + total + fixed * total1;
-        const int64_t mine = one + fixed * one1, off = prefix + base + inc + fixed * (base1 + inc1) - mine;
-        const int64_t from = max(part_begin(sum, cta, p.n_ctas), prefix);
-        if (b < p.batch.B && off <= from && from < off + mine) {
-          sh.seq = b;
-          sh.off = off;
-        }
-        if (b0 + kScanWarps * 32 < p.batch.B) named_sync(1, kScanWarps * 32);
-      }
-      if (threadIdx.x == 0) {
-        sh.total = sum;
-        sh.prefix = prefix;
-        sh.fixed = fixed;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.scanned);
-    }
     const int g = warp >> 2, quad = warp & 3, r = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const int row_tok = r / p.group, row_head = r % p.group;
