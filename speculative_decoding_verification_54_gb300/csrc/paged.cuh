@@ -27,6 +27,9 @@ struct PagedBatch {
   int* status;
 };
 
+// entries of a sequence: key tiles past them still count in 32 bits
+constexpr int64_t kMaxEntries = 0x7fffffff - 255;
+
 // Sequence b's rows and lengths, with every value that the host cannot check
 // clamped into its range (the status word records that).
 struct SeqSpan {
@@ -40,6 +43,7 @@ __device__ __forceinline__ SeqSpan seq_span(const PagedBatch& p, int b) {
   s.first = min(max(a, 0), p.N);
   s.n = min(max(e, s.first), p.N) - s.first;
   s.kv = min(static_cast<int64_t>(max(kv, 0)), static_cast<int64_t>(p.table_width) * p.page_size);
+  s.kv = min(s.kv, kMaxEntries);
   if (s.first != a || s.first + s.n != e || s.kv != kv || s.kv < s.n) atomicOr(p.status, kStatusBadCache);
   return s;
 }

@@ -382,3 +382,55 @@ def test_pages_and_lengths_out_of_range_are_reported(sv):
         out, _, _ = _attend(sv, pr, ws=ws)
         assert sv.spec_verify_status(ws) == sv.SPEC_ERR_DEVICE_INPUT
         assert torch.equal(out[:2], good[:2])
+
+
+LARGE = [
+    # dtype, D, Hk, Hq, page, B, q_len, prefix, most own entries, mask: many tiles
+    # and parts on every CTA, so that rings, queues and slots go round
+    ("bf16", 128, 8, 32, 64, 24, 8, 8192, 700, False),
+    ("bf16", 128, 4, 8, 16, 96, 5, 1500, 2500, False),
+    ("fp16", 64, 16, 16, 32, 64, 1, 4000, 300, False),
+    ("fp16", 64, 4, 28, 24, 40, 12, 3001, 900, True),
+    ("bf16", 128, 8, 16, 16, 3, 700, 2050, 1400, False),
+]
+
+
+@pytest.mark.parametrize("dtype,D,Hk,Hq,page,B,q_len,prefix,most,mask", LARGE)
+def test_attention_large(sv, dtype, D, Hk, Hq, page, B, q_len, prefix, most, mask):
+    """Against float64 on the GPU, head by head; the tolerance is
+    _check_attend's with the row's largest sums in place of each row's own."""
+    import torch
+    rng = np.random.default_rng(71)
+    q_lens = rng.integers(1, q_len + 1, B).tolist()
+    kv_lens = [int(rng.integers(n, most + 1)) for n in q_lens]
+    pr = Problem(72, dtype, D, Hk, Hq, page, q_lens, kv_lens, prefix)
+    words = _random_mask(rng, q_lens, pr.N) if mask else None
+    ws = sv.make_attention_workspace(B, pr.N, Hq, D)
+    for _ in range(3):
+        out, lse, _ = _attend(sv, pr, words, ws=ws)
+    assert sv.spec_verify_status(ws) == sv.SPEC_OK
+    u = torch.finfo(pr.q.dtype).eps / 2
+    flat = [p.reshape(-1, Hk, D) if p.is_contiguous() else p.contiguous().reshape(-1, Hk, D) for p in pr.pools]
+    shared = [int(pr.ptable_np[t // page]) * page + t % page for t in range(prefix)]
+    for b, (n, kv) in enumerate(zip(q_lens, kv_lens)):
+        rows = torch.tensor(shared + [int(pr.table_np[b, t // page]) * page + t % page for t in range(kv)], device="cuda")
+        K, V = (x[rows].double().permute(1, 0, 2) for x in flat)                      # [Hk, keys, D]
+        a = int(pr.indptr_np[b])
+        q = pr.q[a:a + n].double().reshape(n, Hk, Hq // Hk, D).permute(1, 2, 0, 3)     # [Hk, group, n, D]
+        new = torch.tensor([[paged.sees(i, j, None if words is None else words[a + i]) for j in range(n)]
+                            for i in range(n)], device="cuda")
+        s = torch.einsum("hgnd,hkd->hgnk", q, K) * D ** -0.5
+        s[..., prefix + kv - n:] = s[..., prefix + kv - n:].masked_fill(~new, -float("inf"))
+        want_lse = torch.logsumexp(s, dim=-1)
+        w = torch.exp(s - want_lse[..., None])
+        want = torch.einsum("hgnk,hkd->hgnd", w, V)
+        absv = torch.einsum("hgnk,hkd->hgnd", w, V.abs())
+        es = D * 2.0 ** -23 * float((torch.einsum("hgnd,hkd->hgnk", q.abs(), K.abs()) * D ** -0.5).max())
+        keys = prefix + kv
+        tol = (u + 2 * es + 2.0 ** -20 + keys * 2.0 ** -23) * absv + u * want.abs() \
+            + keys * 2.0 ** -25 * float(V.abs().max()) + 2.0 ** -25
+        got = out[a:a + n].double().reshape(n, Hk, Hq // Hk, D).permute(1, 2, 0, 3)
+        assert bool(((got - want).abs() <= tol).all()), (b, float(((got - want).abs() - tol).max()))
+        got_lse = lse[a:a + n].double().reshape(n, Hk, Hq // Hk).permute(1, 2, 0)
+        ltol = es + keys * 2.0 ** -23 + 2.0 ** -20 + want_lse.abs() * 2.0 ** -22
+        assert bool(((got_lse - want_lse).abs() <= ltol).all()), b
