@@ -37,6 +37,19 @@
 // The reference m of a row rises only when a tile's maximum passes it by more
 // than 2^8, and only then is O (in TMEM) multiplied; weights stay below 256, l
 // and O are exact with respect to any m.
+//
+// What bounds it.  Own pages: HBM (16 caches of up to 32,768 entries, 944 MB:
+// 150 us, 6.3 TB/s, 0.93 of the measured copy bandwidth).  Prefix: the chain of
+// a key tile, scores -> weights (some 1,700 clocks: 128 columns from TMEM, their
+// maximum, 128 exponentials at 8 a clock per SM quarter, the stores) -> O and the
+// next scores (1,024 clocks of products).  P takes the place of S, so a group's
+// chain is serial; the two groups overlap and take 3,250 clocks a tile where
+// the products alone take 2,048 (B = 128, prefix 32,768: 357 us, 1.0 PFLOP/s of
+// the pairs that exist).  Tried and not kept: 64-key steps with two score
+// buffers (scores of 64 keys cost 48 clocks an instruction against 64 for 128:
+// 474 us then against 435), halves of a row in two threads (701), the first 64
+// keys' weights announced early (no change), an issuer per group (432: products
+// of both groups interleave and each group's finish later).
 #pragma once
 
 #include <type_traits>
@@ -262,6 +275,7 @@ struct AtShared {
 };
 template <int D>
 constexpr int kAtSlots = kAtRingBytes / (kAtTile * D * 2);
+static_assert(kAtSlots<128> >= 5 && kAtSlots<64> >= 5, "the loaders' waits count on it");
 template <int D>
 constexpr uint32_t at_smem_bytes() {
   return 2u * kAtTile * D * 2 + kAtRingBytes + sizeof(AtShared<kAtSlots<D>>);
@@ -619,6 +633,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
             page = p.n_pages;
           }
           const int at_slot = static_cast<int>(key % page_size);
+          // (A wait tells neighbouring phases apart: the slot's occupant before
+          // the last one is free, since the tile that this warp loaded before,
+          // at most three places back, came after a later one was.)
           if (use > 0)
             ok = __all_sync(0xffffffffu, mbar_wait(&sh.kv_empty[slot], (use & 1) ^ 1, status, kWaitLimitCycles));
           if (!ok) break;
