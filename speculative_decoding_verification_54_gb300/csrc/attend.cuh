@@ -96,7 +96,7 @@ struct AttendParams {
 };
 
 // ---------------------------------------------------------------------------
-// the two lines of work
+// the line of work
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int new_positions(const PagedBatch& p) {
   return min(max(p.q_indptr[p.B], 0), p.N);
