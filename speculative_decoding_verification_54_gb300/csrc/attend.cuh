@@ -816,9 +816,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         dst_o = p.slab_o + row * D;
         dst_ml = p.slab_ml + row;
       }
-      // Every phase of both groups' barriers is waited for by both groups (a
-      // wait tells neighbouring phases apart, not farther ones); with two row
-      // tiles the other group's only after this group's results are out.
+      // With one row tile a group waits for both groups' products, with two for
+      // its own: the other's phase is only counted.  (A wait there could come two
+      // phases late and never end: group 0 needs nothing of group 1 for a next
+      // part of one tile, and completes its phase again.)  A wait tells
+      // neighbouring phases apart, and no phase before the one waited for is open:
+      // products complete in the order in which one thread issued them, and
+      // this group's of the last part or of this one came after them.
       ok = products_done(two ? g : 0);
       if (!two && tiles > 1) ok = products_done(1) && ok;
       if (!ok) break;
@@ -875,7 +879,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       }
       tc_fence_before();
       if (two) {
-        ok = products_done(g ^ 1);
+        ph_o[g ^ 1] ^= 1;
       } else {  // O and the exchanged values are free again once all have read them
         ok = meet_all(1);
         ph_meet ^= 1;

@@ -434,3 +434,31 @@ def test_attention_large(sv, dtype, D, Hk, Hq, page, B, q_len, prefix, most, mas
         got_lse = lse[a:a + n].double().reshape(n, Hk, Hq // Hk).permute(1, 2, 0)
         ltol = es + keys * 2.0 ** -23 + 2.0 ** -20 + want_lse.abs() * 2.0 ** -22
         assert bool(((got_lse - want_lse).abs() <= ltol).all()), b
+
+
+# dtype, D, Hk, Hq, page, q_len, kv_len, prefix: parts of one key tile, with one row tile or two, one after the other
+SHORT_PARTS = [
+    ("bf16", 128, 8, 16, 16, 128, 128, 0),
+    ("bf16", 128, 8, 16, 16, 100, 128, 0),
+    ("fp16", 64, 8, 16, 32, 128, 128, 0),
+    ("bf16", 128, 4, 8, 64, 200, 250, 300),
+]
+
+
+@pytest.mark.parametrize("dtype,D,Hk,Hq,page,q_len,kv_len,prefix", SHORT_PARTS)
+def test_attention_parts_of_one_tile_in_a_row(sv, dtype, D, Hk, Hq, page, q_len, kv_len, prefix):
+    """Many passes without a pause: no wait of the kernel may run out, and every
+    pass gives the same bits."""
+    import torch
+    B = 64
+    pr = Problem(81, dtype, D, Hk, Hq, page, [q_len] * B, [kv_len] * B, prefix)
+    ws = sv.make_attention_workspace(B, pr.N, Hq, D)
+    out, lse, _ = _attend(sv, pr, ws=ws)
+    first, first_lse = out.clone(), lse.clone()
+    other = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(400):
+        _attend(sv, pr, ws=ws, out=out, lse=lse)
+        other += (out != first).sum() + (lse != first_lse).sum()
+    torch.cuda.synchronize()
+    assert sv.spec_verify_status(ws) == sv.SPEC_OK
+    assert int(other) == 0
