@@ -18,19 +18,24 @@
 // sines of those positions into shared memory, once for all heads; then each
 // thread owns two 16-byte vectors of every head it visits, the two that turn
 // together where pairs are (f, f + rot/2), so that it reads its 8 pairs'
-// cosines once per position and every vector once, and streams the heads.
-// Bound by the copies: q, k, v read once, written once.
+// cosines from shared memory and every vector once.  The tile's (position,
+// head) pairs are one sequence, dealt out in turn: heads that do not fill the
+// threads leave none idle (28 + 8 heads of 128, 5,534 positions: 24.0 us against
+// 29.4 position by position).  Bound by the copies: q, k, v read once, written
+// once (32,768 positions of 256 dims: 188 us, 5.7 TB/s, 0.84 of the measured
+// copy bandwidth).
 #pragma once
 
 #include "paged.cuh"
 
 namespace specv {
 
-// 256 threads, three CTAs an SM, two heads a thread in flight: 203 us on 32,768
-// positions of 256 dims; four heads 218, four CTAs 215, two CTAs with four heads 254.
+// 256 threads, three CTAs an SM, three heads a thread in flight.  On 32,768
+// positions of 256 dims and on 5,534 of 128: two heads 188.2 and 24.6 us, three
+// 188.2 and 24.0, four 190.9 and 24.3.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendMaxTile = 24;   // positions a CTA takes, at most
-constexpr int kAppendBatch = 2;     // heads a thread has in flight
+constexpr int kAppendBatch = 3;      // heads a thread has in flight
 constexpr int kAppendSms = 152;      // GB300's; the tile size goes by it
 
 struct AppendParams {
@@ -84,6 +89,14 @@ __device__ __forceinline__ float2 unit_of(int64_t position, uint64_t turn64) {
   float2 cs;
   sincospif(x, &cs.y, &cs.x);
   return cs;
+}
+
+// Where angle f stands in a position's table.  A thread reads the 8 angles of
+// a vector, its neighbour the next 8: [angle in its vector][vector] puts a
+// warp's reads side by side, in all banks (188 us against 228 in order of f, where
+// neighbours stand 64 bytes apart).
+__device__ __forceinline__ int unit_index(int f, int half) {
+  return (half & 7) == 0 ? (f & 7) * (half >> 3) + (f >> 3) : f;
 }
 
 // a 16-byte vector that is read once: past L1
@@ -210,7 +223,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const __gr
         const int64_t pos = p.positions != nullptr
                                 ? static_cast<int64_t>(p.positions[static_cast<int64_t>(a) * p.batch.N + n0 + t])
                                 : p.position_base + s_entry[t];
-        ap_units[t * p.half + f] = unit_of(pos, turn64);
+        ap_units[t * p.half + unit_index(f, p.half)] = unit_of(pos, turn64);
       }
     }
     __syncthreads();
@@ -228,58 +241,68 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const __gr
   const int v1 = paired ? u + hv : v0 + 1;
   const bool two = v1 < vpr;
   const int d0 = 8 * v0, d1 = 8 * v1;
-  for (int t = 0; t < tile; ++t) {
-    if (!s_live[t]) continue;
-    const int64_t n = n0 + t, dst0 = s_dst[t];
-    const float2* cs = ap_units + t * p.half;
-    // a pair of vectors turns by its 8 angles; neighbours have 4 each
-    float c[8], s[8];
-    if (paired || (kInterleaved && d0 < rot)) {
+  // the tile's (position, row) pairs in one sequence: no thread waits for a
+  // position's last rows where their count is no multiple of rpi
+  const int t_step = rpi / rows, row_step = rpi - t_step * rows;
+  int t_at = r0 / rows, row_at = r0 - t_at * rows;
+  while (t_at < tile) {
+    uint4 a[kAppendBatch], b[kAppendBatch];
+    int ts[kAppendBatch], rs[kAppendBatch];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int f = kInterleaved ? (d0 >> 1) + e : d0 + e;
-        const float2 x = f < p.half ? cs[f] : make_float2(1.f, 0.f);
-        c[e] = x.x;
-        s[e] = x.y;
-      }
-    }
-    for (int row0 = r0; row0 < rows; row0 += kAppendBatch * rpi) {
-      uint4 a[kAppendBatch], b[kAppendBatch];
-#pragma unroll
-      for (int i = 0; i < kAppendBatch; ++i) {
-        const int row = row0 + i * rpi;
-        if (row >= rows) continue;
-        const uint16_t* src = p.row_src(n, row);
+    for (int i = 0; i < kAppendBatch; ++i) {
+      ts[i] = t_at < tile && s_live[t_at] ? t_at : -1;
+      rs[i] = row_at;
+      if (ts[i] >= 0) {
+        const uint16_t* src = p.row_src(n0 + t_at, row_at);
         a[i] = ld_once(src + d0);
         if (two) b[i] = ld_once(src + d1);
       }
+      t_at += t_step;
+      row_at += row_step;
+      if (row_at >= rows) {
+        row_at -= rows;
+        ++t_at;
+      }
+    }
 #pragma unroll
-      for (int i = 0; i < kAppendBatch; ++i) {
-        const int row = row0 + i * rpi;
-        if (row >= rows) continue;
-        uint4 x = a[i], y = b[i];
-        if (row < Hq + Hk) {
-          if (paired) {
-            turn_pair<T>(x, y, c, s);
-          } else if (kInterleaved) {
-            if (d0 < rot) turn_neighbours<T>(x, c, s, rot - d0);
-            if (two && d1 < rot) turn_neighbours<T>(y, c + 4, s + 4, rot - d1);
-          } else if (d0 < rot && (p.half & 7) != 0) {
-            turn_scattered<T>(x, p.row_src(n, row), cs, d0, p.half);
-            if (two) turn_scattered<T>(y, p.row_src(n, row), cs, d1, p.half);
+    for (int i = 0; i < kAppendBatch; ++i) {
+      if (ts[i] < 0) continue;
+      const int row = rs[i];
+      const int64_t n = n0 + ts[i], dst0 = s_dst[ts[i]];
+      const float2* cs = ap_units + ts[i] * p.half;
+      uint4 x = a[i], y = b[i];
+      if (row < Hq + Hk) {
+        // a pair of vectors turns by its 8 angles; neighbours have 4 each
+        float c[8], s[8];
+        if (paired || (kInterleaved && d0 < rot)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int f = kInterleaved ? (d0 >> 1) + e : d0 + e;
+            const float2 w = f < p.half ? cs[unit_index(f, p.half)] : make_float2(1.f, 0.f);
+            c[e] = w.x;
+            s[e] = w.y;
           }
         }
-        uint16_t* dst;
-        if (row < Hq) {
-          dst = p.q_out + (n * Hq + row) * p.D;
-        } else {
-          if (dst0 < 0) continue;
-          const bool is_k = row < Hq + Hk;
-          dst = (is_k ? p.cache.k : p.cache.v) + dst0 + (row - Hq - (is_k ? 0 : Hk)) * p.cache.head_stride;
+        if (paired) {
+          turn_pair<T>(x, y, c, s);
+        } else if (kInterleaved) {
+          if (d0 < rot) turn_neighbours<T>(x, c, s, rot - d0);
+          if (two && d1 < rot) turn_neighbours<T>(y, c + 4, s + 4, rot - d1);
+        } else if (d0 < rot && (p.half & 7) != 0) {
+          turn_scattered<T>(x, p.row_src(n, row), cs, d0, p.half);
+          if (two) turn_scattered<T>(y, p.row_src(n, row), cs, d1, p.half);
         }
-        *reinterpret_cast<uint4*>(dst + d0) = x;
-        if (two) *reinterpret_cast<uint4*>(dst + d1) = y;
       }
+      uint16_t* dst;
+      if (row < Hq) {
+        dst = p.q_out + (n * Hq + row) * p.D;
+      } else {
+        if (dst0 < 0) continue;
+        const bool is_k = row < Hq + Hk;
+        dst = (is_k ? p.cache.k : p.cache.v) + dst0 + (row - Hq - (is_k ? 0 : Hk)) * p.cache.head_stride;
+      }
+      *reinterpret_cast<uint4*>(dst + d0) = x;
+      if (two) *reinterpret_cast<uint4*>(dst + d1) = y;
     }
   }
 }
