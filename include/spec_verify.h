@@ -479,8 +479,9 @@ int spec_kv_append(const spec_kv_cache *cache, const void *q, int64_t q_pos_stri
  *   one pass; a position sees itself only if its own bit is set, and new
  *   positions from the 65th on are seen by none).
  * Query head h reads key head h / (n_q_heads / n_heads).  A position that sees
- * nothing gives out 0 and lse -inf.  The prefix's keys and values are read
- * once for the whole batch, not once a sequence.
+ * nothing gives out 0 and lse -inf; one that sees a score of NaN or +inf gives
+ * NaN in both.  The prefix's keys and values are read once for the whole batch,
+ * not once a sequence.
  *
  *   q, out  [N, n_q_heads, D], strides in elements, multiples of 16 bytes
  *

@@ -36,7 +36,9 @@
 //
 // The reference m of a row rises only when a tile's maximum passes it by more
 // than 2^8, and only then is O (in TMEM) multiplied; weights stay below 256, l
-// and O are exact with respect to any m.
+// and O are exact with respect to any m.  A NaN score raises no maximum (m may
+// stay -inf) but makes l and O NaN, and so does an infinite one (inf - inf):
+// l, not m, tells a row that saw nothing, by l = 0.
 //
 // What bounds it.  Own pages: HBM (16 caches of up to 32,768 entries, 944 MB:
 // 150 us, 6.3 TB/s, 0.93 of the measured copy bandwidth).  Prefix: the chain of
@@ -930,7 +932,9 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 
   float o[kPer] = {}, m = -INFINITY, l = 0.f;
   auto add = [&](const float2& a, const float (&v)[kPer]) {
-    if (a.x == -INFINITY) return;  // nothing seen: its O is not looked at
+    // Nothing seen: a.y is 0, its O is not looked at.  (A part whose every score
+    // is NaN has a.x = -inf too, but a.y NaN, which reaches l and o.)
+    if (a.y == 0.f) return;
     const float mm = fmaxf(m, a.x);
     const float fo = m == -INFINITY ? 0.f : ex2(m - mm), fx = ex2(a.x - mm);
     m = mm;
@@ -972,14 +976,14 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
       }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // l: 0 where nothing was seen, else at least 1, or NaN
   uint16_t* dst = p.out + n * p.o_ps + hq * p.o_hs + lane * kPer;
   if (kPer == 4)
     *reinterpret_cast<uint2*>(dst) =
         make_uint2(Pack16<T>::pack(o[0] * inv, o[1] * inv), Pack16<T>::pack(o[kPer - 2] * inv, o[kPer - 1] * inv));
   else
     *reinterpret_cast<uint32_t*>(dst) = Pack16<T>::pack(o[0] * inv, o[1] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+  if (lane == 0 && p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
 }
 
 }  // namespace specv
