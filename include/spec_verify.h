@@ -411,9 +411,11 @@ int spec_round_update(spec_round_state *states, const int32_t *num_accepted, int
  *   workspace    spec_attention_workspace_bytes() bytes, 256-byte aligned,
  *                zeroed once; calls that share one must not overlap
  * Every length and table is read on the device, so a captured graph serves
- * rounds of other lengths.  A length outside its range is clamped, and a page
- * outside [0, n_pages) is neither read (its keys read as zero) nor written;
- * either makes spec_verify_status return SPEC_ERR_DEVICE_INPUT.
+ * rounds of other lengths.  What is outside its range makes spec_verify_status
+ * return SPEC_ERR_DEVICE_INPUT: a page outside [0, n_pages) is neither read (its
+ * keys read as zero) nor written; the attention clamps a length to its range;
+ * the append writes the new entries that have a place in the table (kv_len[b] -
+ * q_len[b] + i in [0, table_width * page_size)) where they belong, and no others.
  * ---------------------------------------------------------------------------
  */
 typedef struct {

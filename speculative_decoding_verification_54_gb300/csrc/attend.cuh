@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 #pragma unroll 1
         for (; off < hi && lo < hi && a.seq < p.batch.B && ok; ++a.seq) {
           if (a.line == 0 && a.seq > 0) break;
-          SeqSpan s = {0, pl.positions, 0};
+          SeqSpan s = {0, pl.positions, 0, 0};
           int64_t hw = pl.per_head(a.fixed);
           if (a.line == 1) {
             s = seq_span(p.batch, a.seq);

@@ -191,9 +191,12 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const __gr
       if (b >= 0) {
         const SeqSpan s = seq_span(p.batch, b);
         live = n >= s.first && n < s.first + s.n;  // not so only where q_indptr is not ascending
-        entry = s.kv - s.n + (n - s.first);
+        // The entry by the lengths as they are, not as seq_span clamps them: a
+        // length past the table must not move the new entries over older ones.
+        // What has no place in the table is not written.
+        entry = n + s.shift;
         int page = -1;
-        if (live && entry >= 0)
+        if (live && entry >= 0 && entry < static_cast<int64_t>(p.batch.table_width) * p.batch.page_size)
           page = p.batch.block_table[static_cast<int64_t>(b) * p.batch.table_width + entry / p.batch.page_size];
         if (page >= 0 && page < p.cache.n_pages)
           dst = page * p.cache.page_stride + (entry % p.batch.page_size) * p.cache.slot_stride;

@@ -35,6 +35,7 @@ constexpr int64_t kMaxEntries = 0x7fffffff - 255;
 struct SeqSpan {
   int first, n;  // rows first .. first + n - 1 of the new positions
   int64_t kv;    // entries of its own pages, the new ones among them
+  int64_t shift; // new position n is entry n + shift, by the lengths as given: not clamped
 };
 
 __device__ __forceinline__ SeqSpan seq_span(const PagedBatch& p, int b) {
@@ -44,6 +45,7 @@ __device__ __forceinline__ SeqSpan seq_span(const PagedBatch& p, int b) {
   s.n = min(max(e, s.first), p.N) - s.first;
   s.kv = min(static_cast<int64_t>(max(kv, 0)), static_cast<int64_t>(p.table_width) * p.page_size);
   s.kv = min(s.kv, kMaxEntries);
+  s.shift = static_cast<int64_t>(kv) - e;
   if (s.first != a || s.first + s.n != e || s.kv != kv || s.kv < s.n) atomicOr(p.status, kStatusBadCache);
   return s;
 }
