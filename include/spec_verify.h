@@ -398,8 +398,8 @@ int spec_round_update(spec_round_state *states, const int32_t *num_accepted, int
  *   cache        HOST struct, below: the pools of key and value pages
  *   q_indptr     int32 [B+1]: the new positions of sequence b are rows
  *                q_indptr[b] .. q_indptr[b+1]-1 of the [N, ...] tensors
- *                (non-decreasing from 0; rows from q_indptr[B] to N are padding
- *                and are neither read nor written)
+ *                (non-decreasing from 0, else SPEC_ERR_DEVICE_INPUT; rows from
+ *                q_indptr[B] to N are padding and are neither read nor written)
  *   block_table  int32 [B, table_width]: the pages of sequence b in order;
  *                entry i sits in slot i % page_size of page
  *                block_table[b, i / page_size].  Entries of pages that the

@@ -928,7 +928,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     ml[line] = p.part_ml[line * rows + row];
     load(p.part_o + (line * rows + row) * D + lane * kPer, x[line]);
   }
-  if (n >= new_positions(p.batch)) return;  // padding
+  if (!in_batch(p.batch, n)) return;  // padding, or (reported) before the first sequence: nothing was left for it
 
   float o[kPer] = {}, m = -INFINITY, l = 0.f;
   auto add = [&](const float2& a, const float (&v)[kPer]) {

@@ -181,6 +181,16 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const __gr
   grid_dep_launch();
   grid_dep_wait();
 
+  // Row offsets that do not begin at 0 or do not ascend: the search below takes
+  // them as they are and may not come across them.  (The last warps first: they
+  // are the ones without a position to look up.)
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAppendThreads + kAppendThreads - 1 - tid; i < p.batch.B;
+       i += static_cast<int64_t>(gridDim.x) * kAppendThreads) {
+    const int b = static_cast<int>(i), at = p.batch.q_indptr[b];
+    if (at > p.batch.q_indptr[b + 1] || (b == 0 && at != 0) || (b == p.batch.B - 1 && p.batch.q_indptr[b + 1] > p.batch.N))
+      atomicOr(p.batch.status, kStatusBadCache);
+  }
+
   // ---- the entries of the tile's positions ----
   for (int t = warp; t < tile; t += kAppendThreads / 32) {
     const int n = n0 + t;

@@ -46,8 +46,14 @@ __device__ __forceinline__ SeqSpan seq_span(const PagedBatch& p, int b) {
   s.kv = min(static_cast<int64_t>(max(kv, 0)), static_cast<int64_t>(p.table_width) * p.page_size);
   s.kv = min(s.kv, kMaxEntries);
   s.shift = static_cast<int64_t>(kv) - e;
-  if (s.first != a || s.first + s.n != e || s.kv != kv || s.kv < s.n) atomicOr(p.status, kStatusBadCache);
+  if (s.first != a || s.first + s.n != e || s.kv != kv || s.kv < s.n || (b == 0 && a != 0))
+    atomicOr(p.status, kStatusBadCache);
   return s;
+}
+
+// The rows that belong to a sequence: from the first one's to the last one's.
+__device__ __forceinline__ bool in_batch(const PagedBatch& p, int n) {
+  return n >= p.q_indptr[0] && n < p.q_indptr[p.B];
 }
 
 // The sequence whose rows hold `n`, found by a whole warp in steps of 32 (two
