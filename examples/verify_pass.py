@@ -133,10 +133,11 @@ def generate(model, prefix, prompts, new_tokens, gamma, seed=0):
             sv.spec_round_update(states, accepted, gamma, gamma)
         for b in range(B):
             done[b] += out[b, :accepted[b] + 1].tolist()
-        # a finished sequence keeps its cache from growing past its pages
+        # a pass appends up to entry prompt + len(done) + gamma, and the pages hold
+        # max_len: a finished sequence drops what it has beyond new_tokens + 1
         for b, s in enumerate(states):
-            if len(done[b]) > new_tokens + gamma + 1:
-                extra = len(done[b]) - (new_tokens + 1)
+            extra = len(done[b]) - (new_tokens + 1)
+            if extra > 0:
                 del done[b][new_tokens + 1:]
                 s.seq_len -= extra
                 s.kv_len -= extra
