@@ -476,7 +476,7 @@ def _positions_first(name, cache, *tensors):
 
 def _batch_checks(name, q_indptr, block_table, kv_len):
     import torch
-    B = kv_len.shape[0]
+    B = kv_len.numel()
     for t, shape in ((q_indptr, (B + 1,)), (kv_len, (B,)), (block_table, (B, block_table.shape[-1]))):
         if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
             raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous "
@@ -484,10 +484,11 @@ def _batch_checks(name, q_indptr, block_table, kv_len):
     return B
 
 
-def _on_gpu(name, *tensors):
+def _refuse_off_gpu(name, *tensors):
     for t in tensors:
         if t is not None and not t.is_cuda:
             raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: a tensor of {tuple(t.shape)} is not on the GPU")
+    raise SpecVerifyError(SPEC_ERR_INVALID_ARG, name)
 
 
 def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspace, inv_freq=None, positions=None,
@@ -510,13 +511,11 @@ def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspa
             and q_indptr.dtype is i32 and kv_len.dtype is i32 and block_table.dtype is i32
             and kv_len.dim() == 1 and q_indptr.shape == (kv_len.shape[0] + 1,)
             and block_table.dim() == 2 and block_table.shape[0] == kv_len.shape[0]
-            and q_indptr.is_contiguous() and kv_len.is_contiguous() and block_table.is_contiguous()
-            and q.is_cuda and k.is_cuda and v.is_cuda and q_out.is_cuda and q_indptr.is_cuda and kv_len.is_cuda
-            and block_table.is_cuda and workspace.is_cuda and device is not None):
-        _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspace)
+            and q_indptr.is_contiguous() and kv_len.is_contiguous() and block_table.is_contiguous()):
+        _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len)
     q_stride, k_stride, v_stride = q.stride(), k.stride(), v.stride()
     if q_stride[2] != 1 or k_stride[2] != 1 or v_stride[2] != 1:
-        _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspace)
+        _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len)
     n_axes, rot, freq, pos, ax = 1, 0, None, None, None
     if inv_freq is not None:
         rot = 2 * inv_freq.shape[0]
@@ -535,7 +534,13 @@ def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspa
             raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_kv_append: axis {axis.dtype} {tuple(axis.shape)}, "
                                   f"expected contiguous int32 [{rot // 2}]")
         ax = axis.data_ptr()
-    _on_gpu("spec_kv_append", inv_freq, positions, axis)
+    # last, so that every other refusal can be had without a GPU
+    if not (q.is_cuda and k.is_cuda and v.is_cuda and q_out.is_cuda and q_indptr.is_cuda and kv_len.is_cuda
+            and block_table.is_cuda and workspace.is_cuda and device is not None
+            and (freq is None or inv_freq.is_cuda) and (pos is None or positions.is_cuda)
+            and (ax is None or axis.is_cuda)):
+        _refuse_off_gpu("spec_kv_append", *cache.tensors, q, k, v, q_out, q_indptr, block_table, kv_len, workspace, inv_freq,
+                positions, axis)
     lib = _lib or load()
     code = lib.spec_kv_append(
         cache.address, q.data_ptr(), q_stride[0], q_stride[1], k.data_ptr(), k_stride[0], k_stride[1], v.data_ptr(),
@@ -546,14 +551,13 @@ def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspa
         _check(code, "spec_kv_append")
 
 
-def _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspace):
+def _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len):
     name, n_heads = "spec_kv_append", cache.n_heads
     _positions_first(name, cache, q, k, v, q_out)
     _batch_checks(name, q_indptr, block_table, kv_len)
     if k.shape[1] != n_heads or v.shape[1] != n_heads or q_out.shape != q.shape or not q_out.is_contiguous():
         raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: q {tuple(q.shape)}, k {tuple(k.shape)}, "
                               f"v {tuple(v.shape)}, q_out {tuple(q_out.shape)}, {n_heads} cache heads")
-    _on_gpu(name, cache.tensors[0], cache.tensors[1], q, k, v, q_out, q_indptr, block_table, kv_len, workspace)
     raise SpecVerifyError(SPEC_ERR_INVALID_ARG, name)
 
 
@@ -573,13 +577,11 @@ def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspac
             and q_indptr.dtype is i32 and kv_len.dtype is i32 and block_table.dtype is i32
             and kv_len.dim() == 1 and q_indptr.shape == (kv_len.shape[0] + 1,)
             and block_table.dim() == 2 and block_table.shape[0] == kv_len.shape[0]
-            and q_indptr.is_contiguous() and kv_len.is_contiguous() and block_table.is_contiguous()
-            and q.is_cuda and out.is_cuda and q_indptr.is_cuda and kv_len.is_cuda and block_table.is_cuda
-            and workspace.is_cuda and device is not None):
-        _refuse_attention(cache, q, out, q_indptr, block_table, kv_len, workspace)
+            and q_indptr.is_contiguous() and kv_len.is_contiguous() and block_table.is_contiguous()):
+        _refuse_attention(cache, q, out, q_indptr, block_table, kv_len)
     q_stride, out_stride = q.stride(), out.stride()
     if q_stride[2] != 1 or out_stride[2] != 1:
-        _refuse_attention(cache, q, out, q_indptr, block_table, kv_len, workspace)
+        _refuse_attention(cache, q, out, q_indptr, block_table, kv_len)
     N, n_q_heads = q_shape[0], q_shape[1]
     shared = mask = stats = None
     if prefix_len > 0:
@@ -598,7 +600,11 @@ def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspac
             raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: lse {lse.dtype} {tuple(lse.shape)}, "
                                   f"expected contiguous float32 [{N}, {n_q_heads}]")
         stats = lse.data_ptr()
-    _on_gpu("spec_prefix_attention", prefix_table, draft_mask, lse)
+    if not (q.is_cuda and out.is_cuda and q_indptr.is_cuda and kv_len.is_cuda and block_table.is_cuda
+            and workspace.is_cuda and device is not None and (shared is None or prefix_table.is_cuda)
+            and (mask is None or draft_mask.is_cuda) and (stats is None or lse.is_cuda)):
+        _refuse_off_gpu("spec_prefix_attention", *cache.tensors, q, out, q_indptr, block_table, kv_len, workspace,
+                prefix_table, draft_mask, lse)
     lib = _lib or load()
     code = lib.spec_prefix_attention(
         cache.address, q.data_ptr(), q_stride[0], q_stride[1], n_q_heads, N, q_indptr.data_ptr(), kv_len.shape[0],
@@ -609,11 +615,10 @@ def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspac
         _check(code, "spec_prefix_attention")
 
 
-def _refuse_attention(cache, q, out, q_indptr, block_table, kv_len, workspace):
+def _refuse_attention(cache, q, out, q_indptr, block_table, kv_len):
     name = "spec_prefix_attention"
     _positions_first(name, cache, q, out)
     _batch_checks(name, q_indptr, block_table, kv_len)
     if out.shape != q.shape:
-        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: q {tuple(q.shape)}, out {tuple(out.shape)}")
-    _on_gpu(name, cache.tensors[0], cache.tensors[1], q, out, q_indptr, block_table, kv_len, workspace)
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: q {tuple(q.shape)}, out {tuple(out.shape)}: shapes differ")
     raise SpecVerifyError(SPEC_ERR_INVALID_ARG, name)
