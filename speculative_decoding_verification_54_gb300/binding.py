@@ -428,6 +428,8 @@ def make_kv_cache(k_pages, v_pages) -> SpecKvCache:
             or k_pages.stride(3) != 1:
         raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"cache pools {tuple(k_pages.shape)} with strides "
                               f"{k_pages.stride()}, {tuple(v_pages.shape)} with {v_pages.stride()}")
+    if k_pages.device != v_pages.device:
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"cache pools on {k_pages.device} and {v_pages.device}")
     n_pages, page_size, n_heads, head_dim = k_pages.shape
     page_stride, slot_stride, head_stride, _ = k_pages.stride()
     cache = SpecKvCache(k_pages.data_ptr(), v_pages.data_ptr(), page_stride, slot_stride, head_stride, n_pages,
@@ -451,14 +453,29 @@ def make_attention_workspace(B: int, N: int, n_q_heads: int, head_dim: int, devi
     return _aligned_zeros(spec_attention_workspace_bytes(B, N, n_q_heads, head_dim), device)
 
 
+# PyTorch's raw getters, looked up once (every call asks both)
+_raw_stream = _raw_device = None
+
+
 def _call_stream(stream, device_index):
     """The caller's stream, or PyTorch's current one (its raw handle: building
     the Stream object costs as much as the launch)."""
+    global _raw_stream
     if stream is not None:
         return _stream(stream)
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(device_index) if raw is not None else torch.cuda.current_stream(device_index).cuda_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(device_index)
+
+
+def _current_device() -> int:
+    global _raw_device
+    if _raw_device is None:
+        import torch
+        _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _raw_device()
 
 
 def _positions_first(name, cache, *tensors):
@@ -484,11 +501,15 @@ def _batch_checks(name, q_indptr, block_table, kv_len):
     return B
 
 
-def _refuse_off_gpu(name, *tensors):
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: a tensor of {tuple(t.shape)} is not on the GPU")
-    raise SpecVerifyError(SPEC_ERR_INVALID_ARG, name)
+def _refuse_place(name, cache, **tensors):
+    """Which tensor is not on the cache's GPU, or that GPU is not the current one."""
+    device = cache.expected[4]
+    if device is None:
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: the cache is not on the GPU")
+    for key, t in tensors.items():
+        if t is not None and t.get_device() != device:
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: {key} is on {t.device}, the cache on cuda:{device}")
+    raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: the cache is on cuda:{device}, which is not the current device")
 
 
 def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspace, inv_freq=None, positions=None,
@@ -535,12 +556,12 @@ def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspa
                                   f"expected contiguous int32 [{rot // 2}]")
         ax = axis.data_ptr()
     # last, so that every other refusal can be had without a GPU
-    if not (q.is_cuda and k.is_cuda and v.is_cuda and q_out.is_cuda and q_indptr.is_cuda and kv_len.is_cuda
-            and block_table.is_cuda and workspace.is_cuda and device is not None
-            and (freq is None or inv_freq.is_cuda) and (pos is None or positions.is_cuda)
-            and (ax is None or axis.is_cuda)):
-        _refuse_off_gpu("spec_kv_append", *cache.tensors, q, k, v, q_out, q_indptr, block_table, kv_len, workspace, inv_freq,
-                positions, axis)
+    if not (q.get_device() == k.get_device() == v.get_device() == q_out.get_device() == q_indptr.get_device()
+            == kv_len.get_device() == block_table.get_device() == workspace.get_device() == device == _current_device()
+            and (freq is None or inv_freq.get_device() == device) and (pos is None or positions.get_device() == device)
+            and (ax is None or axis.get_device() == device)):
+        _refuse_place("spec_kv_append", cache, q=q, k=k, v=v, q_out=q_out, q_indptr=q_indptr, block_table=block_table,
+                      kv_len=kv_len, workspace=workspace, inv_freq=inv_freq, positions=positions, axis=axis)
     lib = _lib or load()
     code = lib.spec_kv_append(
         cache.address, q.data_ptr(), q_stride[0], q_stride[1], k.data_ptr(), k_stride[0], k_stride[1], v.data_ptr(),
@@ -600,11 +621,13 @@ def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspac
             raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: lse {lse.dtype} {tuple(lse.shape)}, "
                                   f"expected contiguous float32 [{N}, {n_q_heads}]")
         stats = lse.data_ptr()
-    if not (q.is_cuda and out.is_cuda and q_indptr.is_cuda and kv_len.is_cuda and block_table.is_cuda
-            and workspace.is_cuda and device is not None and (shared is None or prefix_table.is_cuda)
-            and (mask is None or draft_mask.is_cuda) and (stats is None or lse.is_cuda)):
-        _refuse_off_gpu("spec_prefix_attention", *cache.tensors, q, out, q_indptr, block_table, kv_len, workspace,
-                prefix_table, draft_mask, lse)
+    if not (q.get_device() == out.get_device() == q_indptr.get_device() == kv_len.get_device()
+            == block_table.get_device() == workspace.get_device() == device == _current_device()
+            and (shared is None or prefix_table.get_device() == device)
+            and (mask is None or draft_mask.get_device() == device) and (stats is None or lse.get_device() == device)):
+        _refuse_place("spec_prefix_attention", cache, q=q, out=out, q_indptr=q_indptr, block_table=block_table,
+                      kv_len=kv_len, workspace=workspace, prefix_table=prefix_table if prefix_len > 0 else None,
+                      draft_mask=draft_mask, lse=lse)
     lib = _lib or load()
     code = lib.spec_prefix_attention(
         cache.address, q.data_ptr(), q_stride[0], q_stride[1], n_q_heads, N, q_indptr.data_ptr(), kv_len.shape[0],
