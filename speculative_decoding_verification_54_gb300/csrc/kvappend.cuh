@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const __gr
   // ---- the entries of the tile's positions ----
   for (int t = warp; t < tile; t += kAppendThreads / 32) {
     const int n = n0 + t;
-    const int b = find_seq(p.batch.q_indptr, p.batch.B, n, lane);
+    const int b = find_seq(p.batch, n, lane);
     if (lane == 0) {
       int64_t dst = -1, entry = 0;
       bool live = false;

@@ -53,14 +53,16 @@ __device__ __forceinline__ SeqSpan seq_span(const PagedBatch& p, int b) {
 
 // The rows that belong to a sequence: from the first one's to the last one's.
 __device__ __forceinline__ bool in_batch(const PagedBatch& p, int n) {
-  return n >= p.q_indptr[0] && n < p.q_indptr[p.B];
+  const int first = p.q_indptr[0], end = p.q_indptr[p.B];  // both loads at once
+  return (n >= first) & (n < end);
 }
 
 // The sequence whose rows hold `n`, found by a whole warp in steps of 32 (two
 // dependent loads up to 1,024 sequences); -1 where none does (padding).
-__device__ __forceinline__ int find_seq(const int32_t* q_indptr, int B, int n, int lane) {
-  int lo = 0, len = B;  // the last b of [lo, lo + len) with q_indptr[b] <= n
-  if (q_indptr[0] > n || q_indptr[B] <= n) return -1;
+__device__ __forceinline__ int find_seq(const PagedBatch& p, int n, int lane) {
+  const int32_t* const q_indptr = p.q_indptr;
+  int lo = 0, len = p.B;  // the last b of [lo, lo + len) with q_indptr[b] <= n
+  if (!in_batch(p, n)) return -1;
   while (len > 1) {
     const int step = (len + 31) / 32;
     const int at = lane * step;
