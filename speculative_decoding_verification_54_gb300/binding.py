@@ -437,7 +437,8 @@ def make_kv_cache(k_pages, v_pages) -> SpecKvCache:
     cache.tensors = (k_pages, v_pages)
     cache.address = ctypes.addressof(cache)
     # what every call compares with, read once
-    cache.expected = (k_pages.dtype, n_heads, head_dim, page_size, k_pages.device.index)
+    cache.expected = (k_pages.dtype, n_heads, head_dim, page_size, k_pages.device.index, torch.int32, torch.float32,
+                      torch.int64)
     return cache
 
 
@@ -522,9 +523,8 @@ def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspa
     int32 [B] (the new positions counted); inv_freq float32 [rot_dim / 2] (None:
     no rotation); positions int32 [n_axes, N] and axis int32 [rot_dim / 2], or
     None for position_base + the entry's index."""
-    import torch
-    dt, n_heads, D, _, device = cache.expected
-    i32, q_shape, k_shape = torch.int32, q.shape, k.shape
+    dt, n_heads, D, _, device, i32, f32, _ = cache.expected
+    q_shape, k_shape = q.shape, k.shape
     # one pass over what has to hold; which one does not is found out after
     if not (q.dtype is dt and k.dtype is dt and v.dtype is dt and q_out.dtype is dt
             and len(q_shape) == 3 and q_shape[2] == D and k_shape == (q_shape[0], n_heads, D) and v.shape == k_shape
@@ -540,7 +540,7 @@ def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspa
     n_axes, rot, freq, pos, ax = 1, 0, None, None, None
     if inv_freq is not None:
         rot = 2 * inv_freq.shape[0]
-        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        if inv_freq.dtype is not f32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise SpecVerifyError(SPEC_ERR_INVALID_ARG, "spec_kv_append: inv_freq must be contiguous float32")
         freq = inv_freq.data_ptr()
     if positions is not None:
@@ -591,9 +591,8 @@ def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspac
     [>= ceil(prefix_len / page_size)]; draft_mask int64 [N] (64 bits, bit j: the
     position sees new entry j) or None for a chain; scale defaults to
     D ** -0.5; lse float32 [N, n_q_heads] or None.  The rest as spec_kv_append."""
-    import torch
-    dt, n_heads, D, page_size, device = cache.expected
-    i32, q_shape = torch.int32, q.shape
+    dt, n_heads, D, page_size, device, i32, f32, i64 = cache.expected
+    q_shape = q.shape
     if not (q.dtype is dt and out.dtype is dt and len(q_shape) == 3 and q_shape[2] == D and out.shape == q_shape
             and q_indptr.dtype is i32 and kv_len.dtype is i32 and block_table.dtype is i32
             and kv_len.dim() == 1 and q_indptr.shape == (kv_len.shape[0] + 1,)
@@ -612,12 +611,12 @@ def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspac
                                   f"of {prefix_len} entries")
         shared = prefix_table.data_ptr()
     if draft_mask is not None:
-        if draft_mask.dtype is not torch.int64 or draft_mask.shape != (N,) or not draft_mask.is_contiguous():
+        if draft_mask.dtype is not i64 or draft_mask.shape != (N,) or not draft_mask.is_contiguous():
             raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: draft_mask {draft_mask.dtype} "
                                   f"{tuple(draft_mask.shape)}, expected contiguous int64 [{N}]")
         mask = draft_mask.data_ptr()
     if lse is not None:
-        if lse.dtype is not torch.float32 or lse.shape != (N, n_q_heads) or not lse.is_contiguous():
+        if lse.dtype is not f32 or lse.shape != (N, n_q_heads) or not lse.is_contiguous():
             raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: lse {lse.dtype} {tuple(lse.shape)}, "
                                   f"expected contiguous float32 [{N}, {n_q_heads}]")
         stats = lse.data_ptr()
