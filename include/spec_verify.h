@@ -488,9 +488,10 @@ int spec_kv_append(const spec_kv_cache *cache, const void *q, int64_t q_pos_stri
  *   q, out  [N, n_q_heads, D], strides in elements, multiples of 16 bytes
  *
  * Products of the 16-bit values on the tensor cores, sums and softmax in fp32;
- * the weights are rounded to the cache's type for the product with v.  Entries
+ * the weights are rounded to the cache's type for the product with v (half a
+ * step; an fp16 weight, where small, by 2^-32 of the row's largest).  Entries
  * past a length may hold anything; values of live entries must be finite, also
- * where a mask hides them.  Limits: D 64 or 128, page_size a multiple of 8,
+ * where a mask hides them, and below 2^88 (sums are divided at the end).  Limits: D 64 or 128, page_size a multiple of 8,
  * n_q_heads a multiple of n_heads and at most 128 times it (else
  * SPEC_ERR_UNSUPPORTED); scale > 0.
  */

@@ -34,9 +34,10 @@
 //                   of a page and 64 dims).
 // TMEM: S0 S1 (128 columns each) and O0 O1 (D columns each).
 //
-// The reference m of a row rises only when a tile's maximum passes it by more
-// than 2^8, and only then is O (in TMEM) multiplied; weights stay below 256, l
-// and O are exact with respect to any m.  A NaN score raises no maximum (m may
+// The reference m of a row rises only when a tile's maximum passes the one it
+// was set at by more than 2^8, and only then is O (in TMEM) multiplied; weights
+// stay below 2^8, fp16's (which begin higher) below 2^15; l and O are exact with
+// respect to any m.  A NaN score raises no maximum (m may
 // stay -inf) but makes l and O NaN, and so does an infinite one (inf - inf):
 // l, not m, tells a row that saw nothing, by l = 0.
 //
@@ -72,7 +73,14 @@ constexpr int kAtRingBytes = 160 * 1024;
 constexpr int kAtMaxCtas = 160;     // slabs in the workspace
 constexpr int kAtQueue = 4;         // parts queued ahead
 constexpr int kAtFixed = 15;        // weight of a part's fixed cost
-constexpr float kAtRise = 8.f;      // log2 of the largest weight
+constexpr float kAtRise = 8.f;      // log2 of how far a row's maximum may pass the one its reference was set at
+// log2 of the weight that a maximum gets when the reference is set at it.  fp16
+// weights reach 2^15 of the 65,504 that the type holds: below 2^-14 they lose
+// bits, below 2^-25 all, so the higher they stand the longer the tail that counts
+// (8,192 keys of 2^-25.5 of the largest weight each, values 2,048 times the
+// largest's: 1.18 for 1.35 with 0 here).  bf16 has fp32's exponents.
+template <typename T>
+constexpr float kAtTop = std::is_same<T, __half>::value ? 7.f : 0.f;
 
 struct AttendParams {
   CUtensorMap tmK, tmV;  // [page, head, slot, dim], boxes of 64 dims x box_rows slots
@@ -743,9 +751,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
             tops[c] = fmaxf(tops[c], __uint_as_float(s[c][31]));
           }
           const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * p.scale_log2;
-          const bool rise = top > m + kAtRise || (m == -INFINITY && top > -INFINITY);
+          const bool rise = top > m + (kAtTop<T> + kAtRise) || (m == -INFINITY && top > -INFINITY);
           if (__any_sync(0xffffffffu, rise)) {
-            const float nm = rise ? top : m;
+            const float nm = rise ? top - kAtTop<T> : m;
             const float al = rise ? ex2(m - nm) : 1.f;  // 0 at a row's first keys
             l *= al;
             m = nm;
