@@ -408,7 +408,7 @@ int spec_round_update(spec_round_state *states, const int32_t *num_accepted, int
  *                positions (q_len[b] <= kv_len[b] <= table_width * page_size);
  *                new position i is entry kv_len[b] - q_len[b] + i.  The shared
  *                prefix is not counted.
- *   workspace    spec_attention_workspace_bytes() bytes, 256-byte aligned,
+ *   workspace    as many bytes as the calls below say, 256-byte aligned,
  *                zeroed once; calls that share one must not overlap
  * Every length and table is read on the device, so a captured graph serves
  * rounds of other lengths.  What is outside its range makes spec_verify_status
@@ -432,9 +432,14 @@ typedef struct {
 
 /*
  * Bytes of workspace for either call with up to B sequences, N new positions,
- * n_q_heads query heads of head_dim.
+ * n_q_heads query heads of head_dim, any prefix.  Each call by itself needs less:
+ * the append its status word alone, the attention without a prefix
+ * (prefix_len 0) about half.
  */
 int spec_attention_workspace_bytes(int B, int N, int n_q_heads, int head_dim, size_t *bytes);
+int spec_kv_append_workspace_bytes(size_t *bytes);
+int spec_prefix_attention_workspace_bytes(int B, int N, int n_q_heads, int head_dim,
+                                          int64_t prefix_len, size_t *bytes);
 
 /*
  * Rotate the new queries and keys to their positions and append keys and

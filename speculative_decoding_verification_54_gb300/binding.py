@@ -35,6 +35,7 @@ EXPORTED = (
     "spec_verify_sample_topkp", "spec_centroid_head_workspace_bytes", "spec_centroid_head",
     "spec_verify_sparse_workspace_bytes", "spec_verify_sample_sparse",
     "spec_attention_workspace_bytes", "spec_kv_append", "spec_prefix_attention",
+    "spec_kv_append_workspace_bytes", "spec_prefix_attention_workspace_bytes",
 )
 
 
@@ -84,6 +85,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.spec_verify_sample_sparse.argtypes = [_vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i,
                                               _vp, _vp, _vp, _vp, _sz, _vp]
     lib.spec_attention_workspace_bytes.argtypes = [_i, _i, _i, _i, ctypes.POINTER(_sz)]
+    lib.spec_kv_append_workspace_bytes.argtypes = [ctypes.POINTER(_sz)]
+    lib.spec_prefix_attention_workspace_bytes.argtypes = [_i, _i, _i, _i, _i64, ctypes.POINTER(_sz)]
     lib.spec_kv_append.argtypes = [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i, _i, _vp, _i, _vp, _i, _vp,
                                    _vp, _vp, _i, _vp, _i, _i, _i64, _vp, _vp, _sz, _vp]
     lib.spec_prefix_attention.argtypes = [_vp, _vp, _i64, _i64, _i, _i, _vp, _i, _vp, _i64, _vp, _i, _vp, _vp,
@@ -442,16 +445,33 @@ def make_kv_cache(k_pages, v_pages) -> SpecKvCache:
     return cache
 
 
-def spec_attention_workspace_bytes(B: int, N: int, n_q_heads: int, head_dim: int) -> int:
+def spec_attention_workspace_bytes(B: int, N: int, n_q_heads: int, head_dim: int, prefix: bool = True) -> int:
+    """Bytes for spec_prefix_attention (without a shared prefix: prefix=False,
+    about half); they do for spec_kv_append too."""
+    return spec_prefix_attention_workspace_bytes(B, N, n_q_heads, head_dim, 1 if prefix else 0)
+
+
+def spec_prefix_attention_workspace_bytes(B: int, N: int, n_q_heads: int, head_dim: int, prefix_len: int) -> int:
     out = _sz(0)
-    _check(load().spec_attention_workspace_bytes(B, N, n_q_heads, head_dim, ctypes.byref(out)),
-           "spec_attention_workspace_bytes")
+    _check(load().spec_prefix_attention_workspace_bytes(B, N, n_q_heads, head_dim, prefix_len, ctypes.byref(out)),
+           "spec_prefix_attention_workspace_bytes")
     return out.value
 
 
-def make_attention_workspace(B: int, N: int, n_q_heads: int, head_dim: int, device="cuda"):
-    """Allocate (torch) and zero a workspace for spec_kv_append and spec_prefix_attention."""
-    return _aligned_zeros(spec_attention_workspace_bytes(B, N, n_q_heads, head_dim), device)
+def spec_kv_append_workspace_bytes() -> int:
+    out = _sz(0)
+    _check(load().spec_kv_append_workspace_bytes(ctypes.byref(out)), "spec_kv_append_workspace_bytes")
+    return out.value
+
+
+def make_attention_workspace(B: int, N: int, n_q_heads: int, head_dim: int, device="cuda", prefix: bool = True):
+    """Allocate (torch) and zero a workspace for spec_prefix_attention (and spec_kv_append)."""
+    return _aligned_zeros(spec_attention_workspace_bytes(B, N, n_q_heads, head_dim, prefix), device)
+
+
+def make_append_workspace(device="cuda"):
+    """Allocate (torch) and zero a workspace for spec_kv_append alone."""
+    return _aligned_zeros(spec_kv_append_workspace_bytes(), device)
 
 
 # PyTorch's raw getters, looked up once (every call asks both)

@@ -98,11 +98,18 @@ struct AttendParams {
   int tok_tile;      // positions of a row tile: 128 / group
   int n_ctas;
   int64_t* begin;    // [n_ctas + 1] where the CTAs' parts begin
-  int4* part_meta;   // [2][N * n_q_heads] RowItem of each row
-  float* part_o;     // [2][N * n_q_heads][D]
-  float2* part_ml;   // [2][N * n_q_heads]
-  float* slab_o;     // [n_ctas][256][D]
-  float2* slab_ml;   // [n_ctas][256]
+  // rows' own places: [0] for the prefix, if there is one, then for their
+  // sequences' pages
+  int4* part_meta;   // [1 or 2][N * n_q_heads] RowItem of each row
+  float* part_o;     // [1 or 2][N * n_q_heads][D]
+  float2* part_ml;   // [1 or 2][N * n_q_heads]
+  float* slab_o;     // [n_ctas][slab_rows][D]
+  float2* slab_ml;   // [n_ctas][slab_rows]
+  int slab_rows;     // rows of a block, at most
+
+  __device__ __forceinline__ int64_t place(int line, int64_t row) const {
+    return line == 1 && prefix_len > 0 ? static_cast<int64_t>(batch.N) * n_q_heads + row : row;
+  }
 };
 
 // ---------------------------------------------------------------------------
@@ -162,7 +169,7 @@ __device__ __noinline__ void no_tiles(const AttendParams& p, const SeqSpan& s) {
   for (int i = 0; i < s.n; ++i) {
     if (block_tiles(p, s, i / (2 * p.tok_tile)) > 0) continue;
     for (int h = 0; h < p.n_q_heads; ++h)
-      p.part_meta[(static_cast<int64_t>(p.batch.N) + s.first + i) * p.n_q_heads + h] = make_int4(-1, 0, 0, 0);
+      p.part_meta[p.place(1, static_cast<int64_t>(s.first + i) * p.n_q_heads + h)] = make_int4(-1, 0, 0, 0);
   }
 }
 
@@ -815,14 +822,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       float* dst_o;
       float2* dst_ml;
       int4* dst_meta = nullptr;
-      const int slab_row = (two ? g * 128 : 0) + r;
+      const int slab_row = (two && g == 1 ? a.n0 * p.group : 0) + r;  // < slab_rows where r < rows
       if (a.t0 == 0) {
-        const int64_t row = (static_cast<int64_t>(a.line) * p.batch.N + tok) * p.n_q_heads + a.head * p.group + gq;
+        const int64_t row = p.place(a.line, static_cast<int64_t>(tok) * p.n_q_heads + a.head * p.group + gq);
         dst_o = p.part_o + row * D;
         dst_ml = p.part_ml + row;
         dst_meta = p.part_meta + row;
       } else {
-        const int64_t row = static_cast<int64_t>(cta) * 256 + slab_row;
+        const int64_t row = static_cast<int64_t>(cta) * p.slab_rows + slab_row;
         dst_o = p.slab_o + row * D;
         dst_ml = p.slab_ml + row;
       }
@@ -932,9 +939,10 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   for (int line = 0; line < 2; ++line) {
     item[line] = make_int4(-1, 0, 0, 0);
     if (line == 0 && p.prefix_len == 0) continue;
-    item[line] = p.part_meta[line * rows + row];
-    ml[line] = p.part_ml[line * rows + row];
-    load(p.part_o + (line * rows + row) * D + lane * kPer, x[line]);
+    const int64_t at = p.place(line, row);
+    item[line] = p.part_meta[at];
+    ml[line] = p.part_ml[at];
+    load(p.part_o + at * D + lane * kPer, x[line]);
   }
   if (!in_batch(p.batch, n)) return;  // padding, or (reported) before the first sequence: nothing was left for it
 
@@ -955,7 +963,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     if (item[line].x < 0) continue;
     add(ml[line], x[line]);
     const int first = item[line].x & 255, last = min(item[line].x >> 8 & 255, p.n_ctas - 1);
-    const int slab_row = item[line].x >> 16 & 255, tiles = item[line].y >> 2, w = 1 + (item[line].y & 1),
+    const int slab_row = min(item[line].x >> 16 & 255, p.slab_rows - 1), tiles = item[line].y >> 2, w = 1 + (item[line].y & 1),
               fixed = item[line].y & 2 ? kAtFixed : 0;
     const int64_t off = static_cast<int64_t>(item[line].w) << 32 | static_cast<uint32_t>(item[line].z);
     const int64_t* const begin = p.begin;
@@ -975,7 +983,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
           if (parts == 0u) continue;
           const int part = c0 + __ffs(parts) - 1;
           parts &= parts - 1;
-          const int64_t at = static_cast<int64_t>(part) * 256 + slab_row;
+          const int64_t at = static_cast<int64_t>(part) * p.slab_rows + slab_row;
           a[k] = p.slab_ml[at];
           load(p.slab_o + at * D + lane * kPer, v[k]);
         }

@@ -17,13 +17,17 @@ namespace {
 
 struct AttnLayout {
   size_t header, begin, part_meta, part_o, part_ml, slab_o, slab_ml, total;
+  int slab_rows;
 };
 
-// The parts of the rows (one place per row for the prefix, one for its own
-// pages) and of the CTAs (one slab each, two row tiles).
-AttnLayout attn_layout(int B, int N, int n_q_heads, int D) {
+// The parts of the rows (one place per row for the prefix, if there is any,
+// and one for its own pages) and of the CTAs (one slab each: the rows of a block,
+// which are two row tiles or all there are).
+AttnLayout attn_layout(int N, int n_q_heads, int D, bool prefix) {
   AttnLayout L;
-  const size_t rows = 2 * static_cast<size_t>(N) * n_q_heads, slab_rows = size_t(kAtMaxCtas) * 2 * kAtTile;
+  const int64_t places = static_cast<int64_t>(N) * n_q_heads;
+  L.slab_rows = static_cast<int>(places < 2 * kAtTile ? places : 2 * kAtTile);
+  const size_t rows = (prefix ? 2 : 1) * static_cast<size_t>(places), slab_rows = size_t(kAtMaxCtas) * L.slab_rows;
   size_t off = 0;
   auto take = [&off](size_t bytes) {
     const size_t at = off;
@@ -105,10 +109,9 @@ int check_sizes(int B, int N, int n_q_heads, int D) {
 
 bool vec8(int64_t stride) { return (stride & 7) == 0; }
 
-// What both calls check of the cache, the batch and the workspace.
+// What both calls check of the cache and the batch.
 int check_common(const spec_kv_cache* c, int n_q_heads, int N, const int32_t* q_indptr, int B,
-                 const int32_t* block_table, int table_width, const int32_t* kv_len, const void* ws,
-                 size_t ws_bytes) {
+                 const int32_t* block_table, int table_width, const int32_t* kv_len) {
   if (c == nullptr || c->k_pages == nullptr || c->v_pages == nullptr || q_indptr == nullptr ||
       block_table == nullptr || kv_len == nullptr)
     return SPEC_ERR_INVALID_ARG;
@@ -121,10 +124,11 @@ int check_common(const spec_kv_cache* c, int n_q_heads, int N, const int32_t* q_
   if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !vec8(c->page_stride) || !vec8(c->slot_stride) ||
       !vec8(c->head_stride))
     return SPEC_ERR_ALIGNMENT;
-  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 ||
-      ws_bytes < attn_layout(B, N, n_q_heads, c->head_dim).total)
-    return SPEC_ERR_WORKSPACE;
   return SPEC_OK;
+}
+
+int check_workspace(const void* ws, size_t bytes, size_t needed) {
+  return ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || bytes < needed ? SPEC_ERR_WORKSPACE : SPEC_OK;
 }
 
 PagedView view_of(const spec_kv_cache* c) {
@@ -193,10 +197,21 @@ int launch_attend(const AttendParams& p, cudaStream_t s) {
 
 extern "C" {
 
-int spec_attention_workspace_bytes(int B, int N, int n_q_heads, int head_dim, size_t* bytes) {
-  if (bytes == nullptr) return SPEC_ERR_INVALID_ARG;
+int spec_prefix_attention_workspace_bytes(int B, int N, int n_q_heads, int head_dim, int64_t prefix_len,
+                                          size_t* bytes) {
+  if (bytes == nullptr || prefix_len < 0) return SPEC_ERR_INVALID_ARG;
   if (int e = check_sizes(B, N, n_q_heads, head_dim)) return e;
-  *bytes = attn_layout(B, N, n_q_heads, head_dim).total;
+  *bytes = attn_layout(N, n_q_heads, head_dim, prefix_len > 0).total;
+  return SPEC_OK;
+}
+
+int spec_attention_workspace_bytes(int B, int N, int n_q_heads, int head_dim, size_t* bytes) {
+  return spec_prefix_attention_workspace_bytes(B, N, n_q_heads, head_dim, 1, bytes);
+}
+
+int spec_kv_append_workspace_bytes(size_t* bytes) {
+  if (bytes == nullptr) return SPEC_ERR_INVALID_ARG;
+  *bytes = sizeof(WsHeader);  // the status word's
   return SPEC_OK;
 }
 
@@ -207,9 +222,8 @@ int spec_kv_append(const spec_kv_cache* cache, const void* q, int64_t q_pos_stri
                    const int32_t* positions, int n_axes, const int32_t* axis, int rot_dim, int interleaved,
                    int64_t position_base, void* q_out, void* workspace, size_t workspace_bytes, void* stream) {
   if (q == nullptr || k == nullptr || v == nullptr || q_out == nullptr) return SPEC_ERR_INVALID_ARG;
-  if (int e = check_common(cache, n_q_heads, N, q_indptr, B, block_table, table_width, kv_len, workspace,
-                           workspace_bytes))
-    return e;
+  if (int e = check_common(cache, n_q_heads, N, q_indptr, B, block_table, table_width, kv_len)) return e;
+  if (int e = check_workspace(workspace, workspace_bytes, sizeof(WsHeader))) return e;
   const int D = cache->head_dim;
   if (rot_dim < 0 || rot_dim > D || (rot_dim & 1) != 0 || (rot_dim > 0 && inv_freq == nullptr)) return SPEC_ERR_INVALID_ARG;
   if (interleaved != 0 && interleaved != 1) return SPEC_ERR_INVALID_ARG;
@@ -264,9 +278,9 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
                           int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
                           void* stream) {
   if (q == nullptr || out == nullptr) return SPEC_ERR_INVALID_ARG;
-  if (int e = check_common(cache, n_q_heads, N, q_indptr, B, block_table, table_width, kv_len, workspace,
-                           workspace_bytes))
-    return e;
+  if (int e = check_common(cache, n_q_heads, N, q_indptr, B, block_table, table_width, kv_len)) return e;
+  const AttnLayout L = attn_layout(N, n_q_heads, cache->head_dim, prefix_len > 0);
+  if (int e = check_workspace(workspace, workspace_bytes, L.total)) return e;
   if (prefix_len < 0 || prefix_len > INT32_MAX - kAtTile || (prefix_len > 0 && prefix_table == nullptr) || !(scale > 0.f) || !std::isfinite(scale))
     return SPEC_ERR_INVALID_ARG;
   if (n_q_heads % cache->n_heads != 0 || q_pos_stride < 0 || q_head_stride < 0) return SPEC_ERR_INVALID_ARG;
@@ -301,7 +315,6 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
   p.n_q_heads = n_q_heads;
   p.n_heads = cache->n_heads;
   p.n_ctas = sms < kAtMaxCtas ? sms : kAtMaxCtas;
-  const AttnLayout L = attn_layout(B, N, n_q_heads, cache->head_dim);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.begin = reinterpret_cast<int64_t*>(ws + L.begin);
   p.part_meta = reinterpret_cast<int4*>(ws + L.part_meta);
@@ -309,6 +322,7 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
   p.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
   p.slab_o = reinterpret_cast<float*>(ws + L.slab_o);
   p.slab_ml = reinterpret_cast<float2*>(ws + L.slab_ml);
+  p.slab_rows = L.slab_rows;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = cache->dtype == SPEC_BF16;
   if (cache->head_dim == 64)
