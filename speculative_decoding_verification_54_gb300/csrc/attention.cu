@@ -52,7 +52,7 @@ struct AttnDevice {
 
 // SMs of the current device; the first call on a device raises the attention
 // kernels' shared-memory limits.
-int attn_device(int* sms) {
+int device_sms(int* sms) {
   constexpr int kMaxDevices = 64;
   static AttnDevice devices[kMaxDevices];
   static std::mutex mu;
@@ -262,7 +262,9 @@ int spec_kv_append(const spec_kv_cache* cache, const void* q, int64_t q_pos_stri
   // at most 24 (32,768 positions of 256 dims: 24 a CTA 196 us, 8 203 us, 4 216
   // us, 2 251 us; a position's look-ups cost as much as streaming some 30 KB),
   // and no more than 32 KB of cosines and sines.
-  p.tile = (N + 3 * kAppendSms - 1) / (3 * kAppendSms);
+  int sms = 0;
+  if (int e = device_sms(&sms)) return e;
+  p.tile = (N + 3 * sms - 1) / (3 * sms);
   const int most = p.half > 0 ? 32 * 1024 / (p.half * static_cast<int>(sizeof(float2))) : kAppendMaxTile;
   if (p.tile > most) p.tile = most;
   if (p.tile > kAppendMaxTile) p.tile = kAppendMaxTile;
@@ -291,7 +293,7 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
       !vec8(out_head_stride))
     return SPEC_ERR_ALIGNMENT;
   int sms = 0;
-  if (int e = attn_device(&sms)) return e;
+  if (int e = device_sms(&sms)) return e;
   AttendParams p = {};
   // a box lies inside one page and one key tile
   p.box_rows = 8;

@@ -36,7 +36,6 @@ namespace specv {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendMaxTile = 24;   // positions a CTA takes, at most
 constexpr int kAppendBatch = 3;      // heads a thread has in flight
-constexpr int kAppendSms = 152;      // GB300's; the tile size goes by it
 
 struct AppendParams {
   const uint16_t *q, *k, *v;
