@@ -544,14 +544,14 @@ def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspa
     no rotation); positions int32 [n_axes, N] and axis int32 [rot_dim / 2], or
     None for position_base + the entry's index."""
     dt, n_heads, D, _, device, i32, f32, _ = cache.expected
-    q_shape, k_shape = q.shape, k.shape
+    q_shape, k_shape, table_shape, B = q.shape, k.shape, block_table.shape, kv_len.numel()
     # one pass over what has to hold; which one does not is found out after
     if not (q.dtype is dt and k.dtype is dt and v.dtype is dt and q_out.dtype is dt
             and len(q_shape) == 3 and q_shape[2] == D and k_shape == (q_shape[0], n_heads, D) and v.shape == k_shape
             and q_out.shape == q_shape and q_out.is_contiguous()
             and q_indptr.dtype is i32 and kv_len.dtype is i32 and block_table.dtype is i32
-            and kv_len.dim() == 1 and q_indptr.shape == (kv_len.shape[0] + 1,)
-            and block_table.dim() == 2 and block_table.shape[0] == kv_len.shape[0]
+            and kv_len.dim() == 1 and q_indptr.dim() == 1 and q_indptr.numel() == B + 1
+            and len(table_shape) == 2 and table_shape[0] == B
             and q_indptr.is_contiguous() and kv_len.is_contiguous() and block_table.is_contiguous()):
         _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len)
     q_stride, k_stride, v_stride = q.stride(), k.stride(), v.stride()
@@ -585,8 +585,8 @@ def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspa
     lib = _lib or load()
     code = lib.spec_kv_append(
         cache.address, q.data_ptr(), q_stride[0], q_stride[1], k.data_ptr(), k_stride[0], k_stride[1], v.data_ptr(),
-        v_stride[0], v_stride[1], q_shape[1], q_shape[0], q_indptr.data_ptr(), kv_len.shape[0], block_table.data_ptr(),
-        block_table.shape[1], kv_len.data_ptr(), freq, pos, n_axes, ax, rot, 1 if interleaved else 0, position_base,
+        v_stride[0], v_stride[1], q_shape[1], q_shape[0], q_indptr.data_ptr(), B, block_table.data_ptr(),
+        table_shape[1], kv_len.data_ptr(), freq, pos, n_axes, ax, rot, 1 if interleaved else 0, position_base,
         q_out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _call_stream(stream, device))
     if code != SPEC_OK:
         _check(code, "spec_kv_append")
@@ -612,11 +612,11 @@ def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspac
     position sees new entry j) or None for a chain; scale defaults to
     D ** -0.5; lse float32 [N, n_q_heads] or None.  The rest as spec_kv_append."""
     dt, n_heads, D, page_size, device, i32, f32, i64 = cache.expected
-    q_shape = q.shape
+    q_shape, table_shape, B = q.shape, block_table.shape, kv_len.numel()
     if not (q.dtype is dt and out.dtype is dt and len(q_shape) == 3 and q_shape[2] == D and out.shape == q_shape
             and q_indptr.dtype is i32 and kv_len.dtype is i32 and block_table.dtype is i32
-            and kv_len.dim() == 1 and q_indptr.shape == (kv_len.shape[0] + 1,)
-            and block_table.dim() == 2 and block_table.shape[0] == kv_len.shape[0]
+            and kv_len.dim() == 1 and q_indptr.dim() == 1 and q_indptr.numel() == B + 1
+            and len(table_shape) == 2 and table_shape[0] == B
             and q_indptr.is_contiguous() and kv_len.is_contiguous() and block_table.is_contiguous()):
         _refuse_attention(cache, q, out, q_indptr, block_table, kv_len)
     q_stride, out_stride = q.stride(), out.stride()
@@ -649,8 +649,8 @@ def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspac
                       draft_mask=draft_mask, lse=lse)
     lib = _lib or load()
     code = lib.spec_prefix_attention(
-        cache.address, q.data_ptr(), q_stride[0], q_stride[1], n_q_heads, N, q_indptr.data_ptr(), kv_len.shape[0],
-        shared, prefix_len, block_table.data_ptr(), block_table.shape[1], kv_len.data_ptr(), mask,
+        cache.address, q.data_ptr(), q_stride[0], q_stride[1], n_q_heads, N, q_indptr.data_ptr(), B,
+        shared, prefix_len, block_table.data_ptr(), table_shape[1], kv_len.data_ptr(), mask,
         D ** -0.5 if scale is None else scale, out.data_ptr(), out_stride[0], out_stride[1], stats,
         workspace.data_ptr(), workspace.nbytes, _call_stream(stream, device))
     if code != SPEC_OK:
