@@ -107,6 +107,7 @@ struct AttendParams {
   float2* slab_ml;   // [n_ctas][slab_rows]
   int slab_rows;     // rows of a block, at most
 
+  // a row's index in part_* (row: of [N * n_q_heads])
   __device__ __forceinline__ int64_t place(int line, int64_t row) const {
     return line == 1 && prefix_len > 0 ? static_cast<int64_t>(batch.N) * n_q_heads + row : row;
   }
@@ -169,7 +170,8 @@ __device__ __noinline__ void no_tiles(const AttendParams& p, const SeqSpan& s) {
   for (int i = 0; i < s.n; ++i) {
     if (block_tiles(p, s, i / (2 * p.tok_tile)) > 0) continue;
     for (int h = 0; h < p.n_q_heads; ++h)
-      p.part_meta[p.place(1, static_cast<int64_t>(s.first + i) * p.n_q_heads + h)] = make_int4(-1, 0, 0, 0);
+      if (in_bounds(s.first >= 0 && s.first + i < p.batch.N, p.batch.status))
+        p.part_meta[p.place(1, static_cast<int64_t>(s.first + i) * p.n_q_heads + h)] = make_int4(-1, 0, 0, 0);
   }
 }
 
@@ -364,6 +366,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           if (!ok) return;
           if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[g], kHalves * 128u * p.group * p.tok_tile);
           __syncwarp();
+          // (tiled copies stay inside their tensor by themselves: recorded only)
+          in_bounds(first >= 0 && first < p.batch.N && (head + 1) * p.group <= p.n_q_heads, status);
           if (lane < kHalves)
             tma_load_3d(smem_u32(qbuf) + g * kTileBytes + lane * kHalfBytes, &p.tmQ, lane * 64, head * p.group, first,
                         &sh.q_full[g]);
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           own_off += __shfl_sync(0xffffffffu, inc, 31);
         }
       }
-      if (ok && lane == 0) {
+      if (ok && lane == 0 && in_bounds(cta < p.n_ctas, status)) {
         p.begin[cta] = lo;
         if (cta == p.n_ctas - 1) p.begin[cta + 1] = hi;
       }
@@ -627,9 +631,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
             line == 0 ? p.prefix_table : p.batch.block_table + static_cast<int64_t>(seq) * p.batch.table_width;
         // the page of this lane's box in the part's tile i, loaded three tiles
         // ahead; past the entries n_pages, where the copy fills zeros
+        const uint32_t table_end = line == 0 ? (p.prefix_len - 1u) / page_size + 1 : p.batch.table_width;
         auto page_at = [&](int i) {
           const uint32_t key = static_cast<uint32_t>(t0 + i) * kAtTile + my_box * p.box_rows;
-          return loads && i < tiles && key < static_cast<uint32_t>(len) ? table[key / page_size] : p.n_pages;
+          return loads && i < tiles && key < static_cast<uint32_t>(len) &&
+                         in_bounds(key / page_size < table_end && seq >= 0 && seq < p.batch.B, status)
+                     ? table[key / page_size]
+                     : p.n_pages;
         };
         int page0 = page_at(0), page1 = page_at(1), page2 = page_at(2);
 #pragma unroll 1
@@ -658,6 +666,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[slot], kTileBytes);
           __syncwarp();
+          in_bounds(slot < kSlots && at_slot + p.box_rows <= static_cast<int>(page_size) && head >= 0 && head < p.n_heads,
+                    status);
           if (loads) tma_load_4d(my_dst + slot * kTileBytes, map, my_half * 64, at_slot, head, page, &sh.kv_full[slot]);
           if (lane == static_cast<int>(slot)) last = at + 1;
         }
@@ -714,7 +724,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           lim = a.old + (tok - a.seq_first) + 1;
         } else {
           lim = a.old;
-          bits = p.draft_mask[tok];
+          bits = in_bounds(tok >= 0 && tok < p.batch.N, status) ? p.draft_mask[tok] : 0;
           if (a.seq_n < 64) bits &= (1ull << a.seq_n) - 1;
         }
       }
@@ -808,6 +818,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
           uint8_t* v = ring + (at % kSlots) * kTileBytes;
           for (int x = r; x < (end - live) * 8 * kHalves; x += 128) {
             const int row = live + x / (8 * kHalves), c = x % (8 * kHalves);
+            if (!in_bounds(row < kAtTile, status)) continue;
             *reinterpret_cast<uint4*>(v + (c / 8) * kHalfBytes + row * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_async_shared();
@@ -858,7 +869,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         f1 = g == 0 ? fo : fm;
       }
       if (warp_live) {
-        const bool mine_to_write = r < rows;
+        const bool mine_to_write =
+            r < rows && in_bounds(a.t0 == 0 ? tok >= 0 && tok < p.batch.N && a.head * p.group + gq < p.n_q_heads
+                                            : cta < p.n_ctas && slab_row < p.slab_rows,
+                                  status);
         if (two) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -983,6 +997,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
           if (parts == 0u) continue;
           const int part = c0 + __ffs(parts) - 1;
           parts &= parts - 1;
+          if (!in_bounds(part < p.n_ctas && slab_row >= 0 && slab_row < p.slab_rows, p.batch.status)) continue;
           const int64_t at = static_cast<int64_t>(part) * p.slab_rows + slab_row;
           a[k] = p.slab_ml[at];
           load(p.slab_o + at * D + lane * kPer, v[k]);

@@ -205,16 +205,19 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const __gr
         // What has no place in the table is not written.
         entry = n + s.shift;
         int page = -1;
-        if (live && entry >= 0 && entry < static_cast<int64_t>(p.batch.table_width) * p.batch.page_size)
+        if (live && entry >= 0 && entry < static_cast<int64_t>(p.batch.table_width) * p.batch.page_size &&
+            in_bounds(b < p.batch.B && entry / p.batch.page_size < p.batch.table_width, p.batch.status))
           page = p.batch.block_table[static_cast<int64_t>(b) * p.batch.table_width + entry / p.batch.page_size];
         if (page >= 0 && page < p.cache.n_pages)
           dst = page * p.cache.page_stride + (entry % p.batch.page_size) * p.cache.slot_stride;
         else
           atomicOr(p.batch.status, kStatusBadCache);
       }
-      s_live[t] = live;
-      s_dst[t] = dst;
-      s_entry[t] = entry;
+      if (in_bounds(t < kAppendMaxTile, p.batch.status)) {
+        s_live[t] = live;
+        s_dst[t] = dst;
+        s_entry[t] = entry;
+      }
     }
   }
   __syncthreads();
@@ -235,7 +238,8 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const __gr
         const int64_t pos = p.positions != nullptr
                                 ? static_cast<int64_t>(p.positions[static_cast<int64_t>(a) * p.batch.N + n0 + t])
                                 : p.position_base + s_entry[t];
-        ap_units[t * p.half + unit_index(f, p.half)] = unit_of(pos, turn64);
+        if (in_bounds(t < p.tile && unit_index(f, p.half) >= 0 && unit_index(f, p.half) < p.half, p.batch.status))
+          ap_units[t * p.half + unit_index(f, p.half)] = unit_of(pos, turn64);
       }
     }
     __syncthreads();
@@ -262,7 +266,11 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const __gr
     int ts[kAppendBatch], rs[kAppendBatch];
 #pragma unroll
     for (int i = 0; i < kAppendBatch; ++i) {
-      ts[i] = t_at < tile && s_live[t_at] ? t_at : -1;
+      const bool inside =
+          t_at < tile && in_bounds(t_at >= 0 && t_at < kAppendMaxTile && row_at >= 0 && row_at < rows && d0 + 8 <= p.D &&
+                                       (!two || d1 + 8 <= p.D),
+                                   p.batch.status);
+      ts[i] = inside && s_live[t_at] ? t_at : -1;
       rs[i] = row_at;
       if (ts[i] >= 0) {
         const uint16_t* src = p.row_src(n0 + t_at, row_at);
@@ -309,7 +317,10 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const __gr
       if (row < Hq) {
         dst = p.q_out + (n * Hq + row) * p.D;
       } else {
-        if (dst0 < 0) continue;
+        if (dst0 < 0 || !in_bounds(dst0 <= (p.cache.n_pages - 1) * p.cache.page_stride +
+                                               (p.batch.page_size - 1) * p.cache.slot_stride,
+                                   p.batch.status))
+          continue;
         const bool is_k = row < Hq + Hk;
         dst = (is_k ? p.cache.k : p.cache.v) + dst0 + (row - Hq - (is_k ? 0 : Hk)) * p.cache.head_stride;
       }
