@@ -448,7 +448,7 @@ int spec_prefix_attention_workspace_bytes(int B, int N, int n_q_heads, int head_
  *   q [N, n_q_heads, D], k and v [N, n_heads, D]   elements; strides in elements
  *                between positions and between heads, so all three can be views
  *                of one projection's output
- *   q_out        [N, n_q_heads, D] contiguous; must not overlap q
+ *   q_out        [N, n_q_heads, D] contiguous; must not overlap q, k or v
  *   inv_freq     float32 [rot_dim / 2]: angle per position of each pair
  *   positions    int32 [n_axes, N] (row a: the positions on axis a, such as
  *                time, height and width), or NULL: position_base + the entry's
@@ -496,9 +496,9 @@ int spec_kv_append(const spec_kv_cache *cache, const void *q, int64_t q_pos_stri
  * the weights are rounded to the cache's type for the product with v (half a
  * step; an fp16 weight, where small, by 2^-32 of the row's largest).  Entries
  * past a length may hold anything; values of live entries must be finite, also
- * where a mask hides them, and below 2^88 (sums are divided at the end).  Limits: D 64 or 128, page_size a multiple of 8,
- * n_q_heads a multiple of n_heads and at most 128 times it (else
- * SPEC_ERR_UNSUPPORTED); scale > 0.
+ * where a mask hides them, and below 2^88 (sums are divided at the end).
+ * Limits: D 64 or 128, page_size a multiple of 8, n_q_heads a multiple of
+ * n_heads and at most 128 times it (else SPEC_ERR_UNSUPPORTED); scale > 0.
  */
 int spec_prefix_attention(const spec_kv_cache *cache, const void *q, int64_t q_pos_stride,
                           int64_t q_head_stride, int n_q_heads, int N, const int32_t *q_indptr,

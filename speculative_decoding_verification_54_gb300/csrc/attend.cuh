@@ -47,8 +47,9 @@
 // maximum, 128 exponentials at 8 a clock per SM quarter, the stores) -> O and the
 // next scores (1,024 clocks of products).  P takes the place of S, so a group's
 // chain is serial; the two groups overlap and take 3,250 clocks a tile where
-// the products alone take 2,048 (B = 128, prefix 32,768: 357 us, 1.0 PFLOP/s of
-// the pairs that exist).  Tried and not kept: 64-key steps with two score
+// the products alone take 2,048 (B = 128, prefix 32,768: 366 to 387 us on five
+// boxes, 0.92 to 0.97 PFLOP/s of the pairs that exist).  A softmax thread holds
+// 128 scores: 100 bytes a thread spill at D = 128, 52 at D = 64.  Tried and not kept: 64-key steps with two score
 // buffers (scores of 64 keys cost 48 clocks an instruction against 64 for 128:
 // 474 us then against 435), halves of a row in two threads (701), the first 64
 // keys' weights announced early (no change), an issuer per group (432: products

@@ -259,9 +259,9 @@ int spec_kv_append(const spec_kv_cache* cache, const void* q, int64_t q_pos_stri
   p.D = D;
   p.half = rot_dim / 2;
   // Positions a CTA takes: as few as fill the GPU once with three CTAs an SM,
-  // at most 24 (32,768 positions of 256 dims: 24 a CTA 196 us, 8 203 us, 4 216
-  // us, 2 251 us; a position's look-ups cost as much as streaming some 30 KB),
-  // and no more than 32 KB of cosines and sines.
+  // at most 24 (32,768 positions of 256 dims: 24 a CTA 188 us, 8 186 us, 4 195
+  // us, 2 232 us; 5,528 of 128, where 13 fill the GPU once: 13 20.0 us, 8 22.2
+  // us, 4 26.5 us), and no more than 32 KB of cosines and sines.
   int sms = 0;
   if (int e = device_sms(&sms)) return e;
   p.tile = (N + 3 * sms - 1) / (3 * sms);

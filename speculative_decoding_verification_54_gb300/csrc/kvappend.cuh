@@ -20,7 +20,7 @@
 // together where pairs are (f, f + rot/2), so that it reads its 8 pairs'
 // cosines from shared memory and every vector once.  The tile's (position,
 // head) pairs are one sequence, dealt out in turn: heads that do not fill the
-// threads leave none idle (28 + 8 heads of 128, 5,534 positions: 24.0 us against
+// threads leave none idle (28 + 8 heads of 128, 5,528 positions: 24.0 us against
 // 29.4 position by position).  Bound by the copies: q, k, v read once, written
 // once (32,768 positions of 256 dims: 188 us, 5.7 TB/s, 0.84 of the measured
 // copy bandwidth).
@@ -31,7 +31,7 @@
 namespace specv {
 
 // 256 threads, three CTAs an SM, three heads a thread in flight.  On 32,768
-// positions of 256 dims and on 5,534 of 128: two heads 188.2 and 24.6 us, three
+// positions of 256 dims and on 5,528 of 128: two heads 188.2 and 24.6 us, three
 // 188.2 and 24.0, four 190.9 and 24.3.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendMaxTile = 24;   // positions a CTA takes, at most
