@@ -495,8 +495,10 @@ int spec_kv_append(const spec_kv_cache *cache, const void *q, int64_t q_pos_stri
  * Products of the 16-bit values on the tensor cores, sums and softmax in fp32;
  * the weights are rounded to the cache's type for the product with v (half a
  * step; an fp16 weight, where small, by 2^-32 of the row's largest).  Entries
- * past a length may hold anything; values of live entries must be finite, also
- * where a mask hides them, and below 2^88 (sums are divided at the end).
+ * past a length may hold anything, and so may live entries in rows that do not
+ * see them: a value of NaN or infinity reaches the rows that see it and no others.
+ * (A row behind such an entry, or one whose values' sum passes the largest fp32
+ * before its division, is summed again key by key: right, but slow.)
  * Limits: D 64 or 128, page_size a multiple of 8, n_q_heads a multiple of
  * n_heads and at most 128 times it (else SPEC_ERR_UNSUPPORTED); scale > 0.
  */

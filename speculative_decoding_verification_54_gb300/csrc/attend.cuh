@@ -93,6 +93,7 @@ struct AttendParams {
   int n_pages, box_rows;
   const int32_t* prefix_table;
   int prefix_len;
+  int slab_rows;     // rows of a block, at most
   const uint64_t* draft_mask;
   float scale_log2;  // scale * log2(e)
   int n_q_heads, n_heads, group;
@@ -106,7 +107,11 @@ struct AttendParams {
   float2* part_ml;   // [1 or 2][N * n_q_heads]
   float* slab_o;     // [n_ctas][slab_rows][D]
   float2* slab_ml;   // [n_ctas][slab_rows]
-  int slab_rows;     // rows of a block, at most
+  // the queries and the cache as they are, for rows that are summed again (last:
+  // nothing else reads here)
+  const uint16_t* q;
+  int64_t q_ps, q_hs;
+  PagedView cache;
 
   // a row's index in part_* (row: of [N * n_q_heads])
   __device__ __forceinline__ int64_t place(int line, int64_t row) const {
@@ -926,6 +931,108 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------------------
+// A row whose output is not finite although its sum of weights is: an entry that
+// the row does not see may hold an infinity or a NaN, which the tensor cores take
+// times a weight of 0, or the sum passed the largest fp32 before its division.
+// The warp sums the row again, only over what it sees and with the weights
+// divided first: scores with a key a lane, then the values with dims over the
+// lanes.  The prefix's sum (m0, o0) stands where it is finite.  In a verify pass
+// this keeps a bad draft out of the rows before it: some 0.5 us a key of the
+// sequence (the verify batch with one bad draft behind 510 entries: 274 us for
+// 46).  Kept short: with the keys' steps unrolled by eight the join's code cost every
+// launch 1 us, called or not.
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__device__ __noinline__ void sum_row_again(const AttendParams& p, int n, int hq, float m, float inv, float m0, float4 o0) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31, b = find_seq(p.batch, n, lane);
+  if (b < 0) return;
+  const SeqSpan s = seq_span(p.batch, b);
+  const int kv = static_cast<int>(s.kv), first = s.first, count = s.n;
+  const int64_t in_page = (hq / p.group) * p.cache.head_stride;
+  const uint16_t* const q = p.q + n * p.q_ps + hq * p.q_hs;
+  float sum[kPer] = {};
+  // the prefix's sum stands if it is finite
+  const bool stands = fabsf(o0.x) < INFINITY && fabsf(o0.y) < INFINITY && fabsf(o0.z) < INFINITY && fabsf(o0.w) < INFINITY;
+  const int from = __all_sync(0xffffffffu, stands) ? 1 : 0;
+  if (from == 1) {
+    const float f = m0 == -INFINITY ? 0.f : ex2(m0 - m) * inv;
+    sum[0] = o0.x * f;
+    sum[1] = o0.y * f;
+    sum[kPer - 2] = o0.z * f;
+    sum[kPer - 1] = o0.w * f;
+  }
+#pragma unroll 1
+  for (int line = from; line < 2; ++line) {
+    // entries below `lim` are seen, then those of the mask's bits
+    const int32_t* const table =
+        line == 0 ? p.prefix_table : p.batch.block_table + static_cast<int64_t>(b) * p.batch.table_width;
+    const int entries = line == 0 ? p.prefix_len : kv, old = entries - (line == 0 ? 0 : count);
+    const bool masked = line == 1 && p.draft_mask != nullptr;
+    const int lim = line == 0 || masked ? old : old + (n - first) + 1;
+    const uint64_t bits = masked ? p.draft_mask[n] : 0;
+#pragma unroll 1
+    for (int t0 = 0; t0 < entries; t0 += 32) {
+      const int t = t0 + lane, j = t - old;
+      const bool seen = t < entries && (t < lim || (j >= 0 && j < 64 && (bits >> j & 1) != 0));
+      const bool inside = in_bounds(line == 0 || t >= entries || t / p.batch.page_size < p.batch.table_width, p.batch.status);
+      const int page = seen && inside ? table[t / p.batch.page_size] : -1;
+      const bool valid = page >= 0 && page < p.n_pages;  // others' keys and values read as zero (and are reported)
+      const int64_t at = valid ? page * p.cache.page_stride + (t % p.batch.page_size) * p.cache.slot_stride + in_page : 0;
+      float dot = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {  // four loads in flight
+        uint4 k[4] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (valid) k[i] = *reinterpret_cast<const uint4*>(p.cache.k + at + c + 8 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x[8], y[8];
+          unpack8<T>(*reinterpret_cast<const uint4*>(q + c + 8 * i), x);
+          unpack8<T>(k[i], y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = fmaf(x[e], y[e], dot);
+        }
+      }
+      const float w = ex2(fmaf(dot, p.scale_log2, -m)) * inv;
+      const unsigned any = __ballot_sync(0xffffffffu, valid);
+#pragma unroll 1
+      for (int u = 0; u < 32; u += 4) {
+        if ((any >> u & 15) == 0) continue;
+        float wu[4];
+        uint32_t v[4][kPer / 2] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool there = any >> (u + i) & 1;
+          wu[i] = __shfl_sync(0xffffffffu, w, u + i);
+          const uint16_t* from = p.cache.v + __shfl_sync(0xffffffffu, at, u + i) + lane * kPer;
+          if (there) {
+#pragma unroll
+            for (int x = 0; x < kPer / 2; ++x) v[i][x] = reinterpret_cast<const uint32_t*>(from)[x];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if ((any >> (u + i) & 1) == 0) continue;
+#pragma unroll
+          for (int x = 0; x < kPer / 2; ++x) {
+            float v0, v1;
+            Pack16<T>::unpack(v[i][x], v0, v1);
+            sum[2 * x] = fmaf(wu[i], v0, sum[2 * x]);
+            sum[2 * x + 1] = fmaf(wu[i], v1, sum[2 * x + 1]);
+          }
+        }
+      }
+    }
+  }
+  uint16_t* const dst = p.out + n * p.o_ps + hq * p.o_hs + lane * kPer;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2)
+    *reinterpret_cast<uint32_t*>(dst + i) = Pack16<T>::pack(sum[i], sum[i + 1]);
+}
+
+// ---------------------------------------------------------------------------
 // join: one warp per row adds the row's parts.  Each item's first part says
 // where the others are, so a row whose items were not split takes one round of
 // loads.
@@ -961,7 +1068,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   }
   if (!in_batch(p.batch, n)) return;  // padding, or (reported) before the first sequence: nothing was left for it
 
-  float o[kPer] = {}, m = -INFINITY, l = 0.f;
+  float o[kPer] = {}, m = -INFINITY, l = 0.f, m0 = -INFINITY, o0[kPer] = {};  // 0: of the prefix
   auto add = [&](const float2& a, const float (&v)[kPer]) {
     // Nothing seen: a.y is 0, its O is not looked at.  (A part whose every score
     // is NaN has a.x = -inf too, but a.y NaN, which reaches l and o.)
@@ -975,6 +1082,11 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   };
 #pragma unroll
   for (int line = 0; line < 2; ++line) {
+    if (line == 1) {
+      m0 = m;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) o0[i] = o[i];
+    }
     if (item[line].x < 0) continue;
     add(ml[line], x[line]);
     const int first = item[line].x & 255, last = min(item[line].x >> 8 & 255, p.n_ctas - 1);
@@ -1016,6 +1128,11 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   else
     *reinterpret_cast<uint32_t*>(dst) = Pack16<T>::pack(o[0] * inv, o[1] * inv);
   if (lane == 0 && p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) finite = finite && fabsf(o[i]) < INFINITY;
+  if (__any_sync(0xffffffffu, !finite) && l < INFINITY)  // l: as in all lanes
+    sum_row_again<T, D>(p, n, hq, m, inv, m0, make_float4(o0[0], o0[1], o0[kPer - 2], o0[kPer - 1]));
 }
 
 }  // namespace specv

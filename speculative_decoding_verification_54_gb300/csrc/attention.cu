@@ -308,6 +308,10 @@ int spec_prefix_attention(const spec_kv_cache* cache, const void* q, int64_t q_p
   p.o_ps = out_pos_stride;
   p.o_hs = out_head_stride;
   p.lse = lse;
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_ps = q_pos_stride;
+  p.q_hs = q_head_stride;
+  p.cache = view_of(cache);
   p.batch = batch_of(cache, N, q_indptr, B, block_table, table_width, kv_len, workspace);
   p.n_pages = static_cast<int>(cache->n_pages);
   p.prefix_table = prefix_table;

@@ -33,6 +33,9 @@ for c in (t.LARGE[1], t.LARGE[3], t.LARGE[4]):  # split items, a mask, row block
     t.test_attention_large(sv, *c)
     n += 1
 t.test_pages_and_lengths_out_of_range_are_reported(sv)
+from tests import test_gpu_paged_hidden as h  # rows that the join sums again
+for c in h.SHAPES[2:4]:
+    h.test_new_entries(sv, c, "last")
 print("ok", n)
 """
 
