@@ -511,6 +511,110 @@ int spec_prefix_attention(const spec_kv_cache *cache, const void *q, int64_t q_p
                           void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * spec_kv_append with norms of the query and key heads in the same launch:
+ *   x <- x * rsqrt(mean(x^2) + norm_eps) * weight
+ * over a head's D dims in fp32, before the rotation; nothing is rounded between.
+ *
+ *   q_weight, k_weight  float32 [D], for all heads; NULL: that side is not
+ *                       normalised.  Where a model's weight is an offset from 1,
+ *                       pass 1 + it.
+ *   norm_eps            >= 0
+ *
+ * Squares are summed in fp32: a head whose sum passes 3.4e38 (values of 1e18 and
+ * more) becomes 0.  The other arguments, the workspace and the errors are
+ * spec_kv_append's.
+ */
+int spec_kv_append_norm(const spec_kv_cache *cache, const void *q, int64_t q_pos_stride,
+                        int64_t q_head_stride, const void *k, int64_t k_pos_stride,
+                        int64_t k_head_stride, const void *v, int64_t v_pos_stride,
+                        int64_t v_head_stride, int n_q_heads, int N, const int32_t *q_indptr, int B,
+                        const int32_t *block_table, int table_width, const int32_t *kv_len,
+                        const float *inv_freq, const int32_t *positions, int n_axes,
+                        const int32_t *axis, int rot_dim, int interleaved, int64_t position_base,
+                        const float *q_weight, const float *k_weight, float norm_eps, void *q_out,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The paged cache in 8 bits: keys and values as e4m3 codes with a scale for each
+ * block of entries, head and side.  Twice the entries in the same memory, and
+ * half the bytes where the attention is bound by the cache's.
+ *
+ * A block is `block` neighbouring slots of a page that begin at a multiple of it;
+ * its scale is 2^e, kept as the byte e + 127 (the E8M0 format), and a code stands
+ * for code * 2^e, which is a number of the 16-bit type: reading it loses nothing.
+ * e is floor(log2 of the block's largest finite magnitude) - 7, at least -100
+ * (bf16) or -15 (fp16); a code is the nearest one, ties to even: half a step is
+ * 2^-4 of a value that is not below 2^-13 of its block's largest.
+ * Magnitudes past 61440 (fp16) or 240 * 2^120 (bf16) are taken to that; NaN and
+ * infinities are kept as NaN.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct {
+  void *k_pages, *v_pages;      /* device pools of codes; both have the strides below    */
+  void *k_scales, *v_scales;    /* device, one byte a block and head                     */
+  int64_t page_stride;          /* bytes from a page's codes to the next's; these three  */
+  int64_t slot_stride;          /*   multiples of 16                                     */
+  int64_t head_stride;
+  int64_t scale_page_stride;    /* bytes from a page's scales to the next's              */
+  int64_t scale_block_stride;   /*   from a block's to the next's                        */
+  int64_t scale_head_stride;
+  int64_t n_pages;
+  int32_t page_size;            /* a multiple of block                                   */
+  int32_t n_heads;
+  int32_t head_dim;             /* a multiple of 16 up to 256                            */
+  int32_t block;                /* entries of a block: 8, 16, 32 or 64                   */
+  int32_t dtype;                /* SPEC_BF16 or SPEC_F16: of q, k, v and outputs         */
+} spec_kv_cache8;
+
+/*
+ * spec_kv_append_norm to an 8-bit cache.  Values are quantised from fp32, after
+ * norm and rotation.  Where the new entries of a block stand behind older ones the
+ * scale is the larger of the old and theirs; if it rises, the older entries' codes
+ * are rewritten for it, which loses only bits below 2^-17 of what is then the
+ * block's largest.  (So a large draft that is rejected may cost its block's older
+ * entries such bits.)  A page that a sequence appends to must be in no other
+ * sequence's table of the same call at the entries that are written or share a
+ * block with them; other blocks, of this page too, may be shared.
+ */
+int spec_kv_append8(const spec_kv_cache8 *cache, const void *q, int64_t q_pos_stride,
+                    int64_t q_head_stride, const void *k, int64_t k_pos_stride,
+                    int64_t k_head_stride, const void *v, int64_t v_pos_stride,
+                    int64_t v_head_stride, int n_q_heads, int N, const int32_t *q_indptr, int B,
+                    const int32_t *block_table, int table_width, const int32_t *kv_len,
+                    const float *inv_freq, const int32_t *positions, int n_axes,
+                    const int32_t *axis, int rot_dim, int interleaved, int64_t position_base,
+                    const float *q_weight, const float *k_weight, float norm_eps, void *q_out,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Read entries back: row out_indptr[b] + i of k_out and v_out (16-bit type, [R,
+ * n_heads, D], strides in elements, multiples of 8) becomes entry first[b] + i of
+ * sequence b.  out_indptr int32 [B+1], from 0, not descending; first int32 [B] or
+ * NULL (0); rows from out_indptr[B] to R are left as they are.  Either output may be
+ * NULL.  An entry that has no place in the table, or whose page is outside [0,
+ * n_pages), gives zeros and SPEC_ERR_DEVICE_INPUT.  R up to 2^24; the workspace of
+ * spec_kv_append_workspace_bytes.
+ */
+int spec_kv_read8(const spec_kv_cache8 *cache, const int32_t *out_indptr, int R, int B,
+                  const int32_t *block_table, int table_width, const int32_t *first,
+                  void *k_out, int64_t k_pos_stride, int64_t k_head_stride, void *v_out,
+                  int64_t v_pos_stride, int64_t v_head_stride, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/*
+ * spec_prefix_attention over an 8-bit cache: the same arguments, outputs, masks,
+ * precision (over the values that the codes stand for), limits and workspace.
+ */
+int spec_prefix_attention8(const spec_kv_cache8 *cache, const void *q, int64_t q_pos_stride,
+                           int64_t q_head_stride, int n_q_heads, int N, const int32_t *q_indptr,
+                           int B, const int32_t *prefix_table, int64_t prefix_len,
+                           const int32_t *block_table, int table_width, const int32_t *kv_len,
+                           const uint64_t *draft_mask, float scale, void *out,
+                           int64_t out_pos_stride, int64_t out_head_stride, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Synchronise `stream`, then return the device-side status recorded in
  * `workspace` since the last call (SPEC_OK, SPEC_ERR_TIMEOUT or
  * SPEC_ERR_DEVICE_INPUT) and clear it.  Returns SPEC_ERR_CUDA if the

@@ -14,7 +14,7 @@ LIB = os.path.join(LIBDIR, "libspecverify.so")
 # the bounds-checked debug build: every checked row / chunk / token index that
 # falls outside its extent is recorded in the status word (SPEC_ERR_DEVICE_BOUNDS)
 LIB_CHECKED = os.path.join(LIBDIR, "libspecverify_checked.so")
-SOURCES = ["spec_verify.cu", "attention.cu", "round_driver.cpp"]
+SOURCES = ["spec_verify.cu", "attention.cu", "attention8.cu", "round_driver.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -40,7 +40,7 @@ def up_to_date(lib: str = LIB) -> bool:
 
 
 def _command(out: str, checked: bool, extra_flags=()):
-    return ([nvcc_path(), "-O3", "-lineinfo", "-std=c++17", *ARCH, "--threads", "2", "-shared",
+    return ([nvcc_path(), "-O3", "-lineinfo", "-std=c++17", *ARCH, "--threads", "4", "-shared",
              "-Xcompiler", "-fPIC", "-cudart", "static", "-I", INCLUDE, "-I", CSRC]
             + (["-DSPEC_CHECK_BOUNDS"] if checked else []) + list(extra_flags)
             + ["-o", out] + [os.path.join(CSRC, s) for s in SOURCES])

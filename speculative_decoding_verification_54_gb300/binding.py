@@ -36,6 +36,7 @@ EXPORTED = (
     "spec_verify_sparse_workspace_bytes", "spec_verify_sample_sparse",
     "spec_attention_workspace_bytes", "spec_kv_append", "spec_prefix_attention",
     "spec_kv_append_workspace_bytes", "spec_prefix_attention_workspace_bytes",
+    "spec_kv_append_norm", "spec_kv_append8", "spec_kv_read8", "spec_prefix_attention8",
 )
 
 
@@ -91,6 +92,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                    _vp, _vp, _i, _vp, _i, _i, _i64, _vp, _vp, _sz, _vp]
     lib.spec_prefix_attention.argtypes = [_vp, _vp, _i64, _i64, _i, _i, _vp, _i, _vp, _i64, _vp, _i, _vp, _vp,
                                           ctypes.c_float, _vp, _i64, _i64, _vp, _vp, _sz, _vp]
+    lib.spec_kv_append_norm.argtypes = lib.spec_kv_append.argtypes[:24] + [_vp, _vp, ctypes.c_float, _vp, _vp, _sz, _vp]
+    lib.spec_kv_append8.argtypes = list(lib.spec_kv_append_norm.argtypes)
+    lib.spec_kv_read8.argtypes = [_vp, _vp, _i, _i, _vp, _i, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _sz, _vp]
+    lib.spec_prefix_attention8.argtypes = list(lib.spec_prefix_attention.argtypes)
     lib.spec_verify_status.argtypes = [_vp, _vp]
     lib.spec_verify_error_string.argtypes = [_i]
     lib.spec_verify_error_string.restype = ctypes.c_char_p
@@ -499,14 +504,20 @@ def _current_device() -> int:
     return _raw_device()
 
 
+def _cache_of(name, cache, kind, maker):
+    """A cache of the other kind is another struct: never handed on."""
+    if type(cache) is not kind:
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: a cache of {maker} is wanted, not {type(cache).__name__}")
+
+
 def _positions_first(name, cache, *tensors):
     """Shared checks of [N, heads, head_dim] tensors: the cache's dtype and
     head_dim, one N, adjacent dims."""
-    pool = cache.tensors[0]
-    N, D = tensors[0].shape[0], pool.shape[3]
+    dtype, D = cache.expected[0], cache.expected[2]
+    N = tensors[0].shape[0]
     for t in tensors:
-        if t.dtype != pool.dtype:
-            raise SpecVerifyError(SPEC_ERR_UNSUPPORTED, f"{name}: dtype {t.dtype}, cache {pool.dtype}")
+        if t.dtype != dtype:
+            raise SpecVerifyError(SPEC_ERR_UNSUPPORTED, f"{name}: dtype {t.dtype}, cache {dtype}")
         if t.dim() != 3 or t.shape[0] != N or t.shape[2] != D or t.stride(2) != 1:
             raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: shape {tuple(t.shape)} strides {t.stride()}, "
                                   f"expected [{N}, heads, {D}] with adjacent dims")
@@ -543,6 +554,8 @@ def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspa
     int32 [B] (the new positions counted); inv_freq float32 [rot_dim / 2] (None:
     no rotation); positions int32 [n_axes, N] and axis int32 [rot_dim / 2], or
     None for position_base + the entry's index."""
+    if type(cache) is not SpecKvCache:
+        _cache_of("spec_kv_append", cache, SpecKvCache, "make_kv_cache")
     dt, n_heads, D, _, device, i32, f32, _ = cache.expected
     q_shape, k_shape, table_shape, B = q.shape, k.shape, block_table.shape, kv_len.numel()
     # one pass over what has to hold; which one does not is found out after
@@ -592,8 +605,8 @@ def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspa
         _check(code, "spec_kv_append")
 
 
-def _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len):
-    name, n_heads = "spec_kv_append", cache.n_heads
+def _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, name="spec_kv_append"):
+    n_heads = cache.n_heads
     _positions_first(name, cache, q, k, v, q_out)
     _batch_checks(name, q_indptr, block_table, kv_len)
     if k.shape[1] != n_heads or v.shape[1] != n_heads or q_out.shape != q.shape or not q_out.is_contiguous():
@@ -607,10 +620,17 @@ def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspac
     """Attention of the new positions over the shared prefix and their
     sequences' pages.
 
-    q, out [N, n_q_heads, D] in the cache's dtype; prefix_table int32
+    cache from make_kv_cache; q, out [N, n_q_heads, D] in the cache's dtype; prefix_table int32
     [>= ceil(prefix_len / page_size)]; draft_mask int64 [N] (64 bits, bit j: the
     position sees new entry j) or None for a chain; scale defaults to
     D ** -0.5; lse float32 [N, n_q_heads] or None.  The rest as spec_kv_append."""
+    _cache_of("spec_prefix_attention", cache, SpecKvCache, "make_kv_cache")
+    _attention((_lib or load()).spec_prefix_attention, "spec_prefix_attention", cache, q, out, q_indptr, block_table, kv_len,
+               workspace, prefix_table, prefix_len, draft_mask, scale, lse, stream)
+
+
+def _attention(call, name, cache, q, out, q_indptr, block_table, kv_len, workspace, prefix_table, prefix_len, draft_mask,
+               scale, lse, stream):
     dt, n_heads, D, page_size, device, i32, f32, i64 = cache.expected
     q_shape, table_shape, B = q.shape, block_table.shape, kv_len.numel()
     if not (q.dtype is dt and out.dtype is dt and len(q_shape) == 3 and q_shape[2] == D and out.shape == q_shape
@@ -618,49 +638,229 @@ def spec_prefix_attention(cache, q, out, q_indptr, block_table, kv_len, workspac
             and kv_len.dim() == 1 and q_indptr.dim() == 1 and q_indptr.numel() == B + 1
             and len(table_shape) == 2 and table_shape[0] == B
             and q_indptr.is_contiguous() and kv_len.is_contiguous() and block_table.is_contiguous()):
-        _refuse_attention(cache, q, out, q_indptr, block_table, kv_len)
+        _refuse_attention(cache, q, out, q_indptr, block_table, kv_len, name)
     q_stride, out_stride = q.stride(), out.stride()
     if q_stride[2] != 1 or out_stride[2] != 1:
-        _refuse_attention(cache, q, out, q_indptr, block_table, kv_len)
+        _refuse_attention(cache, q, out, q_indptr, block_table, kv_len, name)
     N, n_q_heads = q_shape[0], q_shape[1]
     shared = mask = stats = None
     if prefix_len > 0:
         if prefix_table is None or prefix_table.dtype is not i32 or prefix_table.dim() != 1 \
                 or not prefix_table.is_contiguous() or prefix_table.shape[0] * page_size < prefix_len:
-            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: prefix_table does not hold the pages "
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: prefix_table does not hold the pages "
                                   f"of {prefix_len} entries")
         shared = prefix_table.data_ptr()
     if draft_mask is not None:
         if draft_mask.dtype is not i64 or draft_mask.shape != (N,) or not draft_mask.is_contiguous():
-            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: draft_mask {draft_mask.dtype} "
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: draft_mask {draft_mask.dtype} "
                                   f"{tuple(draft_mask.shape)}, expected contiguous int64 [{N}]")
         mask = draft_mask.data_ptr()
     if lse is not None:
         if lse.dtype is not f32 or lse.shape != (N, n_q_heads) or not lse.is_contiguous():
-            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"spec_prefix_attention: lse {lse.dtype} {tuple(lse.shape)}, "
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: lse {lse.dtype} {tuple(lse.shape)}, "
                                   f"expected contiguous float32 [{N}, {n_q_heads}]")
         stats = lse.data_ptr()
     if not (q.get_device() == out.get_device() == q_indptr.get_device() == kv_len.get_device()
             == block_table.get_device() == workspace.get_device() == device == _current_device()
             and (shared is None or prefix_table.get_device() == device)
             and (mask is None or draft_mask.get_device() == device) and (stats is None or lse.get_device() == device)):
-        _refuse_place("spec_prefix_attention", cache, q=q, out=out, q_indptr=q_indptr, block_table=block_table,
+        _refuse_place(name, cache, q=q, out=out, q_indptr=q_indptr, block_table=block_table,
                       kv_len=kv_len, workspace=workspace, prefix_table=prefix_table if prefix_len > 0 else None,
                       draft_mask=draft_mask, lse=lse)
-    lib = _lib or load()
-    code = lib.spec_prefix_attention(
+    code = call(
         cache.address, q.data_ptr(), q_stride[0], q_stride[1], n_q_heads, N, q_indptr.data_ptr(), B,
         shared, prefix_len, block_table.data_ptr(), table_shape[1], kv_len.data_ptr(), mask,
         D ** -0.5 if scale is None else scale, out.data_ptr(), out_stride[0], out_stride[1], stats,
         workspace.data_ptr(), workspace.nbytes, _call_stream(stream, device))
     if code != SPEC_OK:
-        _check(code, "spec_prefix_attention")
+        _check(code, name)
 
 
-def _refuse_attention(cache, q, out, q_indptr, block_table, kv_len):
-    name = "spec_prefix_attention"
+def _refuse_attention(cache, q, out, q_indptr, block_table, kv_len, name):
     _positions_first(name, cache, q, out)
     _batch_checks(name, q_indptr, block_table, kv_len)
     if out.shape != q.shape:
         raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: q {tuple(q.shape)}, out {tuple(out.shape)}: shapes differ")
     raise SpecVerifyError(SPEC_ERR_INVALID_ARG, name)
+
+
+# ---------------------------------------------------------------------------
+# norms in the append, and the cache in 8 bits
+# ---------------------------------------------------------------------------
+class SpecKvCache8(ctypes.Structure):
+    """spec_kv_cache8: the pools of codes and of scales (strides in bytes)."""
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("k_scales", _vp), ("v_scales", _vp), ("page_stride", _i64),
+                ("slot_stride", _i64), ("head_stride", _i64), ("scale_page_stride", _i64), ("scale_block_stride", _i64),
+                ("scale_head_stride", _i64), ("n_pages", _i64), ("page_size", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("block", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+def make_kv_cache8(k_pages, v_pages, k_scales, v_scales, dtype=None) -> SpecKvCache8:
+    """The 8-bit cache over pools [n_pages, page_size, n_heads, head_dim] of
+    float8_e4m3fn codes (or uint8, the same bytes; any strides but the last, both
+    alike) and scales [n_pages, page_size / block, n_heads] of float8_e8m0fnu (or
+    uint8; any strides, both alike), for queries, keys, values and outputs of
+    `dtype` (bfloat16, the default, or float16).  The block is what the shapes
+    say: 8, 16, 32 or 64 entries.  The struct keeps the tensors alive."""
+    import torch
+    dtype = torch.bfloat16 if dtype is None else dtype
+    codes = {torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+    if dtype not in codes:
+        raise SpecVerifyError(SPEC_ERR_UNSUPPORTED, f"cache of {dtype}")
+    if k_pages.dtype not in (torch.float8_e4m3fn, torch.uint8) or v_pages.dtype != k_pages.dtype:
+        raise SpecVerifyError(SPEC_ERR_UNSUPPORTED, f"cache dtypes {k_pages.dtype}, {v_pages.dtype}: float8_e4m3fn codes")
+    if k_scales.dtype not in (torch.float8_e8m0fnu, torch.uint8) or v_scales.dtype != k_scales.dtype:
+        raise SpecVerifyError(SPEC_ERR_UNSUPPORTED, f"scale dtypes {k_scales.dtype}, {v_scales.dtype}: float8_e8m0fnu")
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() \
+            or k_pages.stride(3) != 1:
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"cache pools {tuple(k_pages.shape)} with strides "
+                              f"{k_pages.stride()}, {tuple(v_pages.shape)} with {v_pages.stride()}")
+    n_pages, page_size, n_heads, head_dim = k_pages.shape
+    if k_scales.dim() != 3 or k_scales.shape != v_scales.shape or k_scales.stride() != v_scales.stride() \
+            or k_scales.shape[0] != n_pages or k_scales.shape[2] != n_heads or k_scales.shape[1] < 1 \
+            or page_size % k_scales.shape[1]:
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"scales {tuple(k_scales.shape)} with strides {k_scales.stride()}, "
+                              f"{tuple(v_scales.shape)} with {v_scales.stride()}: expected [{n_pages}, {page_size} / "
+                              f"block, {n_heads}]")
+    if not k_pages.device == v_pages.device == k_scales.device == v_scales.device:
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"cache pools on {k_pages.device}, {v_pages.device}, scales on "
+                              f"{k_scales.device}, {v_scales.device}")
+    block = page_size // k_scales.shape[1]
+    if block not in (8, 16, 32, 64):
+        raise SpecVerifyError(SPEC_ERR_UNSUPPORTED, f"blocks of {block} entries: 8, 16, 32 or 64")
+    page_stride, slot_stride, head_stride, _ = k_pages.stride()
+    cache = SpecKvCache8(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), page_stride,
+                         slot_stride, head_stride, *k_scales.stride(), n_pages, page_size, n_heads, head_dim, block,
+                         codes[dtype])
+    cache.tensors = (k_pages, v_pages, k_scales, v_scales)
+    cache.address = ctypes.addressof(cache)
+    cache.expected = (dtype, n_heads, head_dim, page_size, k_pages.device.index, torch.int32, torch.float32, torch.int64)
+    return cache
+
+
+def spec_kv_append_norm(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspace, inv_freq=None, positions=None,
+                        axis=None, interleaved=False, position_base=0, q_weight=None, k_weight=None, norm_eps=1e-6,
+                        stream=None) -> None:
+    """spec_kv_append with root-mean-square norms of each query and key head
+    before the rotation: q_weight, k_weight float32 [D], None for no norm of that
+    side.  The rest as spec_kv_append."""
+    _cache_of("spec_kv_append_norm", cache, SpecKvCache, "make_kv_cache")
+    _append_norm((_lib or load()).spec_kv_append_norm, "spec_kv_append_norm", cache, q, k, v, q_out, q_indptr, block_table,
+                 kv_len, workspace, inv_freq, positions, axis, interleaved, position_base, q_weight, k_weight, norm_eps,
+                 stream)
+
+
+def spec_kv_append8(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspace, inv_freq=None, positions=None,
+                    axis=None, interleaved=False, position_base=0, q_weight=None, k_weight=None, norm_eps=1e-6,
+                    stream=None) -> None:
+    """spec_kv_append_norm to an 8-bit cache (from make_kv_cache8): keys and values
+    are quantised as they are written, with a scale for each block of entries."""
+    _cache_of("spec_kv_append8", cache, SpecKvCache8, "make_kv_cache8")
+    _append_norm((_lib or load()).spec_kv_append8, "spec_kv_append8", cache, q, k, v, q_out, q_indptr, block_table, kv_len,
+                 workspace, inv_freq, positions, axis, interleaved, position_base, q_weight, k_weight, norm_eps, stream)
+
+
+def _append_norm(call, name, cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspace, inv_freq, positions, axis,
+                 interleaved, position_base, q_weight, k_weight, norm_eps, stream):
+    dt, n_heads, D, _, device, i32, f32, _ = cache.expected
+    q_shape, k_shape, table_shape, B = q.shape, k.shape, block_table.shape, kv_len.numel()
+    if not (q.dtype is dt and k.dtype is dt and v.dtype is dt and q_out.dtype is dt
+            and len(q_shape) == 3 and q_shape[2] == D and k_shape == (q_shape[0], n_heads, D) and v.shape == k_shape
+            and q_out.shape == q_shape and q_out.is_contiguous()
+            and q_indptr.dtype is i32 and kv_len.dtype is i32 and block_table.dtype is i32
+            and kv_len.dim() == 1 and q_indptr.dim() == 1 and q_indptr.numel() == B + 1
+            and len(table_shape) == 2 and table_shape[0] == B
+            and q_indptr.is_contiguous() and kv_len.is_contiguous() and block_table.is_contiguous()):
+        _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, name)
+    q_stride, k_stride, v_stride = q.stride(), k.stride(), v.stride()
+    if q_stride[2] != 1 or k_stride[2] != 1 or v_stride[2] != 1:
+        _refuse_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, name)
+    n_axes, rot, freq, pos, ax, qw, kw = 1, 0, None, None, None, None, None
+    if inv_freq is not None:
+        rot = 2 * inv_freq.shape[0]
+        if inv_freq.dtype is not f32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: inv_freq must be contiguous float32")
+        freq = inv_freq.data_ptr()
+    if positions is not None:
+        n_axes = positions.shape[0]
+        if positions.dtype is not i32 or positions.shape != (n_axes, q_shape[0]) or not positions.is_contiguous():
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: positions {positions.dtype} "
+                                  f"{tuple(positions.shape)}, expected contiguous int32 [n_axes, {q_shape[0]}]")
+        pos = positions.data_ptr()
+    if axis is not None:
+        if axis.dtype is not i32 or 2 * axis.numel() != rot or not axis.is_contiguous():
+            raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: axis {axis.dtype} {tuple(axis.shape)}, "
+                                  f"expected contiguous int32 [{rot // 2}]")
+        ax = axis.data_ptr()
+    if q_weight is not None:
+        qw = _norm_weight(name, "q_weight", q_weight, D, f32)
+    if k_weight is not None:
+        kw = _norm_weight(name, "k_weight", k_weight, D, f32)
+    if not (q.get_device() == k.get_device() == v.get_device() == q_out.get_device() == q_indptr.get_device()
+            == kv_len.get_device() == block_table.get_device() == workspace.get_device() == device == _current_device()
+            and (freq is None or inv_freq.get_device() == device) and (pos is None or positions.get_device() == device)
+            and (ax is None or axis.get_device() == device) and (qw is None or q_weight.get_device() == device)
+            and (kw is None or k_weight.get_device() == device)):
+        _refuse_place(name, cache, q=q, k=k, v=v, q_out=q_out, q_indptr=q_indptr, block_table=block_table, kv_len=kv_len,
+                      workspace=workspace, inv_freq=inv_freq, positions=positions, axis=axis, q_weight=q_weight,
+                      k_weight=k_weight)
+    code = call(
+        cache.address, q.data_ptr(), q_stride[0], q_stride[1], k.data_ptr(), k_stride[0], k_stride[1], v.data_ptr(),
+        v_stride[0], v_stride[1], q_shape[1], q_shape[0], q_indptr.data_ptr(), B, block_table.data_ptr(),
+        table_shape[1], kv_len.data_ptr(), freq, pos, n_axes, ax, rot, 1 if interleaved else 0, position_base, qw, kw,
+        norm_eps, q_out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _call_stream(stream, device))
+    if code != SPEC_OK:
+        _check(code, name)
+
+
+def _norm_weight(name, key, w, D, f32):
+    if w.dtype is not f32 or w.shape != (D,) or not w.is_contiguous():
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: {key} {w.dtype} {tuple(w.shape)}, expected contiguous "
+                              f"float32 [{D}]")
+    return w.data_ptr()
+
+
+def spec_kv_read8(cache, k_out, v_out, out_indptr, block_table, workspace, first=None, stream=None) -> None:
+    """Entries of an 8-bit cache back in 16 bits: rows out_indptr[b] ..
+    out_indptr[b+1]-1 of k_out and v_out [R, n_heads, D] (the cache's dtype; either
+    may be None) become the entries of sequence b from first[b] (int32 [B], None: 0)
+    on.  out_indptr int32 [B+1], block_table int32 [B, width]; a workspace of
+    make_append_workspace."""
+    name = "spec_kv_read8"
+    _cache_of(name, cache, SpecKvCache8, "make_kv_cache8")
+    dt, n_heads, D, _, device, i32, _, _ = cache.expected
+    outs = [t for t in (k_out, v_out) if t is not None]
+    if not outs:
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: no output")
+    _positions_first(name, cache, *outs)
+    if any(t.shape[1] != n_heads for t in outs):
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: outputs {[tuple(t.shape) for t in outs]}, {n_heads} cache heads")
+    B = out_indptr.numel() - 1
+    if out_indptr.dtype is not i32 or out_indptr.dim() != 1 or B < 1 or not out_indptr.is_contiguous() \
+            or block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != B \
+            or not block_table.is_contiguous():
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: out_indptr {out_indptr.dtype} {tuple(out_indptr.shape)}, "
+                              f"block_table {block_table.dtype} {tuple(block_table.shape)}, expected contiguous int32 "
+                              f"[B + 1] and [B, width]")
+    if first is not None and (first.dtype is not i32 or first.shape != (B,) or not first.is_contiguous()):
+        raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: first {first.dtype} {tuple(first.shape)}, expected "
+                              f"contiguous int32 [{B}]")
+    if not (all(t.get_device() == device for t in outs) and out_indptr.get_device() == block_table.get_device()
+            == workspace.get_device() == device == _current_device() and (first is None or first.get_device() == device)):
+        _refuse_place(name, cache, k_out=k_out, v_out=v_out, out_indptr=out_indptr, block_table=block_table,
+                      workspace=workspace, first=first)
+    strides = [(None, 0, 0) if t is None else (t.data_ptr(), t.stride(0), t.stride(1)) for t in (k_out, v_out)]
+    _check((_lib or load()).spec_kv_read8(
+        cache.address, out_indptr.data_ptr(), outs[0].shape[0], B, block_table.data_ptr(), block_table.shape[1],
+        None if first is None else first.data_ptr(), *strides[0], *strides[1], workspace.data_ptr(), workspace.nbytes,
+        _call_stream(stream, device)), name)
+
+
+def spec_prefix_attention8(cache, q, out, q_indptr, block_table, kv_len, workspace, prefix_table=None, prefix_len=0,
+                           draft_mask=None, scale=None, lse=None, stream=None) -> None:
+    """spec_prefix_attention over an 8-bit cache (from make_kv_cache8); q and out
+    in the cache's 16-bit dtype, the rest alike."""
+    _cache_of("spec_prefix_attention8", cache, SpecKvCache8, "make_kv_cache8")
+    _attention((_lib or load()).spec_prefix_attention8, "spec_prefix_attention8", cache, q, out, q_indptr, block_table,
+               kv_len, workspace, prefix_table, prefix_len, draft_mask, scale, lse, stream)

@@ -1,0 +1,498 @@
+// append8.cuh — the append with norms of query and key heads and rotary
+// positions in one launch, to a cache of 16 bits or of 8, and the read-back of the
+// 8-bit cache.
+//
+// Norm.  y = x * rsqrt(mean(x^2) + eps) * w over a head's dims, in fp32, before the
+// rotation; the result is rounded once, to the cache's type or to its code.
+//
+// Layout.  As in kvappend.cuh a CTA puts its positions' cosines and sines into
+// shared memory; a row (position and head) is held by `lanes` neighbouring lanes
+// of a warp, two 16-byte vectors a lane (those that turn together where pairs are
+// halves apart), so the norm's sum is a few shuffles and every value is read once.
+//
+// Blocks of the 8-bit cache.  A block's scale needs all its new rows, so one CTA
+// owns each block: the CTA whose tile of positions holds the block's first new
+// position (its lead) takes all of it, queries included.  A unit is a block of one
+// key head and side; it is held in registers by as many warps as keep four rows'
+// steps a lane (block * lanes / 128), so values are rotated and normalised once,
+// reduced to their maximum and written.  Where older entries stand in the block
+// its scale only rises, and when it does their codes are rewritten (exact but
+// for e4m3's subnormals).
+//
+// Bound by the copies: q, k, v read once, q (16 bits) and codes written once.
+#pragma once
+
+#include "kvappend.cuh"
+#include "paged8.cuh"
+
+namespace specv {
+
+constexpr int kA8Threads = 256, kA8Warps = kA8Threads / 32;
+constexpr int kA8MaxOwn = kAppendMaxTile + 63;  // positions of a CTA: its tile's and the rest of its last block
+constexpr int kA8Steps = 4;                     // rows' steps of a unit that a lane holds
+
+struct Append8Params {
+  AppendParams a;  // (its cache: the 16-bit pools; with 8 bits only n_heads counts)
+  Paged8View c8;
+  const float *q_weight, *k_weight;  // [D] or null: no norm
+  float eps;
+  int lanes;       // lanes of a row: a power of two
+  int unit_warps;  // warps of a unit
+};
+
+// What a lane holds of a row.
+struct RowLane {
+  int d0, d1;   // the first dims of its two vectors
+  bool live, two, paired;
+};
+
+// A row's two vectors in fp32, normalised and rotated.  `row`: the row in memory
+// (pairs whose other dim is in no vector of the lane are read there).  All lanes
+// of a warp call it.
+template <typename T, bool kInterleaved>
+__device__ __forceinline__ void row_values(const Append8Params& p, const RowLane& u, uint4 av, uint4 bv, bool turn,
+                                           const float* weight, const uint16_t* row, const float2* cs, float (&x)[8],
+                                           float (&y)[8]) {
+  const int half = p.a.half, rot = 2 * half;
+  unpack8<T>(av, x);
+  unpack8<T>(bv, y);
+  float r = 1.f;
+  if (p.q_weight != nullptr || p.k_weight != nullptr) {
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], fmaf(y[e], y[e], sum));
+    for (int s = p.lanes >> 1; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    if (weight != nullptr) {
+      r = __frsqrt_rn(sum / static_cast<float>(p.a.D) + p.eps);
+      if (u.live) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * r * weight[u.d0 + e];
+        if (u.two) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = y[e] * r * weight[u.d1 + e];
+        }
+      }
+    }
+  }
+  if (!turn || !u.live) return;
+  if (u.paired || kInterleaved) {
+    if (kInterleaved && u.d0 >= rot) return;
+    float c[8], s[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int f = kInterleaved ? (u.d0 >> 1) + e : u.d0 + e;
+      const float2 w = f < half ? cs[unit_index(f, half)] : make_float2(1.f, 0.f);
+      c[e] = w.x;
+      s[e] = w.y;
+    }
+    if (!kInterleaved) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float t = fmaf(y[e], -s[e], x[e] * c[e]);
+        y[e] = fmaf(x[e], s[e], y[e] * c[e]);
+        x[e] = t;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (u.d0 + 2 * e < rot) {
+          const float t = fmaf(x[2 * e + 1], -s[e], x[2 * e] * c[e]);
+          x[2 * e + 1] = fmaf(x[2 * e], s[e], x[2 * e + 1] * c[e]);
+          x[2 * e] = t;
+        }
+        if (u.two && u.d1 + 2 * e < rot) {  // d1 = d0 + 8
+          const float t = fmaf(y[2 * e + 1], -s[e + 4], y[2 * e] * c[e + 4]);
+          y[2 * e + 1] = fmaf(y[2 * e], s[e + 4], y[2 * e + 1] * c[e + 4]);
+          y[2 * e] = t;
+        }
+      }
+    }
+  } else if (u.d0 < rot && (half & 7) != 0) {  // pairs not a whole number of vectors apart
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      if (v == 1 && !u.two) break;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int d = (v == 0 ? u.d0 : u.d1) + e;
+        if (d >= rot) continue;
+        const bool first = d < half;
+        const int o = first ? d + half : d - half;
+        const float2 w = cs[unit_index(first ? d : o, half)];
+        float z = Pack16<T>::up(row[o]);
+        if (weight != nullptr) z = z * r * weight[o];
+        if (v == 0)
+          x[e] = fmaf(z, first ? -w.y : w.y, x[e] * w.x);
+        else
+          y[e] = fmaf(z, first ? -w.y : w.y, y[e] * w.x);
+      }
+    }
+  }
+}
+
+template <typename T, bool kInterleaved, bool k8>
+__global__ void __launch_bounds__(kA8Threads, 2) append_norm_kernel(const __grid_constant__ Append8Params p) {
+  extern __shared__ float2 ap_units[];  // [positions of the CTA][half]
+  __shared__ int64_t s_dst[kA8MaxOwn];  // element offset of the entry in the pools, -1: not written
+  __shared__ int64_t s_entry[kA8MaxOwn];
+  __shared__ int s_page[kA8MaxOwn];
+  __shared__ int8_t s_live[kA8MaxOwn], s_is_lead[kA8MaxOwn];
+  __shared__ int16_t s_lead[kA8MaxOwn + 1];  // places of the leads, then the end
+  __shared__ int s_begin, s_end, s_leads;
+  __shared__ float s_top[kA8Warps];
+  const PagedBatch& batch = p.a.batch;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n0 = static_cast<int>(blockIdx.x) * p.a.tile;
+  const int tile = min(p.a.tile, batch.N - n0);
+  const int block = 1 << p.c8.block_shift;
+  // positions looked at: the tile's, and with 8 bits those that its last block may reach to
+  const int look = k8 ? min(p.a.tile + block - 1, batch.N - n0) : tile;
+  const int64_t page_stride = k8 ? p.c8.page_stride : p.a.cache.page_stride;
+  const int64_t slot_stride = k8 ? p.c8.slot_stride : p.a.cache.slot_stride;
+  const int64_t n_pages = k8 ? p.c8.n_pages : p.a.cache.n_pages;
+  grid_dep_launch();
+  grid_dep_wait();
+
+  // row offsets that do not begin at 0 or do not ascend are reported
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kA8Threads + kA8Threads - 1 - tid; i < batch.B;
+       i += static_cast<int64_t>(gridDim.x) * kA8Threads) {
+    const int b = static_cast<int>(i), at = batch.q_indptr[b];
+    if (at > batch.q_indptr[b + 1] || (b == 0 && at != 0) || (b == batch.B - 1 && batch.q_indptr[b + 1] > batch.N))
+      atomicOr(batch.status, kStatusBadCache);
+  }
+
+  // ---- the entries of the positions, a thread each ----
+  for (int t = tid; t < look; t += kA8Threads) {
+    const int n = n0 + t;
+    const int b = find_seq_alone(batch, n);
+    int64_t dst = -1, entry = 0;
+    bool live = false, lead = true;
+    int page = -1;
+    if (b >= 0) {
+      const SeqSpan s = seq_span(batch, b);
+      live = n >= s.first && n < s.first + s.n;  // not so only where q_indptr is not ascending
+      entry = n + s.shift;  // by the lengths as given, not clamped: no length moves an entry over an older one
+      lead = !live || n == s.first || (entry & (block - 1)) == 0;
+      if (live && entry >= 0 && entry < static_cast<int64_t>(batch.table_width) * batch.page_size &&
+          in_bounds(b < batch.B && entry / batch.page_size < batch.table_width, batch.status))
+        page = batch.block_table[static_cast<int64_t>(b) * batch.table_width + entry / batch.page_size];
+      if (page >= 0 && page < n_pages)
+        dst = page * page_stride + (entry % batch.page_size) * slot_stride;
+      else
+        atomicOr(batch.status, kStatusBadCache);
+    }
+    if (in_bounds(t < kA8MaxOwn, batch.status)) {
+      s_live[t] = live;
+      s_dst[t] = dst;
+      s_entry[t] = entry;
+      s_page[t] = page;
+      s_is_lead[t] = lead;
+    }
+  }
+  __syncthreads();
+  int begin = 0, end = tile;
+  if (k8) {
+    // the positions from the tile's first lead to the next tile's
+    if (warp == 0) {
+      int from = look, to = look, leads = 0;
+      for (int t0 = 0; t0 < look; t0 += 32) {
+        const int t = t0 + lane;
+        const bool lead = t < look && s_is_lead[t];
+        const unsigned mine = __ballot_sync(0xffffffffu, lead && t < tile), next = __ballot_sync(0xffffffffu, lead && t >= tile);
+        if (from == look && mine != 0u) from = t0 + __ffs(mine) - 1;
+        if (to == look && next != 0u) to = t0 + __ffs(next) - 1;
+        if (lead && t < tile && in_bounds(leads + __popc(mine & ((1u << lane) - 1)) < kA8MaxOwn, batch.status))
+          s_lead[leads + __popc(mine & ((1u << lane) - 1))] = static_cast<int16_t>(t);
+        leads += __popc(mine);
+      }
+      if (lane == 0) {
+        if (from == look) to = look;  // no lead: nothing to do
+        s_lead[leads] = static_cast<int16_t>(to);
+        s_begin = from;
+        s_end = to;
+        s_leads = leads;
+      }
+    }
+    __syncthreads();
+    begin = s_begin;
+    end = s_end;
+    if (begin >= end) return;
+  }
+
+  // ---- cosines and sines, one thread per frequency and several positions ----
+  if (p.a.half > 0) {
+    const int groups = kA8Threads / p.a.half;  // half <= 256
+    const int f = tid % p.a.half, g = tid / p.a.half;
+    if (g < groups) {
+      const double turns = static_cast<double>(p.a.inv_freq[f]) * 0.15915494309189533577;  // 1 / (2 pi)
+      const uint64_t turn64 = __double2ull_rn((turns - floor(turns)) * 0x1p63) << 1;
+      int a = p.a.axis != nullptr ? p.a.axis[f] : 0;
+      if (a < 0 || a >= p.a.n_axes) {
+        atomicOr(batch.status, kStatusBadCache);
+        a = 0;
+      }
+      for (int t = begin + g; t < end; t += groups) {
+        const int64_t pos = p.a.positions != nullptr
+                                ? static_cast<int64_t>(p.a.positions[static_cast<int64_t>(a) * batch.N + n0 + t])
+                                : p.a.position_base + s_entry[t];
+        if (in_bounds(t < kA8MaxOwn && unit_index(f, p.a.half) >= 0 && unit_index(f, p.a.half) < p.a.half, batch.status))
+          ap_units[(t - begin) * p.a.half + unit_index(f, p.a.half)] = unit_of(pos, turn64);
+      }
+    }
+    __syncthreads();
+  }
+
+  // ---- this lane's part of every row it visits ----
+  const int vpr = p.a.D >> 3, upr = (vpr + 1) >> 1, rows_at_once = 32 / p.lanes;
+  const int u = lane & (p.lanes - 1), row_of_warp = lane / p.lanes;
+  const int hv = p.a.half >> 3;
+  RowLane my;
+  my.live = u < upr;
+  my.paired = !kInterleaved && (p.a.half & 7) == 0 && u < hv;
+  const int v0 = my.paired ? u : !kInterleaved && (p.a.half & 7) == 0 ? 2 * hv + 2 * (u - hv) : 2 * u;
+  const int v1 = my.paired ? u + hv : v0 + 1;
+  my.two = v1 < vpr;
+  my.d0 = 8 * v0;
+  my.d1 = 8 * v1;
+  const int Hq = p.a.n_q_heads, Hk = p.a.cache.n_heads;
+
+  // ---- queries (and with a 16-bit cache keys and values): (position, row) pairs in one sequence ----
+  {
+    const int rows = k8 ? Hq : Hq + 2 * Hk, at_once = kA8Warps * rows_at_once;
+    const int r0 = warp * rows_at_once + row_of_warp;
+    const int t_step = at_once / rows, row_step = at_once - t_step * rows;
+    int t_at = begin + r0 / rows, row_at = r0 % rows;
+    int t_first = begin + (warp * rows_at_once) / rows;  // of the warp's first row: uniform
+    int row_first = (warp * rows_at_once) % rows;
+    while (t_first < end) {
+      uint4 a[kAppendBatch], b[kAppendBatch];
+      int ts[kAppendBatch], rs[kAppendBatch];
+#pragma unroll
+      for (int i = 0; i < kAppendBatch; ++i) {
+        const bool inside = my.live && t_at < end &&
+                            in_bounds(t_at >= 0 && t_at < kA8MaxOwn && row_at >= 0 && row_at < rows && my.d0 + 8 <= p.a.D &&
+                                          (!my.two || my.d1 + 8 <= p.a.D),
+                                      batch.status);
+        ts[i] = inside && s_live[t_at] ? t_at : -1;
+        rs[i] = row_at;
+        a[i] = b[i] = make_uint4(0, 0, 0, 0);
+        if (ts[i] >= 0) {
+          const uint16_t* src = p.a.row_src(n0 + t_at, row_at);
+          a[i] = ld_once(src + my.d0);
+          if (my.two) b[i] = ld_once(src + my.d1);
+        }
+        t_at += t_step;
+        row_at += row_step;
+        if (row_at >= rows) {
+          row_at -= rows;
+          ++t_at;
+        }
+        t_first += t_step;
+        row_first += row_step;
+        if (row_first >= rows) {
+          row_first -= rows;
+          ++t_first;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAppendBatch; ++i) {
+        const int t = max(ts[i], begin), row = rs[i];
+        const int64_t n = n0 + t;
+        const bool is_q = row < Hq, is_v = row >= Hq + Hk;
+        float x[8], y[8];
+        row_values<T, kInterleaved>(p, my, a[i], b[i], ts[i] >= 0 && !is_v, is_v ? nullptr : is_q ? p.q_weight : p.k_weight,
+                                    p.a.row_src(n, row), ap_units + (t - begin) * p.a.half, x, y);
+        if (ts[i] < 0) continue;
+        uint16_t* dst;
+        if (is_q) {
+          dst = p.a.q_out + (n * Hq + row) * p.a.D;
+        } else {
+          if (s_dst[t] < 0 || !in_bounds(s_dst[t] <= (n_pages - 1) * page_stride + (batch.page_size - 1) * slot_stride,
+                                         batch.status))
+            continue;
+          dst = (is_v ? p.a.cache.v : p.a.cache.k) + s_dst[t] + (row - Hq - (is_v ? Hk : 0)) * p.a.cache.head_stride;
+        }
+        *reinterpret_cast<uint4*>(dst + my.d0) = pack8<T>(x);
+        if (my.two) *reinterpret_cast<uint4*>(dst + my.d1) = pack8<T>(y);
+      }
+    }
+  }
+  if (!k8) return;
+
+  // ---- keys and values of the 8-bit cache, a unit at a time ----
+  const int units = s_leads * 2 * Hk, at_once = kA8Warps / p.unit_warps;
+  const int unit_of_warp = warp / p.unit_warps, part = warp - unit_of_warp * p.unit_warps;
+  const float most = 240.f * two_to(Scale8<T>::kHigh);
+  for (int first = 0; first < units; first += at_once) {  // all warps make the same rounds
+    const int unit = first + unit_of_warp;
+    const bool here = unit < units && unit_of_warp < at_once;
+    const int l = here ? unit / (2 * Hk) : 0, h = here ? unit - l * 2 * Hk : 0;
+    const bool is_v = h >= Hk;
+    const int head = is_v ? h - Hk : h;
+    const int t0 = s_lead[l];
+    const int64_t dst0 = s_dst[t0];
+    const bool writes = here && s_live[t0] && dst0 >= 0;
+    const int slot = static_cast<int>(s_entry[t0] % batch.page_size), behind = slot & (block - 1);
+    // never more than the block holds, whatever row offsets that do not ascend make of it
+    const int rows = min(s_lead[l + 1] - t0, block - behind);
+    uint8_t* const pool = is_v ? p.c8.v : p.c8.k;
+    uint8_t* const scale = (is_v ? p.c8.v_scales : p.c8.k_scales) + (writes ? p.c8.scale_at(s_page[t0], slot, head) : 0);
+    int was = Scale8<T>::kLow;
+    if (writes && behind > 0) was = stored_exponent<T>(*scale);
+    uint4 a[kA8Steps], b[kA8Steps];
+#pragma unroll
+    for (int i = 0; i < kA8Steps; ++i) {
+      const int r = (i * p.unit_warps + part) * rows_at_once + row_of_warp;
+      a[i] = b[i] = make_uint4(0, 0, 0, 0);
+      if (writes && my.live && r < rows && in_bounds(t0 + r < end, batch.status)) {
+        const uint16_t* src = p.a.row_src(n0 + t0 + r, Hq + h);
+        a[i] = ld_once(src + my.d0);
+        b[i] = ld_once(src + my.d1);  // D is a multiple of 16: there are always two
+      }
+    }
+    float x[kA8Steps][8], y[kA8Steps][8], top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kA8Steps; ++i) {
+      const int r = (i * p.unit_warps + part) * rows_at_once + row_of_warp;
+      const bool mine = writes && r < rows;
+      const int t = t0 + (mine ? r : 0);
+      row_values<T, kInterleaved>(p, my, a[i], b[i], mine && !is_v, is_v ? nullptr : p.k_weight,
+                                  p.a.row_src(n0 + t, Hq + h), ap_units + (t - begin) * p.a.half, x[i], y[i]);
+      if (mine && my.live) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(finite_abs(x[i][e]), finite_abs(y[i][e])));
+      }
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    if (p.unit_warps > 1) {
+      if (lane == 0) s_top[warp] = top;
+      __syncthreads();
+      for (int w = 0; w < p.unit_warps; ++w)
+        if (unit_of_warp < at_once) top = fmaxf(top, s_top[unit_of_warp * p.unit_warps + w]);
+      __syncthreads();
+    }
+    if (!writes) continue;
+    const int now = max(block_exponent<T>(top), was);
+    if (lane == 0 && part == 0) *scale = static_cast<uint8_t>(now + 127);
+    if (behind > 0 && now > was) {  // older codes to the new scale
+      const int64_t block0 = dst0 - behind * p.c8.slot_stride + head * p.c8.head_stride;
+      const float less = two_to(max(was - now, -126));
+      for (int r = part * rows_at_once + row_of_warp; r < behind; r += p.unit_warps * rows_at_once) {
+        if (!my.live) continue;
+        uint8_t* const at = pool + block0 + r * p.c8.slot_stride;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          uint2* const c = reinterpret_cast<uint2*>(at + (v == 0 ? my.d0 : my.d1));
+          float z[8];
+          values8(*c, 1.f, z);
+          *c = code8(z, less, INFINITY);
+        }
+      }
+    }
+    const float inv = two_to(-now);
+#pragma unroll
+    for (int i = 0; i < kA8Steps; ++i) {
+      const int r = (i * p.unit_warps + part) * rows_at_once + row_of_warp;
+      if (r >= rows || !my.live ||
+          !in_bounds(dst0 + r * p.c8.slot_stride <=
+                         (n_pages - 1) * page_stride + (batch.page_size - 1) * slot_stride && slot + r < batch.page_size,
+                     batch.status))
+        continue;
+      uint8_t* const at = pool + dst0 + r * p.c8.slot_stride + head * p.c8.head_stride;
+      *reinterpret_cast<uint2*>(at + my.d0) = code8(x[i], inv, most);
+      *reinterpret_cast<uint2*>(at + my.d1) = code8(y[i], inv, most);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// read-back: entries of the sequences as rows of 16 bits
+// ---------------------------------------------------------------------------
+struct Read8Params {
+  Paged8View c8;
+  PagedBatch batch;      // q_indptr: the rows out; kv_len: not used
+  const int32_t* first;  // [B] the entry of each sequence's first row, or null: 0
+  uint16_t *k_out, *v_out;  // either may be null
+  int64_t k_ps, k_hs, v_ps, v_hs;
+  int D, tile;           // positions of a CTA
+};
+
+constexpr int kR8Threads = 256, kR8MaxTile = 64, kR8Batch = 4;
+
+// A thread turns 16 codes (16 bytes) into 32 bytes, four in flight; the CTA's
+// (row, side, head, 16 dims) in one sequence, so that neighbours write neighbouring
+// bytes.  Bound by HBM: one byte read, two written a value.
+template <typename T>
+__global__ void __launch_bounds__(kR8Threads) read8_kernel(const __grid_constant__ Read8Params p) {
+  __shared__ int64_t s_src[kR8MaxTile];  // offset of the entry in the pools, -1: zeros, -2: no row
+  __shared__ int s_page[kR8MaxTile], s_slot[kR8MaxTile];
+  const PagedBatch& batch = p.batch;
+  const int tid = threadIdx.x;
+  const int n0 = static_cast<int>(blockIdx.x) * p.tile, tile = min(p.tile, batch.N - n0);
+  grid_dep_launch();
+  grid_dep_wait();
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kR8Threads + kR8Threads - 1 - tid; i < batch.B;
+       i += static_cast<int64_t>(gridDim.x) * kR8Threads) {
+    const int b = static_cast<int>(i), at = batch.q_indptr[b];
+    if (at > batch.q_indptr[b + 1] || (b == 0 && at != 0) || (b == batch.B - 1 && batch.q_indptr[b + 1] > batch.N))
+      atomicOr(batch.status, kStatusBadCache);
+  }
+  for (int t = tid; t < tile; t += kR8Threads) {
+    const int n = n0 + t, b = find_seq_alone(batch, n);
+    int64_t src = -2;
+    int page = -1, slot = 0;
+    if (b >= 0 && n < batch.q_indptr[b + 1]) {
+      const int64_t entry = static_cast<int64_t>(p.first != nullptr ? p.first[b] : 0) + (n - batch.q_indptr[b]);
+      src = -1;
+      if (entry >= 0 && entry < static_cast<int64_t>(batch.table_width) * batch.page_size &&
+          in_bounds(b < batch.B, batch.status)) {
+        page = batch.block_table[static_cast<int64_t>(b) * batch.table_width + entry / batch.page_size];
+        slot = static_cast<int>(entry % batch.page_size);
+      }
+      if (page >= 0 && page < p.c8.n_pages)
+        src = page * p.c8.page_stride + slot * p.c8.slot_stride;
+      else
+        atomicOr(batch.status, kStatusBadCache);
+    }
+    if (in_bounds(t < kR8MaxTile, batch.status)) {
+      s_src[t] = src;
+      s_page[t] = page;
+      s_slot[t] = slot;
+    }
+  }
+  __syncthreads();
+  const int chunks = p.D >> 4, side = p.c8.n_heads * chunks, per_row = 2 * side, total = tile * per_row;
+  for (int i0 = tid; i0 < total; i0 += kR8Threads * kR8Batch) {
+    uint4 c[kR8Batch];
+    int e[kR8Batch];
+    uint16_t* dst[kR8Batch];
+#pragma unroll
+    for (int k = 0; k < kR8Batch; ++k) {
+      const int i = i0 + k * kR8Threads, t = i / per_row, x = i - t * per_row;
+      const bool is_v = x >= side;
+      const int y = is_v ? x - side : x, head = y / chunks, d = (y - head * chunks) * 16;
+      dst[k] = nullptr;
+      c[k] = make_uint4(0, 0, 0, 0);
+      e[k] = 0;
+      if (i >= total || !in_bounds(t < kR8MaxTile, batch.status) || s_src[t] == -2) continue;
+      uint16_t* const out = is_v ? p.v_out : p.k_out;
+      if (out == nullptr) continue;
+      dst[k] = out + static_cast<int64_t>(n0 + t) * (is_v ? p.v_ps : p.k_ps) + head * (is_v ? p.v_hs : p.k_hs) + d;
+      if (s_src[t] < 0) continue;
+      c[k] = *reinterpret_cast<const uint4*>((is_v ? p.c8.v : p.c8.k) + s_src[t] + head * p.c8.head_stride + d);
+      e[k] = stored_exponent<T>((is_v ? p.c8.v_scales : p.c8.k_scales)[p.c8.scale_at(s_page[t], s_slot[t], head)]);
+    }
+#pragma unroll
+    for (int k = 0; k < kR8Batch; ++k) {
+      if (dst[k] == nullptr) continue;
+      const float scale = two_to(e[k]);
+      float x[8], y[8];
+      values8(make_uint2(c[k].x, c[k].y), scale, x);
+      values8(make_uint2(c[k].z, c[k].w), scale, y);
+      reinterpret_cast<uint4*>(dst[k])[0] = pack8<T>(x);
+      reinterpret_cast<uint4*>(dst[k])[1] = pack8<T>(y);
+    }
+  }
+}
+
+}  // namespace specv

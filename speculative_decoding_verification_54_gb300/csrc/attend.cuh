@@ -98,6 +98,8 @@ struct AttendParams {
   float scale_log2;  // scale * log2(e)
   int n_q_heads, n_heads, group;
   int tok_tile;      // positions of a row tile: 128 / group
+  int block;         // positions of an item: two row tiles, with 8-bit codes one
+  int narrow;        // up to so many of them the item counts as narrow in the line
   int n_ctas;
   int64_t* begin;    // [n_ctas + 1] where the CTAs' parts begin
   // rows' own places: [0] for the prefix, if there is one, then for their
@@ -117,6 +119,22 @@ struct AttendParams {
   __device__ __forceinline__ int64_t place(int line, int64_t row) const {
     return line == 1 && prefix_len > 0 ? static_cast<int64_t>(batch.N) * n_q_heads + row : row;
   }
+  // the cache's entries one by one: 16-bit values as they are
+  static constexpr bool kCodes = false;
+  __device__ __forceinline__ int64_t head_stride() const { return cache.head_stride; }
+  __device__ __forceinline__ int64_t entry_at(int64_t page, int slot) const {
+    return page * cache.page_stride + slot * cache.slot_stride;
+  }
+  template <typename T>
+  __device__ __forceinline__ void scales(int64_t, int, int, float&, float&) const {}
+  template <typename T>
+  __device__ __forceinline__ uint4 keys8(int64_t at, float) const {
+    return *reinterpret_cast<const uint4*>(cache.k + at);
+  }
+  template <typename T>
+  __device__ __forceinline__ uint32_t values2(int64_t at, float) const {
+    return *reinterpret_cast<const uint32_t*>(cache.v + at);
+  }
 };
 
 // ---------------------------------------------------------------------------
@@ -131,13 +149,13 @@ __device__ __forceinline__ int block_tiles(const AttendParams& p, const SeqSpan&
   const int kv = static_cast<int>(s.kv);
   const int64_t last = p.draft_mask != nullptr
                            ? kv
-                           : static_cast<int64_t>(kv) - s.n + min(static_cast<int64_t>(s.n), static_cast<int64_t>(rb + 1) * 2 * p.tok_tile);
+                           : static_cast<int64_t>(kv) - s.n + min(static_cast<int64_t>(s.n), static_cast<int64_t>(rb + 1) * p.block);
   return last <= 0 ? 0 : static_cast<int>((last + kAtTile - 1) / kAtTile);
 }
 
-// Row tiles of a block.
-__device__ __forceinline__ int block_rows(int positions, int tok_tile, int rb) {
-  return positions - rb * 2 * tok_tile > tok_tile ? 2 : 1;
+// Row tiles of a block (with 8-bit codes: 2 for a wide one).
+__device__ __forceinline__ int block_rows(const AttendParams& p, int positions, int rb) {
+  return positions - rb * p.block > p.narrow ? 2 : 1;
 }
 
 // Weights are in units of some 400 clocks: a key tile took 3,250 with two row
@@ -162,9 +180,9 @@ struct SeqWeight {
 };
 __device__ __forceinline__ SeqWeight seq_weight(const AttendParams& p, const SeqSpan& s) {
   SeqWeight w = {0, 0};
-  for (int rb = 0; rb * 2 * p.tok_tile < s.n; ++rb) {
+  for (int rb = 0; rb * p.block < s.n; ++rb) {
     const int tiles = block_tiles(p, s, rb);
-    w.tiles_alone += static_cast<int64_t>(tiles) * tile_weight(block_rows(s.n, p.tok_tile, rb));
+    w.tiles_alone += static_cast<int64_t>(tiles) * tile_weight(block_rows(p, s.n, rb));
     w.items += tiles > 0;
   }
   return w;
@@ -172,9 +190,9 @@ __device__ __forceinline__ SeqWeight seq_weight(const AttendParams& p, const Seq
 
 // The rows of the blocks that see no key at all (fewer entries than new
 // positions, which the status word reports): the join finds no parts there.
-__device__ __noinline__ void no_tiles(const AttendParams& p, const SeqSpan& s) {
+inline __device__ __noinline__ void no_tiles(const AttendParams& p, const SeqSpan& s) {
   for (int i = 0; i < s.n; ++i) {
-    if (block_tiles(p, s, i / (2 * p.tok_tile)) > 0) continue;
+    if (block_tiles(p, s, i / p.block) > 0) continue;
     for (int h = 0; h < p.n_q_heads; ++h)
       if (in_bounds(s.first >= 0 && s.first + i < p.batch.N, p.batch.status))
         p.part_meta[p.place(1, static_cast<int64_t>(s.first + i) * p.n_q_heads + h)] = make_int4(-1, 0, 0, 0);
@@ -193,11 +211,11 @@ __device__ __forceinline__ PrefixItems prefix_items(const AttendParams& p) {
   PrefixItems L;
   L.positions = new_positions(p.batch);
   L.tiles = (p.prefix_len + kAtTile - 1) / kAtTile;
-  L.blocks = (L.positions + 2 * p.tok_tile - 1) / (2 * p.tok_tile);
+  L.blocks = (L.positions + p.block - 1) / p.block;
   L.tiles_alone = L.blocks == 0 ? 0
                                 : static_cast<int64_t>(L.tiles) *
                                       ((L.blocks - 1) * tile_weight(2) +
-                                       tile_weight(block_rows(L.positions, p.tok_tile, L.blocks - 1)));
+                                       tile_weight(block_rows(p, L.positions, L.blocks - 1)));
   return L;
 }
 
@@ -469,9 +487,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 #pragma unroll 1
           for (; a.head < p.n_heads && off < hi && ok; ++a.head) {
 #pragma unroll 1
-            for (int at = 0; at < s.n && ok; at += 2 * p.tok_tile) {
-              const int rb = at / (2 * p.tok_tile);
-              const int tiles = a.line == 0 ? pl.tiles : block_tiles(p, s, rb), w = block_rows(s.n, p.tok_tile, rb);
+            for (int at = 0; at < s.n && ok; at += p.block) {
+              const int rb = at / p.block;
+              const int tiles = a.line == 0 ? pl.tiles : block_tiles(p, s, rb), w = block_rows(p, s.n, rb);
               a.off = off;
               a.tiles = tiles;
               a.w = w;
@@ -942,14 +960,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 // 46).  Kept short: with the keys' steps unrolled by eight the join's code cost every
 // launch 1 us, called or not.
 // ---------------------------------------------------------------------------
-template <typename T, int D>
-__device__ __noinline__ void sum_row_again(const AttendParams& p, int n, int hq, float m, float inv, float m0, float4 o0) {
+template <typename T, int D, typename P>
+__device__ __noinline__ void sum_row_again(const P& p, int n, int hq, float m, float inv, float m0, float4 o0) {
   constexpr int kPer = D / 32;
   const int lane = threadIdx.x & 31, b = find_seq(p.batch, n, lane);
   if (b < 0) return;
   const SeqSpan s = seq_span(p.batch, b);
   const int kv = static_cast<int>(s.kv), first = s.first, count = s.n;
-  const int64_t in_page = (hq / p.group) * p.cache.head_stride;
+  const int64_t in_page = (hq / p.group) * p.head_stride();
   const uint16_t* const q = p.q + n * p.q_ps + hq * p.q_hs;
   float sum[kPer] = {};
   // the prefix's sum stands if it is finite
@@ -978,14 +996,16 @@ __device__ __noinline__ void sum_row_again(const AttendParams& p, int n, int hq,
       const bool inside = in_bounds(line == 0 || t >= entries || t / p.batch.page_size < p.batch.table_width, p.batch.status);
       const int page = seen && inside ? table[t / p.batch.page_size] : -1;
       const bool valid = page >= 0 && page < p.n_pages;  // others' keys and values read as zero (and are reported)
-      const int64_t at = valid ? page * p.cache.page_stride + (t % p.batch.page_size) * p.cache.slot_stride + in_page : 0;
+      const int64_t at = valid ? p.entry_at(page, t % p.batch.page_size) + in_page : 0;
+      float k_scale = 1.f, v_scale = 1.f;
+      if (P::kCodes && valid) p.template scales<T>(page, t % p.batch.page_size, hq / p.group, k_scale, v_scale);
       float dot = 0.f;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {  // four loads in flight
         uint4 k[4] = {};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (valid) k[i] = *reinterpret_cast<const uint4*>(p.cache.k + at + c + 8 * i);
+          if (valid) k[i] = p.template keys8<T>(at + c + 8 * i, k_scale);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float x[8], y[8];
@@ -1006,10 +1026,11 @@ __device__ __noinline__ void sum_row_again(const AttendParams& p, int n, int hq,
         for (int i = 0; i < 4; ++i) {
           const bool there = any >> (u + i) & 1;
           wu[i] = __shfl_sync(0xffffffffu, w, u + i);
-          const uint16_t* from = p.cache.v + __shfl_sync(0xffffffffu, at, u + i) + lane * kPer;
+          const int64_t from = __shfl_sync(0xffffffffu, at, u + i) + lane * kPer;
+          const float vs = P::kCodes ? __shfl_sync(0xffffffffu, v_scale, u + i) : 1.f;
           if (there) {
 #pragma unroll
-            for (int x = 0; x < kPer / 2; ++x) v[i][x] = reinterpret_cast<const uint32_t*>(from)[x];
+            for (int x = 0; x < kPer / 2; ++x) v[i][x] = p.template values2<T>(from + 2 * x, vs);
           }
         }
 #pragma unroll
@@ -1037,8 +1058,8 @@ __device__ __noinline__ void sum_row_again(const AttendParams& p, int n, int hq,
 // where the others are, so a row whose items were not split takes one round of
 // loads.
 // ---------------------------------------------------------------------------
-template <typename T, int D>
-__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p) {
+template <typename T, int D, typename P>
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ P p) {
   constexpr int kPer = D / 32;  // dims of a lane
   const int lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(p.batch.N) * p.n_q_heads;
@@ -1132,7 +1153,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 #pragma unroll
   for (int i = 0; i < kPer; ++i) finite = finite && fabsf(o[i]) < INFINITY;
   if (__any_sync(0xffffffffu, !finite) && l < INFINITY)  // l: as in all lanes
-    sum_row_again<T, D>(p, n, hq, m, inv, m0, make_float4(o0[0], o0[1], o0[kPer - 2], o0[kPer - 1]));
+    sum_row_again<T, D, P>(p, n, hq, m, inv, m0, make_float4(o0[0], o0[1], o0[kPer - 2], o0[kPer - 1]));
 }
 
 }  // namespace specv
