@@ -46,6 +46,28 @@ struct RowLane {
   bool live, two, paired;
 };
 
+// Two vectors whose dims' partners stand anywhere in the row: read one by one.  (Not
+// inlined: it would be most of the kernel's code, and the others waited for it.)
+struct Row16 {
+  float x[16];
+};
+template <typename T>
+__device__ __noinline__ Row16 turn_apart(Row16 v, int d0, int d1, int half, const uint16_t* row, const float2* cs,
+                                         const float* weight, float r) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int d = e < 8 ? d0 + e : d1 + e - 8;
+    if (d >= 2 * half) continue;
+    const bool first = d < half;
+    const int o = first ? d + half : d - half;
+    const float2 w = cs[unit_index(first ? d : o, half)];
+    float z = Pack16<T>::up(row[o]);
+    if (weight != nullptr) z = z * r * weight[o];
+    v.x[e] = fmaf(z, first ? -w.y : w.y, v.x[e] * w.x);
+  }
+  return v;
+}
+
 // A row's two vectors in fp32, normalised and rotated.  `row`: the row in memory
 // (pairs whose other dim is in no vector of the lane are read there).  All lanes
 // of a warp call it.
@@ -108,23 +130,17 @@ __device__ __forceinline__ void row_values(const Append8Params& p, const RowLane
       }
     }
   } else if (u.d0 < rot && (half & 7) != 0) {  // pairs not a whole number of vectors apart
+    Row16 v;
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      if (v == 1 && !u.two) break;
+    for (int e = 0; e < 8; ++e) {
+      v.x[e] = x[e];
+      v.x[8 + e] = y[e];
+    }
+    v = turn_apart<T>(v, u.d0, u.two ? u.d1 : rot, half, row, cs, weight, r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int d = (v == 0 ? u.d0 : u.d1) + e;
-        if (d >= rot) continue;
-        const bool first = d < half;
-        const int o = first ? d + half : d - half;
-        const float2 w = cs[unit_index(first ? d : o, half)];
-        float z = Pack16<T>::up(row[o]);
-        if (weight != nullptr) z = z * r * weight[o];
-        if (v == 0)
-          x[e] = fmaf(z, first ? -w.y : w.y, x[e] * w.x);
-        else
-          y[e] = fmaf(z, first ? -w.y : w.y, y[e] * w.x);
-      }
+    for (int e = 0; e < 8; ++e) {
+      x[e] = v.x[e];
+      y[e] = v.x[8 + e];
     }
   }
 }

@@ -37,8 +37,8 @@
 namespace specv {
 
 constexpr int kQ8Threads = 512;
-// 168 + 168 + 96 + 80 = 4 x 128, the launch's
-constexpr int kQ8SoftmaxRegs = 168, kQ8ConvertRegs = 96, kQ8OtherRegs = 80;
+// 184 + 184 + 80 + 64 = 4 x 128, the launch's
+constexpr int kQ8SoftmaxRegs = 184, kQ8ConvertRegs = 80, kQ8OtherRegs = 64;
 constexpr int kQ8Queue = 2;          // parts queued ahead
 constexpr float kQ8Unset = 3.0e38f;  // minus the reference of a row that has seen nothing
 
@@ -73,8 +73,8 @@ struct Q8Shared {
   static constexpr int kSlots = 32 * 1024 / (kAtTile * D);  // of the key ring and of the value ring
   uint64_t raw_full[2][kSlots], raw_empty[2][kSlots];       // [keys, values]
   uint64_t kc_full[2], kc_empty[2], vc_full[2], vc_empty[2];
-  uint64_t s_full[2], p_full, pv_done, o_free, q_full[2], q_empty[2], part_full[kQ8Queue], part_empty[kQ8Queue], done;
-  __align__(16) float neg_ref[kAtTile];       // minus the rows' references (log2)
+  uint64_t s_full[2], p_full[2], pv_done[2], meet[2], o_free, q_full[2], q_ready[2], q_empty[2], part_full[kQ8Queue], part_empty[kQ8Queue], done;
+  __align__(16) float neg_ref[2][kAtTile / 2];   // per group: minus its columns' references (log2)
   __align__(16) float cross[2][4][kAtTile / 2];  // per group: its warps' maxima or sums of the columns
   uint8_t scales[2][kSlots][16];              // [keys, values] of 8 keys each
   AtPart parts[kQ8Queue];
@@ -89,72 +89,71 @@ constexpr uint32_t q8_smem_bytes() {
 }
 static_assert(q8_smem_bytes<128>() <= 227 * 1024 && q8_smem_bytes<64>() <= 227 * 1024, "one CTA's shared memory");
 
-// Four codes to four 16-bit values (two words) times `scale`, a power of two as
-// two values of the type.
+// Four codes (a word) to four 16-bit values (two words) times 2^e.
 template <typename T>
 struct Codes;
 template <>
 struct Codes<__half> {
+  static constexpr bool kEvenOdd = false;
   uint32_t scale;
   __device__ __forceinline__ explicit Codes(int e) {
     const __half2 s = __float2half2_rn(two_to(e));
     scale = *reinterpret_cast<const uint32_t*>(&s);
   }
-  __device__ __forceinline__ uint32_t pair(uint16_t c) const {
-    const uint32_t h = half2_of_codes(c);
+  __device__ __forceinline__ uint32_t pair(uint32_t c) const {
+    const uint32_t h = half2_of_codes(static_cast<uint16_t>(c));
     uint32_t d;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(scale));
     return d;
   }
-  __device__ __forceinline__ void four(uint32_t w, uint32_t& lo, uint32_t& hi) const {
-    lo = pair(static_cast<uint16_t>(w));
-    hi = pair(static_cast<uint16_t>(w >> 16));
+  // whether the words need rare(), gathered over several of them
+  __device__ static __forceinline__ uint32_t rare_bits(uint32_t) { return 0; }
+  __device__ __forceinline__ bool is_rare(uint32_t) const { return false; }
+  __device__ __forceinline__ void four(uint32_t w, uint32_t& a, uint32_t& b) const {
+    a = pair(w);
+    b = pair(w >> 16);
   }
-  __device__ __forceinline__ void sixteen(const uint4& w, uint32_t (&d)[8]) const {
-    four(w.x, d[0], d[1]);
-    four(w.y, d[2], d[3]);
-    four(w.z, d[4], d[5]);
-    four(w.w, d[6], d[7]);
-  }
+  __device__ __forceinline__ void rare(uint32_t w, uint32_t& a, uint32_t& b) const { four(w, a, b); }
 };
 // A code's exponent and fraction bits, put where bf16's lowest exponent and highest
 // fraction bits are, read as the code's value times 2^-120: one exact product
-// with 2^(120 + e) gives the value.  (2^(120 + e) passes bf16's range for e > 7:
-// two products then.)  The code of NaN would read as 480: looked for apart.
+// with 2^(120 + e) gives the value.  A word's even codes and its odd ones share
+// masks, so the first word has codes 0 and 2 and the second 1 and 3 (kEvenOdd: the
+// queries are put in that order too, and the outputs' dims are read in it): six
+// logic operations a word, which run at half rate, where pairs in order take eight.
+// (The type's own conversion, e4m3 to fp16, takes 3 clocks a pair; the two steps
+// from there to bf16 six more.)  Apart, in rare(): the code of NaN, which would read as
+// 480, and e > 7, where 2^(120 + e) passes bf16's range and is two factors.
 template <>
 struct Codes<__nv_bfloat16> {
-  uint32_t scale, more;
-  __device__ __forceinline__ explicit Codes(int e) {
-    const uint32_t a = min(e, 7) + 247, b = max(e - 7, 0) + 127;  // biased exponents of 2^(120 + e) in two factors
+  static constexpr bool kEvenOdd = true;
+  uint32_t scale;
+  int e;
+  __device__ __forceinline__ explicit Codes(int e) : e(e) {
+    const uint32_t a = min(e, 7) + 247;  // biased exponent of 2^(120 + e)
     scale = a << 7 | a << 23;
-    more = b << 7 | b << 23;
   }
   __device__ static __forceinline__ uint32_t mul(uint32_t x, uint32_t y) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(y));
     return d;
   }
-  __device__ __forceinline__ uint32_t pair(uint32_t y) const {  // codes in the high bytes of the halves
-    return mul((y >> 4 & 0x07f007f0u) | (y & 0x80008000u), scale);
+  __device__ static __forceinline__ uint32_t rare_bits(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+  __device__ __forceinline__ bool is_rare(uint32_t bits) const { return (bits & 0x80808080u) != 0 || e > 7; }
+  __device__ __forceinline__ void four(uint32_t w, uint32_t& a, uint32_t& b) const {
+    a = mul((w << 4 & 0x07f007f0u) | (w << 8 & 0x80008000u), scale);
+    b = mul((w >> 4 & 0x07f007f0u) | (w & 0x80008000u), scale);
   }
-  __device__ __forceinline__ void sixteen(const uint4& w, uint32_t (&d)[8]) const {
-    const uint32_t c[4] = {w.x, w.y, w.z, w.w};
-    uint32_t nan = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      nan |= (c[i] & 0x7f7f7f7fu) + 0x01010101u;
-      d[2 * i] = pair(__byte_perm(c[i], 0, 0x1404));
-      d[2 * i + 1] = pair(__byte_perm(c[i], 0, 0x3424));
-    }
-    if (more != 0x3f803f80u) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = mul(d[i], more);
-    }
-    if (nan & 0x80808080u) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if ((c[i / 4] >> (8 * (i % 4)) & 0x7f) == 0x7f) d[i / 2] |= 0x7fffu << (16 * (i % 2));
-    }
+  __device__ __forceinline__ void rare(uint32_t w, uint32_t& a, uint32_t& b) const {
+    four(w, a, b);
+    const uint32_t more = max(e - 7, 0) + 127;
+    a = mul(a, more << 7 | more << 23);
+    b = mul(b, more << 7 | more << 23);
+    const uint32_t nan = rare_bits(w) & 0x80808080u;
+    if (nan & 0x80u) a |= 0x7fffu;
+    if (nan & 0x8000u) b |= 0x7fffu;
+    if (nan & 0x800000u) a |= 0x7fff0000u;
+    if (nan & 0x80000000u) b |= 0x7fff0000u;
   }
 };
 
@@ -174,6 +173,20 @@ __device__ __forceinline__ bool group_any(int g, bool c) {
 template <int kCount>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[kCount]);
 template <>
+__device__ __forceinline__ void tmem_load<8>(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+template <>
 __device__ __forceinline__ void tmem_load<16>(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
@@ -188,24 +201,9 @@ __device__ __forceinline__ void tmem_load<32>(uint32_t taddr, uint32_t (&r)[32])
   tmem_ld32_start(taddr, r);
   tmem_ld32_wait(r);
 }
-template <>
-__device__ __forceinline__ void tmem_load<64>(uint32_t taddr, uint32_t (&r)[64]) {
-  uint32_t a[32], b[32];
-  tmem_ld32_start(taddr, a);
-  tmem_ld32_start(taddr + 32, b);
-  tmem_ld32_wait(a);
-  tmem_ld32_wait(b);
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    r[i] = a[i];
-    r[i + 32] = b[i];
-  }
-}
-
 // One value of each of kCount columns a lane, reduced over the warp's 32 lanes in
 // halves: log2 steps that each halve what a lane holds, until it holds the
-// columns lane * kCount / 32 (kCount 32, 64) or, in lanes 2 c and 2 c + 1, column c
-// (kCount 16).
+// column `lane` (kCount 32) or, in lanes 2 c and 2 c + 1, column c (kCount 16).
 template <int kCount, typename Op>
 __device__ __forceinline__ void reduce_columns(float (&v)[kCount], int lane, Op op) {
 #pragma unroll
@@ -225,6 +223,12 @@ __device__ __forceinline__ void reduce_columns(float (&v)[kCount], int lane, Op 
   }
 }
 
+// How far (log2) a score may pass its row's reference: bf16 weights have fp32's
+// exponents, so 2^24 costs nothing (a row's reference is set once, as good as
+// always); fp16 weights stay below 2^15.
+template <typename T>
+constexpr float kQ8Rise = std::is_same<T, __half>::value ? kAtRise : 24.f;
+
 template <typename T, int D>
 struct Q8Softmax {
   const Attend8Params& p;
@@ -233,62 +237,82 @@ struct Q8Softmax {
   uint32_t tmem;
   int g, quad, lane, key;
   bool ok;
+  uint32_t steps;  // tiles this group has had
+  uint32_t meets;  // parts in which the groups met
 
-  __device__ __forceinline__ uint32_t tm_s(uint32_t j) const { return tmem + 128 * (j & 1) + (static_cast<uint32_t>(quad * 32) << 16); }
-  __device__ __forceinline__ uint32_t tm_o() const { return tmem + 256 + (static_cast<uint32_t>(quad * 32) << 16); }
+  __device__ __forceinline__ uint32_t lanes() const { return static_cast<uint32_t>(quad * 32) << 16; }
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.batch.status, kWaitLimitCycles));
   }
 
-  // Scores of the columns in a tile some of whose keys some rows do not see:
-  // -inf there.
-  template <int C>
-  __device__ __forceinline__ void hide(const AtPart& a, int t, uint32_t (&s)[C]) const {
+  // Which of C columns from col0 on see this thread's key of tile t, bit by column.
+  // (Loops that are not unrolled here and below: code that runs once a part or
+  // less, unrolled, made the kernel 580 KB, and it ran at the rate of its
+  // instruction fetches.)
+  __device__ __forceinline__ uint64_t seen(const AtPart& a, int t, int col0, int C) const {
     const int e = t * kAtTile + key;  // the entry
-    if (e < a.len && e < a.old) return;
+    if (e >= a.len) return 0;
+    if (e < a.old) return ~0ull;
     const int j = e - a.old;  // its place among the new ones
-    int tok = (g * C) / p.group, left = (tok + 1) * p.group - g * C;  // of a column's position the columns to come
-    bool sees = false;
-    auto look = [&]() {
-      sees = false;
-      if (e >= a.len || tok >= a.n0) return;
-      if (p.draft_mask == nullptr) {
+    uint64_t bits = 0;
+    const int last = min(a.n0, (col0 + C - 1) / p.group + 1);
+#pragma unroll 1
+    for (int tok = col0 / p.group; tok < last; ++tok) {
+      bool sees;
+      if (p.draft_mask == nullptr)
         sees = j <= a.first - a.seq_first + tok;
-      } else if (j < 64 && in_bounds(a.first >= 0 && a.first + tok < p.batch.N, p.batch.status)) {
-        sees = (p.draft_mask[a.first + tok] >> j & 1) != 0;
-      }
-    };
-    look();
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if (left == 0) {
-        ++tok;
-        look();
-        left = p.group;
-      }
-      --left;
-      if (!sees) s[c] = 0xff800000u;
+      else
+        sees = j < 64 && in_bounds(a.first >= 0 && a.first + tok < p.batch.N, p.batch.status) &&
+               (p.draft_mask[a.first + tok] >> j & 1) != 0;
+      if (!sees) continue;
+      const int from = max(tok * p.group - col0, 0), to = min((tok + 1) * p.group - col0, C);  // its columns
+      bits |= (to - from == 64 ? ~0ull : (1ull << (to - from)) - 1) << from;
     }
+    return bits;
   }
 
-  // One column of each kCount / 32 lanes' values (reduce_columns) to the group's place.
+  // The columns that reduce_columns left in this lane to the group's place.
   template <int C>
-  __device__ __forceinline__ void to_cross(const float (&v)[C]) const {
-    float* const at = sh.cross[g][quad];
-    if (C == 16) {
-      if ((lane & 1) == 0) at[lane / 2] = v[0];
-    } else {
-#pragma unroll
-      for (int c = 0; c < C / 32; ++c) at[lane * (C / 32) + c] = v[c];
-    }
+  __device__ __forceinline__ void to_cross(int c0, const float (&v)[C]) const {
+    float* const at = sh.cross[g][quad] + c0;
+    if (C == 32)
+      at[lane] = v[0];
+    else if ((lane & 1) == 0)
+      at[lane / 2] = v[0];
   }
 
-  // A part with C columns a group; `base`: tiles before it.
-  template <int C>
+  // The place of row `col` of the part among the parts' rows (times 1: of m and l,
+  // times D: of its output), or -1.
+  __device__ __forceinline__ int64_t place(const AtPart& a, int rows, int col) const {
+    if (col >= rows) return -1;
+    if (a.t0 != 0) {
+      const int cta = static_cast<int>(blockIdx.x);
+      return in_bounds(cta < p.n_ctas && col < p.slab_rows, p.batch.status) ? static_cast<int64_t>(cta) * p.slab_rows + col : -1;
+    }
+    const int tok = col / p.group;
+    if (!in_bounds(a.first >= 0 && a.first + tok < p.batch.N, p.batch.status)) return -1;
+    return p.place(a.line, static_cast<int64_t>(a.first + tok) * p.n_q_heads + a.head * p.group + (col - tok * p.group));
+  }
+  __device__ __forceinline__ void store_ml(const AtPart& a, int64_t at, int col, float m, float l) const {
+    if (at < 0) return;
+    (a.t0 == 0 ? p.part_ml : p.slab_ml)[at] = make_float2(m, l);
+    if (a.t0 == 0) p.part_meta[at] = row_item(a, static_cast<int>(blockIdx.x), col);
+  }
+
+  // A part, C columns a thread.  Wide: the groups share each tile, group g has
+  // columns g C .. g C + C - 1.  Otherwise they alternate tiles, each with all
+  // columns, a reference, sums and an O of its own, joined at the end, so that
+  // their chains of scores, weights and products overlap.  `base`: tiles before it.
+  template <int C, bool kWide>
   __device__ __forceinline__ void part(const AtPart& a, uint32_t base) {
-    constexpr float kTop = kAtTop<T>, kOver = kAtTop<T> + kAtRise;
-    float* const neg_ref = sh.neg_ref + g * C;
+    constexpr float kTop = kAtTop<T>, kOver = kAtTop<T> + kQ8Rise<T>;
+    constexpr int kStep = kWide ? 1 : 2;
+    constexpr int kChunk = C < 32 ? C : 32;  // columns in registers at a time (their scores are read twice)
+    float* const neg_ref = sh.neg_ref[g];
     float(&cross)[4][kAtTile / 2] = sh.cross[g];
+    uint8_t* const pt = pbuf + g * (kQ8PBytes / 2) + key * 128;
+    const uint32_t tm_o = tmem + 256 + 64 * g + lanes();
+    const int col0 = kWide ? g * C : 0;
     const int mine = quad * 32 + lane;  // this thread's column in what is done once a column
     const int tiles = a.t1 - a.t0, rows = a.n0 * p.group;
     // entries below this one are seen by all rows
@@ -298,52 +322,67 @@ struct Q8Softmax {
 #pragma unroll
     for (int c = 0; c < C / 2; ++c) l2[c] = 0;
     group_any(g, false);
+    const int i0 = kWide ? 0 : static_cast<int>((base & 1) ^ g);  // tile j is in S buffer j & 1
 #pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
+    for (int i = i0; i < tiles; i += kStep) {
       const uint32_t j = base + i;
+      const uint32_t tm_s = tmem + 128 * (j & 1) + col0 + lanes();
       const int t = a.t0 + i;
-      uint32_t s[C];
       ok = wait(&sh.s_full[j & 1], (j >> 1) & 1) && ok;
       tc_fence_after();
-      auto scores = [&]() {
-        tmem_load<C>(tm_s(j) + g * C, s);
-        if (open - t * kAtTile < kAtTile) hide<C>(a, t, s);
-      };
-      // scores minus the references, in place; whether one passes its reference by far
-      auto against = [&]() {
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
+      const bool ragged = open - t * kAtTile < kAtTile;
+      uint64_t bits = ~0ull;
+      if (ragged) bits = seen(a, t, col0, C);
+      auto scores = [&](int c0, uint32_t (&s)[kChunk]) {
+        tmem_load<kChunk>(tm_s + c0, s);
+        if (ragged) {
+          const uint32_t see = static_cast<uint32_t>(bits >> c0);
 #pragma unroll
-        for (int c = 0; c < C; c += 4) {
-          const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(neg_ref + c);
-          float x[4];
-          f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, n.x), x[0], x[1]);
-          f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), scale2, n.y), x[2], x[3]);
-          top[c / 4 % 2 * 2] = max3(top[c / 4 % 2 * 2], x[0], x[1]);
-          top[c / 4 % 2 * 2 + 1] = max3(top[c / 4 % 2 * 2 + 1], x[2], x[3]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[c + k] = __float_as_uint(x[k]);
+          for (int c = 0; c < kChunk; ++c) s[c] = see >> c & 1 ? s[c] : 0xff800000u;
         }
-        return fmaxf(max3(top[0], top[1], top[2]), top[3]) > kOver;
       };
-      scores();
-      const bool rise = against();
-      bool waited = false;
-      if (group_any(g, rise || !ok)) {
+      // two scores minus their references
+      auto minus_ref = [&](const uint32_t* s, uint64_t n, float& x, float& y) {
+        f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[0]), __uint_as_float(s[1])), f32x2(p.scale_log2, p.scale_log2), n), x, y);
+      };
+      // whether one passes its reference by far
+      float over = -INFINITY;
+#pragma unroll 1
+      for (int c0 = 0; c0 < C; c0 += kChunk) {
+        uint32_t s[kChunk];
+        scores(c0, s);
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kChunk; c += 4) {
+          const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(neg_ref + c0 + c);
+          float x, y;
+          minus_ref(s + c, n.x, x, y);
+          top[0] = max3(top[0], x, y);
+          minus_ref(s + c + 2, n.y, x, y);
+          top[1] = max3(top[1], x, y);
+        }
+        over = max3(over, top[0], top[1]);
+      }
+      bool waited = steps == 0;
+      if (group_any(g, over > kOver || !ok)) {
         // (O may be multiplied: the last product into it is complete)
-        if (ok && j > 0) ok = wait(&sh.pv_done, (j - 1) & 1);
+        if (ok && !waited) ok = wait(&sh.pv_done[g], (steps - 1) & 1);
         waited = true;
         if (group_any(g, !ok)) {
           ok = false;
           return;
         }
         tc_fence_after();
-        scores();
-        float top[C];
+#pragma unroll 1
+        for (int c0 = 0; c0 < C; c0 += kChunk) {
+          uint32_t s[kChunk];
+          float top[kChunk];
+          scores(c0, s);
 #pragma unroll
-        for (int c = 0; c < C; ++c) top[c] = __uint_as_float(s[c]);
-        reduce_columns<C>(top, lane, [](float x, float y) { return fmaxf(x, y); });
-        to_cross<C>(top);
+          for (int c = 0; c < kChunk; ++c) top[c] = __uint_as_float(s[c]);
+          reduce_columns<kChunk>(top, lane, [](float x, float y) { return fmaxf(x, y); });
+          to_cross<kChunk>(c0, top);
+        }
         group_any(g, false);
         if (mine < C) {
           const float m = fmaxf(max3(cross[0][mine], cross[1][mine], cross[2][mine]), cross[3][mine]) * p.scale_log2;
@@ -353,113 +392,158 @@ struct Q8Softmax {
           if (up) neg_ref[mine] = kTop - m;
         }
         group_any(g, false);
+        if (i > i0) {
 #pragma unroll
-        for (int c = 0; c < C / 2; ++c) {
-          float x, y;
-          f32x2_split(l2[c], x, y);
-          l2[c] = f32x2(x * cross[0][2 * c], y * cross[0][2 * c + 1]);
-        }
-        if (i > 0 && (D == 128 || quad < 2)) {
-#pragma unroll
-          for (int c = 0; c < C; c += 16) {
-            uint32_t o[16];
-            tmem_load<16>(tm_o() + g * C + c, o);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * cross[0][c + x]);
-            tmem_st16(tm_o() + g * C + c, o);
+          for (int c = 0; c < C / 2; ++c) {
+            float x, y;
+            f32x2_split(l2[c], x, y);
+            l2[c] = f32x2(x * cross[0][2 * c], y * cross[0][2 * c + 1]);
           }
-          tmem_st_wait();
+          if (D == 128 || quad < 2) {
+#pragma unroll 1
+            for (int c = 0; c < C; c += 16) {
+              uint32_t o[16];
+              tmem_load<16>(tm_o + c, o);
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * cross[0][c + x]);
+              tmem_st16(tm_o + c, o);
+            }
+            tmem_st_wait();
+          }
         }
-        scores();
-        against();
       }
       // weights: the sums keep them in 32 bits, P in 16 (half a step off at most)
-      uint32_t w[C / 2];
 #pragma unroll
-      for (int c = 0; c < C / 2; ++c) {
-        const float e0 = ex2(__uint_as_float(s[2 * c])), e1 = ex2(__uint_as_float(s[2 * c + 1]));
-        l2[c] = add_f32x2(l2[c], f32x2(e0, e1));
-        w[c] = Pack16<T>::pack(e0, e1);
-      }
-      if (!waited && j > 0) ok = wait(&sh.pv_done, (j - 1) & 1) && ok;
-      // P: [key][64 rows], two tiles, 128-byte swizzle
+      for (int c0 = 0; c0 < C; c0 += kChunk) {
+        uint32_t s[kChunk], w[kChunk / 2];
+        scores(c0, s);
 #pragma unroll
-      for (int c = 0; c < C; c += 8) {
-        const int col = g * C + c;
-        uint8_t* const at = pbuf + (col >> 6) * (kQ8PBytes / 2) + key * 128 + (((col >> 3 & 7) ^ (key & 7)) << 4);
-        *reinterpret_cast<uint4*>(at) = make_uint4(w[c / 2], w[c / 2 + 1], w[c / 2 + 2], w[c / 2 + 3]);
+        for (int c = 0; c < kChunk; c += 4) {
+          const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(neg_ref + c0 + c);
+          float x[4];
+          minus_ref(s + c, n.x, x[0], x[1]);
+          minus_ref(s + c + 2, n.y, x[2], x[3]);
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            const float e0 = ex2(x[k]), e1 = ex2(x[k + 1]);
+            l2[(c0 + c + k) / 2] = add_f32x2(l2[(c0 + c + k) / 2], f32x2(e0, e1));
+            w[(c + k) / 2] = Pack16<T>::pack(e0, e1);
+          }
+        }
+        if (!waited) {
+          ok = wait(&sh.pv_done[g], (steps - 1) & 1) && ok;
+          waited = true;
+        }
+        // P: [key][64 rows], 128-byte swizzle
+#pragma unroll
+        for (int c = 0; c < kChunk; c += 8)
+          *reinterpret_cast<uint4*>(pt + (((c0 + c) / 8 ^ (key & 7)) << 4)) =
+              make_uint4(w[c / 2], w[c / 2 + 1], w[c / 2 + 2], w[c / 2 + 3]);
       }
       fence_async_shared();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full);
+      if (lane == 0) mbar_arrive(&sh.p_full[g]);
+      ++steps;
     }
 
     // ---- the part's results ----
-    ok = wait(&sh.pv_done, (base + tiles - 1) & 1) && ok;
+    if (steps > 0) ok = wait(&sh.pv_done[g], (steps - 1) & 1) && ok;
     if (group_any(g, !ok)) {
       ok = false;
       return;
     }
-    tc_fence_after();
-    const int cta = static_cast<int>(blockIdx.x);
-    {
-      float sum[C];
 #pragma unroll
-      for (int c = 0; c < C / 2; ++c) f32x2_split(l2[c], sum[2 * c], sum[2 * c + 1]);
-      reduce_columns<C>(sum, lane, [](float x, float y) { return x + y; });
-      to_cross<C>(sum);
+    for (int c0 = 0; c0 < C; c0 += kChunk) {
+      float sum[kChunk];
+#pragma unroll
+      for (int c = 0; c < kChunk / 2; ++c) f32x2_split(l2[c0 / 2 + c], sum[2 * c], sum[2 * c + 1]);
+      reduce_columns<kChunk>(sum, lane, [](float x, float y) { return x + y; });
+      to_cross<kChunk>(c0, sum);
     }
     group_any(g, false);
-    const int col0 = g * C + mine;
-    if (mine < C && col0 < rows) {
-      const float l = (cross[0][mine] + cross[1][mine]) + (cross[2][mine] + cross[3][mine]);
-      const float n = neg_ref[mine];
-      const float2 ml = make_float2(n == kQ8Unset ? -INFINITY : -n, l);
-      const int tok = col0 / p.group;
-      if (a.t0 == 0) {
-        const int64_t row = p.place(a.line, static_cast<int64_t>(a.first + tok) * p.n_q_heads + a.head * p.group + (col0 - tok * p.group));
-        if (in_bounds(a.first >= 0 && a.first + tok < p.batch.N, p.batch.status)) {
-          p.part_ml[row] = ml;
-          p.part_meta[row] = row_item(a, cta, col0);
-        }
-      } else if (in_bounds(cta < p.n_ctas && col0 < p.slab_rows, p.batch.status)) {
-        p.slab_ml[static_cast<int64_t>(cta) * p.slab_rows + col0] = ml;
+    float l = 0.f;
+    if (mine < C) l = (cross[0][mine] + cross[1][mine]) + (cross[2][mine] + cross[3][mine]);
+    // the lane's dim, in the converted values' order
+    const int at = quad * 32 + lane, dim = Codes<T>::kEvenOdd ? (at & ~3) | (at & 1) << 1 | (at >> 1 & 1) : at;
+    float* const out = (a.t0 == 0 ? p.part_o : p.slab_o) + dim;
+    const bool has_dims = D == 128 || quad < 2;
+    int64_t* const places = reinterpret_cast<int64_t*>(cross[1]);  // of the columns that this group writes
+    if (kWide) {
+      group_any(g, false);  // all sums have been read
+      if (mine < C) {
+        places[mine] = place(a, rows, col0 + mine);
+        store_ml(a, places[mine], col0 + mine, neg_ref[mine] == kQ8Unset ? -INFINITY : -neg_ref[mine], l);
       }
-    }
-    if (D == 128 || quad < 2) {
-      const int dim = quad * 32 + lane;
+      group_any(g, false);
+      tc_fence_after();
+      if (has_dims) {
 #pragma unroll 1
-      for (int c = 0; c < C; c += 16) {
-        uint32_t o[16];
-        tmem_load<16>(tm_o() + g * C + c, o);
-        int col = g * C + c, tok = col / p.group, h = col - tok * p.group;
+        for (int c = 0; c < C; c += 8) {
+          uint32_t o[8];
+          tmem_load<8>(tm_o + c, o);
 #pragma unroll
-        for (int x = 0; x < 16; ++x, ++col) {
-          if (col < rows) {
-            if (a.t0 == 0) {
-              const int64_t row = p.place(a.line, static_cast<int64_t>(a.first + tok) * p.n_q_heads + a.head * p.group + h);
-              if (in_bounds(a.first >= 0 && a.first + tok < p.batch.N, p.batch.status))
-                p.part_o[row * D + dim] = __uint_as_float(o[x]);
-            } else if (in_bounds(cta < p.n_ctas && col < p.slab_rows, p.batch.status)) {
-              p.slab_o[(static_cast<int64_t>(cta) * p.slab_rows + col) * D + dim] = __uint_as_float(o[x]);
-            }
-          }
-          if (++h == p.group) {
-            h = 0;
-            ++tok;
+          for (int x = 0; x < 8; ++x)
+            if (places[c + x] >= 0) out[places[c + x] * D] = __uint_as_float(o[x]);
+        }
+      }
+      tc_fence_before();
+      group_any(g, false);  // the places and the references may be written again
+    } else {
+      if (mine < C) cross[0][mine] = l;
+      // both groups' references, sums and products are there
+      auto meet = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.meet[i]);
+        return wait(&sh.meet[i], meets & 1);
+      };
+      ok = meet(0) && ok;
+      if (group_any(g, !ok)) {
+        ok = false;
+        return;
+      }
+      tc_fence_after();
+      // group g joins its half of the columns; a group without a tile has sums of 0
+      constexpr int kHalf = C / 2;
+      float* const factor = cross[3];  // [2][kHalf]
+      if (mine < kHalf) {
+        const int c = g * kHalf + mine;
+        const float n0 = sh.neg_ref[0][c], n1 = sh.neg_ref[1][c], m = fmaxf(-n0, -n1);
+        const float f0 = n0 == kQ8Unset ? 0.f : ex2(-n0 - m), f1 = n1 == kQ8Unset ? 0.f : ex2(-n1 - m);
+        // (a part of one tile has one O, in the group of its buffer: the other is not looked at)
+        factor[mine] = tiles > 1 || (base & 1) == 0 ? f0 : -1.f;
+        factor[kHalf + mine] = tiles > 1 || (base & 1) != 0 ? f1 : -1.f;
+        places[mine] = place(a, rows, c);
+        store_ml(a, places[mine], c, m == -kQ8Unset ? -INFINITY : m, sh.cross[0][0][c] * f0 + sh.cross[1][0][c] * f1);
+      }
+      group_any(g, false);
+      if (has_dims) {
+        const uint32_t from = tmem + 256 + lanes() + g * kHalf;
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 8) {
+          uint32_t x0[8], x1[8];
+          tmem_load<8>(from + c, x0);
+          tmem_load<8>(from + 64 + c, x1);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float f0 = factor[c + x], f1 = factor[kHalf + c + x];
+            float v = f0 < 0.f ? 0.f : __uint_as_float(x0[x]) * f0;
+            if (f1 >= 0.f) v += __uint_as_float(x1[x]) * f1;
+            if (places[c + x] >= 0) out[places[c + x] * D] = v;
           }
         }
       }
+      tc_fence_before();
+      ok = meet(1) && ok;  // the sums' places and the references may be written again
+      ++meets;
     }
-    tc_fence_before();
-    group_any(g, false);  // the sums' places and the references may be written again
+    __syncwarp();
     if (lane == 0) mbar_arrive(&sh.o_free);
   }
 };
 
-// columns a softmax group has for a part of so many rows
-__device__ __forceinline__ int q8_columns(int rows) { return rows <= 32 ? 16 : rows <= 64 ? 32 : 64; }
+// columns of a part's products; above 64 the softmax groups share each tile
+__device__ __forceinline__ int q8_columns(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_constant__ Attend8Params p) {
@@ -499,8 +583,12 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
       mbar_init(&sh.part_full[i], 1);
       mbar_init(&sh.part_empty[i], 15);  // eight softmax warps, four converters, the issuer, the two loaders
     }
-    mbar_init(&sh.p_full, 8);
-    mbar_init(&sh.pv_done, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&sh.p_full[g], 4);
+      mbar_init(&sh.pv_done[g], 1);
+      mbar_init(&sh.meet[g], 8);
+      mbar_init(&sh.q_ready[g], 4);
+    }
     mbar_init(&sh.o_free, 8);
     mbar_init(&sh.done, 1);
     fence_mbar_init();
@@ -658,6 +746,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
       const uint64_t q_desc = smem_desc_k128(smem_u32(qbuf)), v_desc = smem_desc_mn128(smem_u32(vbuf), kHalfBytes),
                      p_desc = smem_desc_mn128(smem_u32(pbuf), kQ8PBytes / 2);
       uint32_t base = 0;  // tiles before this part
+      uint32_t ph_p[2] = {0, 0};
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, status, kWaitLimitCycles));
@@ -669,12 +758,13 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
         if (!wait(&sh.part_full[q], (n / kQ8Queue) & 1)) break;
         const int line = __shfl_sync(0xffffffffu, sh.parts[q].line, 0);
         const int tiles = __shfl_sync(0xffffffffu, sh.parts[q].t1 - sh.parts[q].t0, 0);
-        const int columns = 2 * q8_columns(__shfl_sync(0xffffffffu, sh.parts[q].n0, 0) * p.group);
+        const int columns = q8_columns(__shfl_sync(0xffffffffu, sh.parts[q].n0, 0) * p.group);
+        const bool wide = columns == 128;
         if (lane == 0) mbar_arrive(&sh.part_empty[q]);
         if (line < 0) break;
         const uint32_t id_qk = idesc_f16_f32(kBf16, false, kAtTile, columns);
         const uint32_t id_pv = idesc_f16_f32(kBf16, true, kAtTile, columns) | 1u << 15;  // A too has K over its rows
-        if (!wait(&sh.q_full[n & 1], (n >> 1) & 1)) break;
+        if (!wait(Codes<T>::kEvenOdd ? &sh.q_ready[n & 1] : &sh.q_full[n & 1], (n >> 1) & 1)) break;
         // scores of the part's tile i
         auto qk = [&](int i) {
           const uint32_t j = base + i, b = j & 1;
@@ -698,14 +788,19 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
           const uint32_t j = base + i, b = j & 1;
           if (!wait(&sh.vc_full[b], (j >> 1) & 1)) break;
           if (i == 0 && n > 0 && !wait(&sh.o_free, (n - 1) & 1)) break;
-          if (!wait(&sh.p_full, j & 1)) break;
+          // the weights: of both groups, or of the one that has this tile
+          if ((wide || b == 0) && !wait(&sh.p_full[0], ph_p[0]++ & 1)) break;
+          if ((wide || b == 1) && !wait(&sh.p_full[1], ph_p[1]++ & 1)) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t ad = v_desc + b * (kTileBytes >> 4);
+            const uint32_t g = wide ? 0 : b;
+            const uint64_t ad = v_desc + b * (kTileBytes >> 4), bd = p_desc + g * (kQ8PBytes / 2 >> 4);
+            const bool more = i >= (wide ? 1 : 2);
 #pragma unroll
             for (int k = 0; k < kAtTile / 16; ++k)
-              tc_mma(utm + 256, ad + k * (2048 >> 4), p_desc + k * (2048 >> 4), id_pv, i > 0 || k > 0);
-            tc_commit(&sh.pv_done);
+              tc_mma(utm + 256 + 64 * g, ad + k * (2048 >> 4), bd + k * (2048 >> 4), id_pv, more || k > 0);
+            if (wide || b == 0) tc_commit(&sh.pv_done[0]);
+            if (wide || b == 1) tc_commit(&sh.pv_done[1]);
             tc_commit(&sh.vc_empty[b]);
           }
           __syncwarp();
@@ -814,14 +909,36 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
       const int at = D == 128 ? c ^ (key & 7) : c ^ (key >> 1 & 3);
       return *reinterpret_cast<const uint4*>(tile + key * D + at * 16);
     };
+    auto any_rare = [&](const Codes<T>& conv, const uint4 (&w)[D / 16]) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        bits |= Codes<T>::rare_bits(w[c].x) | Codes<T>::rare_bits(w[c].y) | Codes<T>::rare_bits(w[c].z) | Codes<T>::rare_bits(w[c].w);
+      return __any_sync(0xffffffffu, conv.is_rare(bits)) != 0;
+    };
 #pragma unroll 1
     for (uint32_t n = 0; ok; ++n) {
       const int q = n % kQ8Queue;
       if (!wait(&sh.part_full[q], (n / kQ8Queue) & 1)) break;
-      const int line = sh.parts[q].line, t0 = sh.parts[q].t0, tiles = sh.parts[q].t1 - t0, len = sh.parts[q].len;
+      const int line = sh.parts[q].line, t0 = sh.parts[q].t0, tiles = sh.parts[q].t1 - t0, len = sh.parts[q].len,
+                columns = q8_columns(sh.parts[q].n0 * p.group);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.part_empty[q]);
       if (line < 0) break;
+      if (Codes<T>::kEvenOdd) {
+        // the queries' dims in the order of the converted keys'
+        if (!wait(&sh.q_full[n & 1], (n >> 1) & 1)) break;
+        uint8_t* const qt = qbuf + (n & 1) * kTileBytes;
+        for (int x = key; x < columns * 8 * kHalves; x += 128) {
+          uint4* const at = reinterpret_cast<uint4*>(qt + (x / (columns * 8)) * kHalfBytes + (x % (columns * 8)) * 16);
+          const uint4 w = *at;
+          *at = make_uint4(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632), __byte_perm(w.z, w.w, 0x5410),
+                           __byte_perm(w.z, w.w, 0x7632));
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_ready[n & 1]);
+      }
 #pragma unroll 1
       for (int i = 0; i < tiles && ok; ++i) {
         const uint32_t j = base + i, b = j & 1, slot = j % kSlots, use = j / kSlots;
@@ -831,18 +948,35 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
         tc_fence_after();
         {
           const uint8_t* const tile = ring + slot * kRawBytes;
+          const uint32_t dst = tmem + lanes + 384 + (D / 2) * b;
           const Codes<T> conv(stored_exponent<T>(sh.scales[0][slot][key >> 3]));
+          uint4 w[D / 16];
 #pragma unroll
-          for (int c = 0; c < D / 16; c += 4) {
-            uint32_t w[32];
+          for (int c = 0; c < D / 16; ++c) w[c] = codes(tile, c);
+          if (!any_rare(conv, w)) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t d[8];
-              conv.sixteen(codes(tile, c + x), d);
+            for (int c = 0; c < D / 16; c += 4) {
+              uint32_t d[32];
 #pragma unroll
-              for (int y = 0; y < 8; ++y) w[8 * x + y] = d[y];
+              for (int x = 0; x < 4; ++x) {
+                conv.four(w[c + x].x, d[8 * x], d[8 * x + 1]);
+                conv.four(w[c + x].y, d[8 * x + 2], d[8 * x + 3]);
+                conv.four(w[c + x].z, d[8 * x + 4], d[8 * x + 5]);
+                conv.four(w[c + x].w, d[8 * x + 6], d[8 * x + 7]);
+              }
+              tmem_st32(dst + 8 * c, d);
             }
-            tmem_st32(tmem + lanes + 384 + (D / 2) * b + 8 * c, w);
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              const uint4 x = codes(tile, c);
+              uint32_t d[8];
+              conv.rare(x.x, d[0], d[1]);
+              conv.rare(x.y, d[2], d[3]);
+              conv.rare(x.z, d[4], d[5]);
+              conv.rare(x.w, d[6], d[7]);
+              tmem_st8(dst + 8 * c, d);
+            }
           }
           tmem_st_wait();
         }
@@ -861,15 +995,35 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
           const Codes<T> conv(stored_exponent<T>(sh.scales[1][slot][key >> 3]));
           const bool live = (t0 + i) * kAtTile + key < len;
           uint8_t* const dst = vbuf + b * kTileBytes + key * 128;
+          uint4 w[D / 16];
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t w[8];
-            conv.sixteen(codes(tile, c), w);
+          for (int c = 0; c < D / 16; ++c) w[c] = live ? codes(tile, c) : make_uint4(0, 0, 0, 0);
+          // 8 dims: one 16-byte vector
+          auto put = [&](int at, const uint32_t* d) {
+            *reinterpret_cast<uint4*>(dst + (at / 8) * kHalfBytes + (((at % 8) ^ (key & 7)) << 4)) = make_uint4(d[0], d[1], d[2], d[3]);
+          };
+          if (!any_rare(conv, w)) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int at = 2 * c + x;  // 8 dims: one 16-byte vector
-              *reinterpret_cast<uint4*>(dst + (at / 8) * kHalfBytes + (((at % 8) ^ (key & 7)) << 4)) =
-                  live ? make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]) : make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t d[8];
+              conv.four(w[c].x, d[0], d[1]);
+              conv.four(w[c].y, d[2], d[3]);
+              conv.four(w[c].z, d[4], d[5]);
+              conv.four(w[c].w, d[6], d[7]);
+              put(2 * c, d);
+              put(2 * c + 1, d + 4);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              const uint4 x = live ? codes(tile, c) : make_uint4(0, 0, 0, 0);
+              uint32_t d[8];
+              conv.rare(x.x, d[0], d[1]);
+              conv.rare(x.y, d[2], d[3]);
+              conv.rare(x.z, d[4], d[5]);
+              conv.rare(x.w, d[6], d[7]);
+              put(2 * c, d);
+              put(2 * c + 1, d + 4);
             }
           }
         }
@@ -884,7 +1038,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
     }
   } else {
     regs_up<kQ8SoftmaxRegs>();
-    Q8Softmax<T, D> sm = {p, sh, pbuf, tmem, warp >> 2, warp & 3, lane, (warp & 3) * 32 + lane, true};
+    Q8Softmax<T, D> sm = {p, sh, pbuf, tmem, warp >> 2, warp & 3, lane, (warp & 3) * 32 + lane, true, 0, 0};
     uint32_t base = 0;
 #pragma unroll 1
     for (uint32_t n = 0;; ++n) {
@@ -897,11 +1051,13 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
       if (a.line < 0) break;
       const int columns = q8_columns(a.n0 * p.group);
       if (columns == 16)
-        sm.template part<16>(a, base);
+        sm.template part<16, false>(a, base);
       else if (columns == 32)
-        sm.template part<32>(a, base);
+        sm.template part<32, false>(a, base);
+      else if (columns == 64)
+        sm.template part<64, false>(a, base);
       else
-        sm.template part<64>(a, base);
+        sm.template part<64, true>(a, base);
       if (!sm.ok) break;
       base += a.t1 - a.t0;
     }
