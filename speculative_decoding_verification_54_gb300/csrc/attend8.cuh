@@ -74,9 +74,15 @@ struct Q8Shared {
   uint64_t raw_full[2][kSlots], raw_empty[2][kSlots];       // [keys, values]
   uint64_t kc_full[2], kc_empty[2], vc_full[2], vc_empty[2];
   uint64_t s_full[2], p_full[2], pv_done[2], meet[2], o_free, q_full[2], q_ready[2], q_empty[2], part_full[kQ8Queue], part_empty[kQ8Queue], done;
-  __align__(16) float neg_ref[2][kAtTile / 2];   // per group: minus its columns' references (log2)
-  __align__(16) float cross[2][4][kAtTile / 2];  // per group: its warps' maxima or sums of the columns
-  uint8_t scales[2][kSlots][16];              // [keys, values] of 8 keys each
+  __align__(16) float neg_ref[2][kAtTile / 2];  // per group: minus its columns' references (log2)
+  float unit[2];                                // log2 of the unit of the groups' O
+  int8_t scales[2][kSlots][16];                 // [keys, values] exponents of 8 keys each
+  int8_t key_exp[4][16];                        // of the keys of tile j % 4
+  int16_t raw_unit[kSlots], v_unit[2];          // log2 of the unit that a tile's values have: in the ring, converted
+  int8_t raw_wide[kSlots], v_wide[2];           // whether they are converted to bf16 (else fp16)
+  int16_t q_exp[2];                             // log2 of the unit of a part's queries
+  int8_t q_bf16[2];                             // whether they stay bf16
+  uint32_t row_max[kAtTile];
   AtPart parts[kQ8Queue];
   uint32_t tmem;
 };
@@ -89,75 +95,36 @@ constexpr uint32_t q8_smem_bytes() {
 }
 static_assert(q8_smem_bytes<128>() <= 227 * 1024 && q8_smem_bytes<64>() <= 227 * 1024, "one CTA's shared memory");
 
-// Four codes (a word) to four 16-bit values (two words) times 2^e.
-template <typename T>
-struct Codes;
-template <>
-struct Codes<__half> {
-  static constexpr bool kEvenOdd = false;
-  uint32_t scale;
-  __device__ __forceinline__ explicit Codes(int e) {
-    const __half2 s = __float2half2_rn(two_to(e));
-    scale = *reinterpret_cast<const uint32_t*>(&s);
-  }
-  __device__ __forceinline__ uint32_t pair(uint32_t c) const {
-    const uint32_t h = half2_of_codes(static_cast<uint16_t>(c));
+// Four codes (a word) to four fp16 values (two words): exact, NaN kept.  3 clocks a
+// pair (a warp on its SM quarter); to bf16, which has no such instruction, it takes 8
+// clocks of logic a pair and more for NaN (below).  So the products are taken in
+// fp16 wherever that is exact.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& a, uint32_t& b) {
+  a = half2_of_codes(static_cast<uint16_t>(w));
+  b = half2_of_codes(static_cast<uint16_t>(w >> 16));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(y));
+  return d;
+}
+// The same to bf16, times 2^e with e in [-227, 7]: a code's exponent and fraction
+// bits, put where bf16's lowest exponent and highest fraction bits are, read as its
+// value times 2^-120; one product with 2^(120 + e).  The code of NaN would read as 480.
+__device__ __forceinline__ void codes_bf16(uint32_t w, int e, uint32_t& a, uint32_t& b) {
+  const uint32_t f = static_cast<uint32_t>(e + 247) << 7, scale = f | f << 16;
+  auto pair = [&](uint32_t y) {  // codes in the halves' high bytes
     uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(scale));
-    return d;
-  }
-  // whether the words need rare(), gathered over several of them
-  __device__ static __forceinline__ uint32_t rare_bits(uint32_t) { return 0; }
-  __device__ __forceinline__ bool is_rare(uint32_t) const { return false; }
-  __device__ __forceinline__ void four(uint32_t w, uint32_t& a, uint32_t& b) const {
-    a = pair(w);
-    b = pair(w >> 16);
-  }
-  __device__ __forceinline__ void rare(uint32_t w, uint32_t& a, uint32_t& b) const { four(w, a, b); }
-};
-// A code's exponent and fraction bits, put where bf16's lowest exponent and highest
-// fraction bits are, read as the code's value times 2^-120: one exact product
-// with 2^(120 + e) gives the value.  A word's even codes and its odd ones share
-// masks, so the first word has codes 0 and 2 and the second 1 and 3 (kEvenOdd: the
-// queries are put in that order too, and the outputs' dims are read in it): six
-// logic operations a word, which run at half rate, where pairs in order take eight.
-// (The type's own conversion, e4m3 to fp16, takes 3 clocks a pair; the two steps
-// from there to bf16 six more.)  Apart, in rare(): the code of NaN, which would read as
-// 480, and e > 7, where 2^(120 + e) passes bf16's range and is two factors.
-template <>
-struct Codes<__nv_bfloat16> {
-  static constexpr bool kEvenOdd = true;
-  uint32_t scale;
-  int e;
-  __device__ __forceinline__ explicit Codes(int e) : e(e) {
-    const uint32_t a = min(e, 7) + 247;  // biased exponent of 2^(120 + e)
-    scale = a << 7 | a << 23;
-  }
-  __device__ static __forceinline__ uint32_t mul(uint32_t x, uint32_t y) {
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(y));
-    return d;
-  }
-  __device__ static __forceinline__ uint32_t rare_bits(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
-  __device__ __forceinline__ bool is_rare(uint32_t bits) const { return (bits & 0x80808080u) != 0 || e > 7; }
-  __device__ __forceinline__ void four(uint32_t w, uint32_t& a, uint32_t& b) const {
-    a = mul((w << 4 & 0x07f007f0u) | (w << 8 & 0x80008000u), scale);
-    b = mul((w >> 4 & 0x07f007f0u) | (w & 0x80008000u), scale);
-  }
-  __device__ __forceinline__ void rare(uint32_t w, uint32_t& a, uint32_t& b) const {
-    four(w, a, b);
-    const uint32_t more = max(e - 7, 0) + 127;
-    a = mul(a, more << 7 | more << 23);
-    b = mul(b, more << 7 | more << 23);
-    const uint32_t nan = rare_bits(w) & 0x80808080u;
-    if (nan & 0x80u) a |= 0x7fffu;
-    if (nan & 0x8000u) b |= 0x7fffu;
-    if (nan & 0x800000u) a |= 0x7fff0000u;
-    if (nan & 0x80000000u) b |= 0x7fff0000u;
-  }
-};
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"((y >> 4 & 0x07f007f0u) | (y & 0x80008000u)), "r"(scale));
+    const uint32_t nan = (y & 0x7f007f00u) + 0x01000100u;
+    return d | (nan & 0x8000u ? 0x7fffu : 0u) | (nan & 0x80000000u ? 0x7fff0000u : 0u);
+  };
+  a = pair(__byte_perm(w, 0, 0x1404));
+  b = pair(__byte_perm(w, 0, 0x3424));
+}
 
-// whether the condition holds in any of the 128 threads of a softmax group
+// whether the condition holds in any of the 128 threads of softmax group 0 or 1, or
+// (2) of the converters
 __device__ __forceinline__ bool group_any(int g, bool c) {
   uint32_t any;
   asm volatile(
@@ -223,11 +190,13 @@ __device__ __forceinline__ void reduce_columns(float (&v)[kCount], int lane, Op 
   }
 }
 
-// How far (log2) a score may pass its row's reference: bf16 weights have fp32's
-// exponents, so 2^24 costs nothing (a row's reference is set once, as good as
-// always); fp16 weights stay below 2^15.
+// Weights are fp16 (mostly, with a bf16 cache too): log2 of the weight that a maximum
+// gets when the reference is set at it, and of the largest one may reach before it is
+// set again; small weights count down to 2^-24 minus the first.  bf16 results have
+// three bits less, so three more rises are saved.
 template <typename T>
-constexpr float kQ8Rise = std::is_same<T, __half>::value ? kAtRise : 24.f;
+constexpr float kQ8Top = std::is_same<T, __half>::value ? 7.f : 4.f;
+constexpr float kQ8Most = 15.f;
 
 template <typename T, int D>
 struct Q8Softmax {
@@ -239,6 +208,7 @@ struct Q8Softmax {
   bool ok;
   uint32_t steps;  // tiles this group has had
   uint32_t meets;  // parts in which the groups met
+  int q_exp;       // log2 of the unit of the part's queries
 
   __device__ __forceinline__ uint32_t lanes() const { return static_cast<uint32_t>(quad * 32) << 16; }
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
@@ -271,10 +241,16 @@ struct Q8Softmax {
     return bits;
   }
 
+  // A group's place for its warps' maxima and sums of the columns: where its weights
+  // are, between the products that read them.
+  __device__ __forceinline__ float* cross(int group, int i) const {
+    return reinterpret_cast<float*>(pbuf + group * (kQ8PBytes / 2)) + i * (kAtTile / 2);
+  }
+
   // The columns that reduce_columns left in this lane to the group's place.
   template <int C>
   __device__ __forceinline__ void to_cross(int c0, const float (&v)[C]) const {
-    float* const at = sh.cross[g][quad] + c0;
+    float* const at = cross(g, quad) + c0;
     if (C == 32)
       at[lane] = v[0];
     else if ((lane & 1) == 0)
@@ -305,11 +281,15 @@ struct Q8Softmax {
   // their chains of scores, weights and products overlap.  `base`: tiles before it.
   template <int C, bool kWide>
   __device__ __forceinline__ void part(const AtPart& a, uint32_t base) {
-    constexpr float kTop = kAtTop<T>, kOver = kAtTop<T> + kQ8Rise<T>;
+    constexpr float kTop = kQ8Top<T>;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr int kStep = kWide ? 1 : 2;
-    constexpr int kChunk = C < 32 ? C : 32;  // columns in registers at a time (their scores are read twice)
+    constexpr int kChunk = C < 32 ? C : 32;  // columns read from TMEM at a time
     float* const neg_ref = sh.neg_ref[g];
-    float(&cross)[4][kAtTile / 2] = sh.cross[g];
+    float* const c0s = cross(g, 0);
+    float* const c1s = cross(g, 1);
+    float* const c2s = cross(g, 2);
+    float* const c3s = cross(g, 3);
     uint8_t* const pt = pbuf + g * (kQ8PBytes / 2) + key * 128;
     const uint32_t tm_o = tmem + 256 + 64 * g + lanes();
     const int col0 = kWide ? g * C : 0;
@@ -322,6 +302,8 @@ struct Q8Softmax {
 #pragma unroll
     for (int c = 0; c < C / 2; ++c) l2[c] = 0;
     group_any(g, false);
+    int unit = 0;  // log2 of the unit of O
+    const float q_scale = p.scale_log2 * two_to(q_exp);
     const int i0 = kWide ? 0 : static_cast<int>((base & 1) ^ g);  // tile j is in S buffer j & 1
 #pragma unroll 1
     for (int i = i0; i < tiles; i += kStep) {
@@ -330,6 +312,9 @@ struct Q8Softmax {
       const int t = a.t0 + i;
       ok = wait(&sh.s_full[j & 1], (j >> 1) & 1) && ok;
       tc_fence_after();
+      // this key's scale (its converter's write came before its product)
+      const float scale = q_scale * two_to(sh.key_exp[j & 3][key >> 3]);
+      const uint64_t scale2 = f32x2(scale, scale);
       const bool ragged = open - t * kAtTile < kAtTile;
       uint64_t bits = ~0ull;
       if (ragged) bits = seen(a, t, col0, C);
@@ -341,30 +326,38 @@ struct Q8Softmax {
           for (int c = 0; c < kChunk; ++c) s[c] = see >> c & 1 ? s[c] : 0xff800000u;
         }
       };
-      // two scores minus their references
-      auto minus_ref = [&](const uint32_t* s, uint64_t n, float& x, float& y) {
-        f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[0]), __uint_as_float(s[1])), f32x2(p.scale_log2, p.scale_log2), n), x, y);
-      };
-      // whether one passes its reference by far
-      float over = -INFINITY;
+      float e[C];  // weights
+      bool waited = steps == 0, wide = false;
+      // Weights by the references as they are.  If one is too large (or the unit of
+      // the values changed) the references are set anew, and once more.
 #pragma unroll 1
-      for (int c0 = 0; c0 < C; c0 += kChunk) {
-        uint32_t s[kChunk];
-        scores(c0, s);
-        float top[2] = {-INFINITY, -INFINITY};
+      for (int turn = 0;; ++turn) {
+        float over[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < kChunk; c += 4) {
-          const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(neg_ref + c0 + c);
-          float x, y;
-          minus_ref(s + c, n.x, x, y);
-          top[0] = max3(top[0], x, y);
-          minus_ref(s + c + 2, n.y, x, y);
-          top[1] = max3(top[1], x, y);
+        for (int c0 = 0; c0 < C; c0 += kChunk) {
+          uint32_t s[kChunk];
+          scores(c0, s);
+#pragma unroll
+          for (int c = 0; c < kChunk; c += 4) {
+            const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(neg_ref + c0 + c);
+            float x[4];
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, n.x), x[0], x[1]);
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), scale2, n.y), x[2], x[3]);
+            over[0] = max3(over[0], x[0], x[1]);
+            over[1] = max3(over[1], x[2], x[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e[c0 + c + k] = ex2(x[k]);
+          }
         }
-        over = max3(over, top[0], top[1]);
-      }
-      bool waited = steps == 0;
-      if (group_any(g, over > kOver || !ok)) {
+        int now = unit;
+        if (kBf16 && turn == 0) {  // the tile's values: their unit and type
+          ok = wait(&sh.vc_full[j & 1], (j >> 1) & 1) && ok;
+          now = sh.v_unit[j & 1];
+          wide = sh.v_wide[j & 1] != 0;
+          if (i == i0) unit = now;
+        }
+        if (!group_any(g, fmaxf(over[0], over[1]) > kQ8Most || now != unit || !ok)) break;
+        if (turn > 1) break;  // (never: the references are right after one turn)
         // (O may be multiplied: the last product into it is complete)
         if (ok && !waited) ok = wait(&sh.pv_done[g], (steps - 1) & 1);
         waited = true;
@@ -379,16 +372,16 @@ struct Q8Softmax {
           float top[kChunk];
           scores(c0, s);
 #pragma unroll
-          for (int c = 0; c < kChunk; ++c) top[c] = __uint_as_float(s[c]);
+          for (int c = 0; c < kChunk; ++c) top[c] = __uint_as_float(s[c]) * scale;
           reduce_columns<kChunk>(top, lane, [](float x, float y) { return fmaxf(x, y); });
           to_cross<kChunk>(c0, top);
         }
         group_any(g, false);
         if (mine < C) {
-          const float m = fmaxf(max3(cross[0][mine], cross[1][mine], cross[2][mine]), cross[3][mine]) * p.scale_log2;
+          const float m = fmaxf(max3(c0s[mine], c1s[mine], c2s[mine]), c3s[mine]);
           const float n = neg_ref[mine];
-          const bool up = m + n > kOver;
-          cross[0][mine] = up ? ex2(kTop - (m + n)) : 1.f;  // (0 at a row's first keys)
+          const bool up = m + n > kQ8Most;
+          c0s[mine] = up ? ex2(kTop - (m + n)) : 1.f;  // (0 at a row's first keys)
           if (up) neg_ref[mine] = kTop - m;
         }
         group_any(g, false);
@@ -397,49 +390,41 @@ struct Q8Softmax {
           for (int c = 0; c < C / 2; ++c) {
             float x, y;
             f32x2_split(l2[c], x, y);
-            l2[c] = f32x2(x * cross[0][2 * c], y * cross[0][2 * c + 1]);
+            l2[c] = f32x2(x * c0s[2 * c], y * c0s[2 * c + 1]);
           }
           if (D == 128 || quad < 2) {
+            const float units = two_to(max(unit - now, -126));
 #pragma unroll 1
             for (int c = 0; c < C; c += 16) {
               uint32_t o[16];
               tmem_load<16>(tm_o + c, o);
 #pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * cross[0][c + x]);
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * (c0s[c + x] * units));
               tmem_st16(tm_o + c, o);
             }
             tmem_st_wait();
           }
         }
+        unit = now;
+        group_any(g, false);  // the maxima's place may be written again
       }
-      // weights: the sums keep them in 32 bits, P in 16 (half a step off at most)
+      if (!waited) ok = wait(&sh.pv_done[g], (steps - 1) & 1) && ok;
+      // the sums keep the weights in 32 bits, P ([key][64 rows], 128-byte swizzle)
+      // in 16 (half a step off at most)
 #pragma unroll
-      for (int c0 = 0; c0 < C; c0 += kChunk) {
-        uint32_t s[kChunk], w[kChunk / 2];
-        scores(c0, s);
+      for (int c = 0; c < C / 2; ++c) l2[c] = add_f32x2(l2[c], f32x2(e[2 * c], e[2 * c + 1]));
+      auto put = [&](auto type) {
+        using W = decltype(type);
 #pragma unroll
-        for (int c = 0; c < kChunk; c += 4) {
-          const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(neg_ref + c0 + c);
-          float x[4];
-          minus_ref(s + c, n.x, x[0], x[1]);
-          minus_ref(s + c + 2, n.y, x[2], x[3]);
-#pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            const float e0 = ex2(x[k]), e1 = ex2(x[k + 1]);
-            l2[(c0 + c + k) / 2] = add_f32x2(l2[(c0 + c + k) / 2], f32x2(e0, e1));
-            w[(c + k) / 2] = Pack16<T>::pack(e0, e1);
-          }
-        }
-        if (!waited) {
-          ok = wait(&sh.pv_done[g], (steps - 1) & 1) && ok;
-          waited = true;
-        }
-        // P: [key][64 rows], 128-byte swizzle
-#pragma unroll
-        for (int c = 0; c < kChunk; c += 8)
-          *reinterpret_cast<uint4*>(pt + (((c0 + c) / 8 ^ (key & 7)) << 4)) =
-              make_uint4(w[c / 2], w[c / 2 + 1], w[c / 2 + 2], w[c / 2 + 3]);
-      }
+        for (int c = 0; c < C; c += 8)
+          *reinterpret_cast<uint4*>(pt + ((c / 8 ^ (key & 7)) << 4)) =
+              make_uint4(Pack16<W>::pack(e[c], e[c + 1]), Pack16<W>::pack(e[c + 2], e[c + 3]),
+                         Pack16<W>::pack(e[c + 4], e[c + 5]), Pack16<W>::pack(e[c + 6], e[c + 7]));
+      };
+      if (kBf16 && wide)
+        put(__nv_bfloat16());
+      else
+        put(__half());
       fence_async_shared();
       tc_fence_before();
       __syncwarp();
@@ -463,12 +448,10 @@ struct Q8Softmax {
     }
     group_any(g, false);
     float l = 0.f;
-    if (mine < C) l = (cross[0][mine] + cross[1][mine]) + (cross[2][mine] + cross[3][mine]);
-    // the lane's dim, in the converted values' order
-    const int at = quad * 32 + lane, dim = Codes<T>::kEvenOdd ? (at & ~3) | (at & 1) << 1 | (at >> 1 & 1) : at;
-    float* const out = (a.t0 == 0 ? p.part_o : p.slab_o) + dim;
+    if (mine < C) l = (c0s[mine] + c1s[mine]) + (c2s[mine] + c3s[mine]);
+    float* const out = (a.t0 == 0 ? p.part_o : p.slab_o) + quad * 32 + lane;
     const bool has_dims = D == 128 || quad < 2;
-    int64_t* const places = reinterpret_cast<int64_t*>(cross[1]);  // of the columns that this group writes
+    int64_t* const places = reinterpret_cast<int64_t*>(c1s);  // of the columns that this group writes
     if (kWide) {
       group_any(g, false);  // all sums have been read
       if (mine < C) {
@@ -484,13 +467,14 @@ struct Q8Softmax {
           tmem_load<8>(tm_o + c, o);
 #pragma unroll
           for (int x = 0; x < 8; ++x)
-            if (places[c + x] >= 0) out[places[c + x] * D] = __uint_as_float(o[x]);
+            if (places[c + x] >= 0) out[places[c + x] * D] = __uint_as_float(o[x]) * two_to(unit);
         }
       }
       tc_fence_before();
       group_any(g, false);  // the places and the references may be written again
     } else {
-      if (mine < C) cross[0][mine] = l;
+      if (mine < C) c0s[mine] = l;
+      if (mine == 0) sh.unit[g] = two_to(unit);
       // both groups' references, sums and products are there
       auto meet = [&](int i) {
         __syncwarp();
@@ -505,16 +489,16 @@ struct Q8Softmax {
       tc_fence_after();
       // group g joins its half of the columns; a group without a tile has sums of 0
       constexpr int kHalf = C / 2;
-      float* const factor = cross[3];  // [2][kHalf]
+      float* const factor = c3s;  // [2][kHalf]
       if (mine < kHalf) {
         const int c = g * kHalf + mine;
         const float n0 = sh.neg_ref[0][c], n1 = sh.neg_ref[1][c], m = fmaxf(-n0, -n1);
         const float f0 = n0 == kQ8Unset ? 0.f : ex2(-n0 - m), f1 = n1 == kQ8Unset ? 0.f : ex2(-n1 - m);
         // (a part of one tile has one O, in the group of its buffer: the other is not looked at)
-        factor[mine] = tiles > 1 || (base & 1) == 0 ? f0 : -1.f;
-        factor[kHalf + mine] = tiles > 1 || (base & 1) != 0 ? f1 : -1.f;
+        factor[mine] = tiles > 1 || (base & 1) == 0 ? f0 * sh.unit[0] : -1.f;
+        factor[kHalf + mine] = tiles > 1 || (base & 1) != 0 ? f1 * sh.unit[1] : -1.f;
         places[mine] = place(a, rows, c);
-        store_ml(a, places[mine], c, m == -kQ8Unset ? -INFINITY : m, sh.cross[0][0][c] * f0 + sh.cross[1][0][c] * f1);
+        store_ml(a, places[mine], c, m == -kQ8Unset ? -INFINITY : m, cross(0, 0)[c] * f0 + cross(1, 0)[c] * f1);
       }
       group_any(g, false);
       if (has_dims) {
@@ -762,9 +746,12 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
         const bool wide = columns == 128;
         if (lane == 0) mbar_arrive(&sh.part_empty[q]);
         if (line < 0) break;
-        const uint32_t id_qk = idesc_f16_f32(kBf16, false, kAtTile, columns);
-        const uint32_t id_pv = idesc_f16_f32(kBf16, true, kAtTile, columns) | 1u << 15;  // A too has K over its rows
-        if (!wait(Codes<T>::kEvenOdd ? &sh.q_ready[n & 1] : &sh.q_full[n & 1], (n >> 1) & 1)) break;
+        if (!wait(kBf16 ? &sh.q_ready[n & 1] : &sh.q_full[n & 1], (n >> 1) & 1)) break;
+        const uint32_t id_qk = idesc_f16_f32(kBf16 && __shfl_sync(0xffffffffu, static_cast<int>(sh.q_bf16[n & 1]), 0) != 0, false,
+                                             kAtTile, columns);
+        // A (the values) too has K over its rows
+        const uint32_t id_pv = idesc_f16_f32(false, true, kAtTile, columns) | 1u << 15,
+                       id_pv_bf16 = idesc_f16_f32(true, true, kAtTile, columns) | 1u << 15;
         // scores of the part's tile i
         auto qk = [&](int i) {
           const uint32_t j = base + i, b = j & 1;
@@ -792,13 +779,14 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
           if ((wide || b == 0) && !wait(&sh.p_full[0], ph_p[0]++ & 1)) break;
           if ((wide || b == 1) && !wait(&sh.p_full[1], ph_p[1]++ & 1)) break;
           tc_fence_after();
+          const uint32_t id = kBf16 && __shfl_sync(0xffffffffu, static_cast<int>(sh.v_wide[b]), 0) != 0 ? id_pv_bf16 : id_pv;
           if (elect_one()) {
             const uint32_t g = wide ? 0 : b;
             const uint64_t ad = v_desc + b * (kTileBytes >> 4), bd = p_desc + g * (kQ8PBytes / 2 >> 4);
             const bool more = i >= (wide ? 1 : 2);
 #pragma unroll
             for (int k = 0; k < kAtTile / 16; ++k)
-              tc_mma(utm + 256 + 64 * g, ad + k * (2048 >> 4), bd + k * (2048 >> 4), id_pv, more || k > 0);
+              tc_mma(utm + 256 + 64 * g, ad + k * (2048 >> 4), bd + k * (2048 >> 4), id, more || k > 0);
             if (wide || b == 0) tc_commit(&sh.pv_done[0]);
             if (wide || b == 1) tc_commit(&sh.pv_done[1]);
             tc_commit(&sh.vc_empty[b]);
@@ -816,6 +804,10 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
       // ---------------- key loads (warp 14) and value loads (warp 15) ----------------
       // A lane (of 16) has 8 keys: their page, ahead of time, and their block's
       // scale; one box a lane where a box (a run of a page's slots) begins.
+      // The values' unit (bf16 caches): they are converted to fp16 as multiples of
+      // 2^unit, exact for blocks whose exponents are within unit - 15 .. unit + 7.
+      // It is the first tile's largest exponent and rises where one passes that range;
+      // a tile with a block below it is converted to bf16 instead.
       const int values = warp == 15 ? 1 : 0;
       const CUtensorMap* const map = values ? &p.tmV : &p.tmK;
       const uint8_t* const scales = values ? p.c8.v_scales : p.c8.k_scales;
@@ -852,10 +844,13 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
           }
           return page;
         };
+        // (256: no scale, its keys are none)
         auto scale_of = [&](int i, int page) -> uint32_t {
           const uint32_t key = static_cast<uint32_t>(t0 + i) * kAtTile + my_key;
-          return page < p.n_pages ? scales[p.c8.scale_at(page, static_cast<int>(key % page_size), head)] : 127;
+          return page < p.n_pages ? scales[p.c8.scale_at(page, static_cast<int>(key % page_size), head)] : 256;
         };
+        int unit = 0;
+        bool any = false;  // unit is set
         // pages three tiles ahead, scales two
         int page0 = page_at(0), page1 = page_at(1), page2 = page_at(2);
         uint32_t scale0 = scale_of(0, page0), scale1 = scale_of(1, page1);
@@ -878,7 +873,22 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
             in_bounds(slot < kSlots && at_slot + p.box_rows <= static_cast<int>(page_size) && head >= 0 && head < p.n_heads, status);
             tma_load_4d(my_dst + slot * kRawBytes, map, 0, at_slot, head, page, &sh.raw_full[values][slot]);
           }
-          if (lane < 16) sh.scales[values][slot][lane] = static_cast<uint8_t>(scale);
+          const bool none = scale == 256 || lane >= 16;
+          const int e = none ? 0 : stored_exponent<T>(scale);
+          int wide = 0;
+          if (kBf16 && values) {
+            const int most = __reduce_max_sync(0xffffffffu, none ? -1000 : e), least = __reduce_min_sync(0xffffffffu, none ? 1000 : e);
+            if (most > -1000 && (!any || most > unit + 7)) {
+              unit = most;
+              any = true;
+            }
+            wide = least < unit - 15;
+          }
+          if (lane < 16) sh.scales[values][slot][lane] = static_cast<int8_t>(none && values ? unit : e);
+          if (values && lane == 0) {
+            sh.raw_unit[slot] = static_cast<int16_t>(unit);
+            sh.raw_wide[slot] = static_cast<int8_t>(wide);
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.raw_full[values][slot]);
         }
@@ -909,31 +919,60 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
       const int at = D == 128 ? c ^ (key & 7) : c ^ (key >> 1 & 3);
       return *reinterpret_cast<const uint4*>(tile + key * D + at * 16);
     };
-    auto any_rare = [&](const Codes<T>& conv, const uint4 (&w)[D / 16]) {
-      uint32_t bits = 0;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        bits |= Codes<T>::rare_bits(w[c].x) | Codes<T>::rare_bits(w[c].y) | Codes<T>::rare_bits(w[c].z) | Codes<T>::rare_bits(w[c].w);
-      return __any_sync(0xffffffffu, conv.is_rare(bits)) != 0;
-    };
 #pragma unroll 1
-    for (uint32_t n = 0; ok; ++n) {
+    for (uint32_t n = 0;; ++n) {
       const int q = n % kQ8Queue;
-      if (!wait(&sh.part_full[q], (n / kQ8Queue) & 1)) break;
+      wait(&sh.part_full[q], (n / kQ8Queue) & 1);
+      if (group_any(2, !ok)) break;
       const int line = sh.parts[q].line, t0 = sh.parts[q].t0, tiles = sh.parts[q].t1 - t0, len = sh.parts[q].len,
-                columns = q8_columns(sh.parts[q].n0 * p.group);
+                rows = sh.parts[q].n0 * p.group, columns = q8_columns(rows);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.part_empty[q]);
       if (line < 0) break;
-      if (Codes<T>::kEvenOdd) {
-        // the queries' dims in the order of the converted keys'
-        if (!wait(&sh.q_full[n & 1], (n >> 1) & 1)) break;
+      bool k_bf16 = false;
+      if (kBf16) {
+        // The queries as fp16 times 2^unit: the largest gets 2^14 or more, and what
+        // is not below 2^-20 of it keeps bf16's 8 bits 2^10 times over.  Rows
+        // smaller than that, or not finite: they stay bf16, and so do the keys.
+        wait(&sh.q_full[n & 1], (n >> 1) & 1);
         uint8_t* const qt = qbuf + (n & 1) * kTileBytes;
-        for (int x = key; x < columns * 8 * kHalves; x += 128) {
-          uint4* const at = reinterpret_cast<uint4*>(qt + (x / (columns * 8)) * kHalfBytes + (x % (columns * 8)) * 16);
-          const uint4 w = *at;
-          *at = make_uint4(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632), __byte_perm(w.z, w.w, 0x5410),
-                           __byte_perm(w.z, w.w, 0x7632));
+        uint32_t top = 0;  // of this thread's row
+        if (ok && key < rows) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 w = *reinterpret_cast<const uint4*>(qt + (c / 8) * kHalfBytes + key * 128 + (((c % 8) ^ (key & 7)) << 4));
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0x7fffu, x[i] >> 16 & 0x7fffu));
+          }
+        }
+        sh.row_max[key] = top;
+        if (group_any(2, !ok)) break;
+        uint32_t most = 0, least = 0xffff;
+#pragma unroll
+        for (int r = 0; r < kAtTile; r += 32) {
+          const uint32_t x = sh.row_max[r + lane];
+          most = max(most, x);
+          least = min(least, x == 0 ? 0xffffu : x);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        least = __reduce_min_sync(0xffffffffu, least);
+        k_bf16 = most >= 0x7f80u || (least >> 7) + 20 < (most >> 7);
+        const int e = most == 0 || k_bf16 ? 0 : max(static_cast<int>(most >> 7) - 127 - 14, -120);
+        if (!k_bf16) {
+          const float f = two_to(-e);
+          for (int x = key; x < columns * 8 * kHalves; x += 128) {
+            uint4* const at = reinterpret_cast<uint4*>(qt + (x / (columns * 8)) * kHalfBytes + (x % (columns * 8)) * 16);
+            float v[8];
+            unpack8<__nv_bfloat16>(*at, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= f;
+            *at = pack8<__half>(v);
+          }
+        }
+        if (key == 0) {
+          sh.q_exp[n & 1] = static_cast<int16_t>(e);
+          sh.q_bf16[n & 1] = k_bf16;
         }
         fence_async_shared();
         __syncwarp();
@@ -942,27 +981,27 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
 #pragma unroll 1
       for (int i = 0; i < tiles && ok; ++i) {
         const uint32_t j = base + i, b = j & 1, slot = j % kSlots, use = j / kSlots;
-        // keys, to TMEM
+        // keys, to TMEM: the codes' values, their scales count in the scores
         if (!wait(&sh.raw_full[0][slot], use & 1)) break;
         if (j >= 2 && !wait(&sh.kc_empty[b], ((j >> 1) & 1) ^ 1)) break;
         tc_fence_after();
         {
           const uint8_t* const tile = ring + slot * kRawBytes;
           const uint32_t dst = tmem + lanes + 384 + (D / 2) * b;
-          const Codes<T> conv(stored_exponent<T>(sh.scales[0][slot][key >> 3]));
-          uint4 w[D / 16];
+          if ((lane & 7) == 0) sh.key_exp[j & 3][key >> 3] = sh.scales[0][slot][key >> 3];
+          if (!kBf16 || !k_bf16) {
+            uint4 w[D / 16];
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) w[c] = codes(tile, c);
-          if (!any_rare(conv, w)) {
+            for (int c = 0; c < D / 16; ++c) w[c] = codes(tile, c);
 #pragma unroll
             for (int c = 0; c < D / 16; c += 4) {
               uint32_t d[32];
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                conv.four(w[c + x].x, d[8 * x], d[8 * x + 1]);
-                conv.four(w[c + x].y, d[8 * x + 2], d[8 * x + 3]);
-                conv.four(w[c + x].z, d[8 * x + 4], d[8 * x + 5]);
-                conv.four(w[c + x].w, d[8 * x + 6], d[8 * x + 7]);
+                codes_f16(w[c + x].x, d[8 * x], d[8 * x + 1]);
+                codes_f16(w[c + x].y, d[8 * x + 2], d[8 * x + 3]);
+                codes_f16(w[c + x].z, d[8 * x + 4], d[8 * x + 5]);
+                codes_f16(w[c + x].w, d[8 * x + 6], d[8 * x + 7]);
               }
               tmem_st32(dst + 8 * c, d);
             }
@@ -971,10 +1010,10 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
             for (int c = 0; c < D / 16; ++c) {
               const uint4 x = codes(tile, c);
               uint32_t d[8];
-              conv.rare(x.x, d[0], d[1]);
-              conv.rare(x.y, d[2], d[3]);
-              conv.rare(x.z, d[4], d[5]);
-              conv.rare(x.w, d[6], d[7]);
+              codes_bf16(x.x, 0, d[0], d[1]);
+              codes_bf16(x.y, 0, d[2], d[3]);
+              codes_bf16(x.z, 0, d[4], d[5]);
+              codes_bf16(x.w, 0, d[6], d[7]);
               tmem_st8(dst + 8 * c, d);
             }
           }
@@ -986,30 +1025,34 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
           mbar_arrive(&sh.kc_full[b]);
           mbar_arrive(&sh.raw_empty[0][slot]);
         }
-        // values, to a swizzled tile; past the last entry zeros (zero times what
-        // stands there must be zero)
+        // values, to a swizzled tile, as multiples of their unit; past the last entry
+        // zeros (zero times what stands there must be zero)
         if (!wait(&sh.raw_full[1][slot], use & 1)) break;
         if (j >= 2 && !wait(&sh.vc_empty[b], ((j >> 1) & 1) ^ 1)) break;
         {
           const uint8_t* const tile = ring + (kSlots + slot) * kRawBytes;
-          const Codes<T> conv(stored_exponent<T>(sh.scales[1][slot][key >> 3]));
-          const bool live = (t0 + i) * kAtTile + key < len;
+          const int e = sh.scales[1][slot][key >> 3] - sh.raw_unit[slot];
+          const bool live = (t0 + i) * kAtTile + key < len, wide = sh.raw_wide[slot] != 0;
           uint8_t* const dst = vbuf + b * kTileBytes + key * 128;
-          uint4 w[D / 16];
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) w[c] = live ? codes(tile, c) : make_uint4(0, 0, 0, 0);
           // 8 dims: one 16-byte vector
           auto put = [&](int at, const uint32_t* d) {
             *reinterpret_cast<uint4*>(dst + (at / 8) * kHalfBytes + (((at % 8) ^ (key & 7)) << 4)) = make_uint4(d[0], d[1], d[2], d[3]);
           };
-          if (!any_rare(conv, w)) {
+          if (!kBf16 || !wide) {
+            const __half2 h = __float2half2_rn(two_to(e));  // e: -15 .. 8
+            const uint32_t scale = *reinterpret_cast<const uint32_t*>(&h);
+            uint4 w[D / 16];
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) w[c] = live ? codes(tile, c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               uint32_t d[8];
-              conv.four(w[c].x, d[0], d[1]);
-              conv.four(w[c].y, d[2], d[3]);
-              conv.four(w[c].z, d[4], d[5]);
-              conv.four(w[c].w, d[6], d[7]);
+              codes_f16(w[c].x, d[0], d[1]);
+              codes_f16(w[c].y, d[2], d[3]);
+              codes_f16(w[c].z, d[4], d[5]);
+              codes_f16(w[c].w, d[6], d[7]);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) d[x] = mul_f16x2(d[x], scale);
               put(2 * c, d);
               put(2 * c + 1, d + 4);
             }
@@ -1018,13 +1061,17 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
             for (int c = 0; c < D / 16; ++c) {
               const uint4 x = live ? codes(tile, c) : make_uint4(0, 0, 0, 0);
               uint32_t d[8];
-              conv.rare(x.x, d[0], d[1]);
-              conv.rare(x.y, d[2], d[3]);
-              conv.rare(x.z, d[4], d[5]);
-              conv.rare(x.w, d[6], d[7]);
+              codes_bf16(x.x, e, d[0], d[1]);
+              codes_bf16(x.y, e, d[2], d[3]);
+              codes_bf16(x.z, e, d[4], d[5]);
+              codes_bf16(x.w, e, d[6], d[7]);
               put(2 * c, d);
               put(2 * c + 1, d + 4);
             }
+          }
+          if (key == 0) {
+            sh.v_unit[b] = sh.raw_unit[slot];
+            sh.v_wide[b] = sh.raw_wide[slot];
           }
         }
         fence_async_shared();
@@ -1038,7 +1085,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
     }
   } else {
     regs_up<kQ8SoftmaxRegs>();
-    Q8Softmax<T, D> sm = {p, sh, pbuf, tmem, warp >> 2, warp & 3, lane, (warp & 3) * 32 + lane, true, 0, 0};
+    Q8Softmax<T, D> sm = {p, sh, pbuf, tmem, warp >> 2, warp & 3, lane, (warp & 3) * 32 + lane, true, 0, 0, 0};
     uint32_t base = 0;
 #pragma unroll 1
     for (uint32_t n = 0;; ++n) {
@@ -1046,9 +1093,15 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
       sm.ok = sm.wait(&sh.part_full[q], (n / kQ8Queue) & 1) && sm.ok;
       if (group_any(sm.g, !sm.ok)) break;
       const AtPart a = sh.parts[q];
+      if (a.line < 0) break;
+      if (kBf16) {
+        // (before the part's place is free: the queries of the part after the next
+        // complete the next phase of this barrier)
+        sm.ok = sm.wait(&sh.q_ready[n & 1], (n >> 1) & 1) && sm.ok;
+        sm.q_exp = sh.q_exp[n & 1];
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.part_empty[q]);
-      if (a.line < 0) break;
       const int columns = q8_columns(a.n0 * p.group);
       if (columns == 16)
         sm.template part<16, false>(a, base);
