@@ -73,7 +73,6 @@ constexpr int kAtSoftmaxRegs = 216, kAtOtherRegs = 72;
 constexpr int kAtRingBytes = 160 * 1024;
 constexpr int kAtMaxCtas = 160;     // slabs in the workspace
 constexpr int kAtQueue = 4;         // parts queued ahead
-constexpr int kAtFixed = 15;        // weight of a part's fixed cost
 constexpr float kAtRise = 8.f;      // log2 of how far a row's maximum may pass the one its reference was set at
 // log2 of the weight that a maximum gets when the reference is set at it.  fp16
 // weights reach 2^15 of the 65,504 that the type holds: below 2^-14 they lose
@@ -119,6 +118,9 @@ struct AttendParams {
   __device__ __forceinline__ int64_t place(int line, int64_t row) const {
     return line == 1 && prefix_len > 0 ? static_cast<int64_t>(batch.N) * n_q_heads + row : row;
   }
+  // Weights in the line, in units of some 400 clocks: a key tile took 3,250 with two
+  // row tiles and 2,000 with one; a part's queries, first scores and results 6,000.
+  static constexpr int kWide = 8, kNarrow = 5, kFixed = 15;
   // the cache's entries one by one: 16-bit values as they are
   static constexpr bool kCodes = false;
   __device__ __forceinline__ int64_t head_stride() const { return cache.head_stride; }
@@ -158,17 +160,18 @@ __device__ __forceinline__ int block_rows(const AttendParams& p, int positions, 
   return positions - rb * p.block > p.narrow ? 2 : 1;
 }
 
-// Weights are in units of some 400 clocks: a key tile took 3,250 with two row
-// tiles and 2,000 with one.  A part's queries, first scores and results took
-// some 6,000: an item weighs that much more, all on its first tile, where the
-// CTAs have several tiles each; where they have few the tiles alone are dealt
-// out, which uses more CTAs (candidates_d64: 28 us against 31.5).
-__device__ __forceinline__ int tile_weight(int row_tiles) { return row_tiles == 2 ? 8 : 5; }
+// A part's fixed cost (P::kFixed): an item weighs that much more, all on its first
+// tile, where the CTAs have several tiles each; where they have few the tiles
+// alone are dealt out, which uses more CTAs (candidates_d64: 28 us against 31.5).
+template <typename P>
+__device__ __forceinline__ int tile_weight(int row_tiles) { return row_tiles == 2 ? P::kWide : P::kNarrow; }
+template <typename P>
 __device__ __forceinline__ int fixed_weight(int64_t tiles_alone, int n_ctas) {
-  return tiles_alone < 30LL * n_ctas ? 0 : kAtFixed;
+  return tiles_alone < 6LL * P::kNarrow * n_ctas ? 0 : P::kFixed;
 }
+template <typename P>
 __device__ __forceinline__ int64_t item_weight(int tiles, int row_tiles, int fixed) {
-  return tiles == 0 ? 0 : static_cast<int64_t>(tiles) * tile_weight(row_tiles) + fixed;
+  return tiles == 0 ? 0 : static_cast<int64_t>(tiles) * tile_weight<P>(row_tiles) + fixed;
 }
 
 // One key head's items of a sequence: the weight of their tiles alone, and how
@@ -178,11 +181,12 @@ struct SeqWeight {
   int items;
   __device__ __forceinline__ int64_t per_head(int fixed) const { return tiles_alone + static_cast<int64_t>(items) * fixed; }
 };
-__device__ __forceinline__ SeqWeight seq_weight(const AttendParams& p, const SeqSpan& s) {
+template <typename P>
+__device__ __forceinline__ SeqWeight seq_weight(const P& p, const SeqSpan& s) {
   SeqWeight w = {0, 0};
   for (int rb = 0; rb * p.block < s.n; ++rb) {
     const int tiles = block_tiles(p, s, rb);
-    w.tiles_alone += static_cast<int64_t>(tiles) * tile_weight(block_rows(p, s.n, rb));
+    w.tiles_alone += static_cast<int64_t>(tiles) * tile_weight<P>(block_rows(p, s.n, rb));
     w.items += tiles > 0;
   }
   return w;
@@ -207,15 +211,16 @@ struct PrefixItems {
     return tiles == 0 ? 0 : tiles_alone + static_cast<int64_t>(blocks) * fixed;
   }
 };
-__device__ __forceinline__ PrefixItems prefix_items(const AttendParams& p) {
+template <typename P>
+__device__ __forceinline__ PrefixItems prefix_items(const P& p) {
   PrefixItems L;
   L.positions = new_positions(p.batch);
   L.tiles = (p.prefix_len + kAtTile - 1) / kAtTile;
   L.blocks = (L.positions + p.block - 1) / p.block;
   L.tiles_alone = L.blocks == 0 ? 0
                                 : static_cast<int64_t>(L.tiles) *
-                                      ((L.blocks - 1) * tile_weight(2) +
-                                       tile_weight(block_rows(p, L.positions, L.blocks - 1)));
+                                      ((L.blocks - 1) * tile_weight<P>(2) +
+                                       tile_weight<P>(block_rows(p, L.positions, L.blocks - 1)));
   return L;
 }
 
@@ -228,13 +233,14 @@ __device__ __forceinline__ int64_t part_begin(int64_t W, int c, int n) {
 }
 // Tile t of an item begins at its `off` (t = 0) or at off + fixed + t * weight:
 // the tiles that begin before x.
+template <typename P>
 __device__ __forceinline__ int tiles_before(int64_t x, int64_t off, int row_tiles, int fixed, int tiles) {
   if (x <= off || tiles == 0) return 0;
   const int64_t y = x - off - fixed;
   if (y <= 0) return 1;
-  if (y >= static_cast<int64_t>(tiles) * 8) return tiles;
+  if (y >= static_cast<int64_t>(tiles) * P::kWide) return tiles;
   const uint32_t z = static_cast<uint32_t>(y);
-  const int t = static_cast<int>(row_tiles == 2 ? (z + 7) / 8 : (z + 4) / 5);
+  const int t = static_cast<int>(row_tiles == 2 ? (z + P::kWide - 1) / P::kWide : (z + P::kNarrow - 1) / P::kNarrow);
   return min(t, tiles);
 }
 
@@ -428,7 +434,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         own += __shfl_xor_sync(0xffffffffu, own, x);
         own_items += __shfl_xor_sync(0xffffffffu, own_items, x);
       }
-      a.fixed = fixed_weight(pl.tiles_alone * p.n_heads + own, p.n_ctas);
+      a.fixed = fixed_weight<AttendParams>(pl.tiles_alone * p.n_heads + own, p.n_ctas);
       const int64_t prefix = pl.per_head(a.fixed) * p.n_heads, total = prefix + own + own_items * a.fixed;
       const int64_t lo = part_begin(total, cta, p.n_ctas), hi = part_begin(total, cta + 1, p.n_ctas);
       // the sequence that this CTA's part of the own pages begins in
@@ -493,14 +499,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
               a.off = off;
               a.tiles = tiles;
               a.w = w;
-              a.t0 = tiles_before(lo, off, w, a.fixed, tiles);
-              a.t1 = tiles_before(hi, off, w, a.fixed, tiles);
-              off += item_weight(tiles, w, a.fixed);
+              a.t0 = tiles_before<AttendParams>(lo, off, w, a.fixed, tiles);
+              a.t1 = tiles_before<AttendParams>(hi, off, w, a.fixed, tiles);
+              off += item_weight<AttendParams>(tiles, w, a.fixed);
               if (a.t0 >= a.t1) continue;
               // the part that the item's last tile begins in
               a.last = cta;
               if (a.t0 == 0 && a.t1 < tiles)
-                a.last = static_cast<int>(((off - tile_weight(w) + 1) * p.n_ctas - 1) / total);
+                a.last = static_cast<int>(((off - tile_weight<AttendParams>(w) + 1) * p.n_ctas - 1) / total);
               a.first = s.first + at;
               a.n0 = min(p.tok_tile, s.n - at);
               a.n1 = min(p.tok_tile, s.n - at - a.n0);
@@ -1112,14 +1118,14 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     add(ml[line], x[line]);
     const int first = item[line].x & 255, last = min(item[line].x >> 8 & 255, p.n_ctas - 1);
     const int slab_row = min(item[line].x >> 16 & 255, p.slab_rows - 1), tiles = item[line].y >> 2, w = 1 + (item[line].y & 1),
-              fixed = item[line].y & 2 ? kAtFixed : 0;
+              fixed = item[line].y & 2 ? P::kFixed : 0;
     const int64_t off = static_cast<int64_t>(item[line].w) << 32 | static_cast<uint32_t>(item[line].z);
     const int64_t* const begin = p.begin;
     for (int c0 = first + 1; c0 <= last; c0 += 32) {
       // lane i: whether part c0 + i holds a tile's beginning
       const int c = c0 + lane;
-      const bool has = c <= last && tiles_before(begin[c], off, w, fixed, tiles) <
-                                        tiles_before(begin[c + 1], off, w, fixed, tiles);
+      const bool has = c <= last && tiles_before<P>(begin[c], off, w, fixed, tiles) <
+                                        tiles_before<P>(begin[c + 1], off, w, fixed, tiles);
       unsigned parts = __ballot_sync(0xffffffffu, has);
       while (parts != 0u) {
         // up to four parts' loads in flight, added in ascending order

@@ -38,12 +38,17 @@ namespace specv {
 
 constexpr int kQ8Threads = 512;
 // 184 + 184 + 80 + 64 = 4 x 128, the launch's
-constexpr int kQ8SoftmaxRegs = 184, kQ8ConvertRegs = 80, kQ8OtherRegs = 64;
+constexpr int kQ8LaunchRegs = 128, kQ8SoftmaxRegs = 184, kQ8ConvertRegs = 80, kQ8OtherRegs = 64;
+static_assert(2 * kQ8SoftmaxRegs + kQ8ConvertRegs + kQ8OtherRegs == kQ8Threads / 128 * kQ8LaunchRegs,
+              "a share above the launch's registers would be waited for for ever");
 constexpr int kQ8Queue = 2;          // parts queued ahead
 constexpr float kQ8Unset = 3.0e38f;  // minus the reference of a row that has seen nothing
 
 struct Attend8Params : AttendParams {
   Paged8View c8;
+  // As AttendParams has them: a key tile takes some 3,600 clocks with over 64 rows
+  // and 2,300 with fewer, a part's queries, first scores and results 12,000.
+  static constexpr int kWide = 9, kNarrow = 6, kFixed = 30;
   static constexpr bool kCodes = true;
   __device__ __forceinline__ int64_t head_stride() const { return c8.head_stride; }
   __device__ __forceinline__ int64_t entry_at(int64_t page, int slot) const {
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
         own += __shfl_xor_sync(0xffffffffu, own, x);
         own_items += __shfl_xor_sync(0xffffffffu, own_items, x);
       }
-      a.fixed = fixed_weight(pl.tiles_alone * p.n_heads + own, p.n_ctas);
+      a.fixed = fixed_weight<Attend8Params>(pl.tiles_alone * p.n_heads + own, p.n_ctas);
       const int64_t prefix = pl.per_head(a.fixed) * p.n_heads, total = prefix + own + own_items * a.fixed;
       const int64_t lo = part_begin(total, cta, p.n_ctas), hi = part_begin(total, cta + 1, p.n_ctas);
       // the sequence that this CTA's part of the own pages begins in
@@ -681,14 +686,14 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
               a.off = off;
               a.tiles = tiles;
               a.w = w;
-              a.t0 = tiles_before(lo, off, w, a.fixed, tiles);
-              a.t1 = tiles_before(hi, off, w, a.fixed, tiles);
-              off += item_weight(tiles, w, a.fixed);
+              a.t0 = tiles_before<Attend8Params>(lo, off, w, a.fixed, tiles);
+              a.t1 = tiles_before<Attend8Params>(hi, off, w, a.fixed, tiles);
+              off += item_weight<Attend8Params>(tiles, w, a.fixed);
               if (a.t0 >= a.t1) continue;
               // the part that the item's last tile begins in
               a.last = cta;
               if (a.t0 == 0 && a.t1 < tiles)
-                a.last = static_cast<int>(((off - tile_weight(w) + 1) * p.n_ctas - 1) / total);
+                a.last = static_cast<int>(((off - tile_weight<Attend8Params>(w) + 1) * p.n_ctas - 1) / total);
               a.first = s.first + at;
               a.n0 = min(p.block, s.n - at);
               a.n1 = 0;
@@ -759,7 +764,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
           tc_fence_after();
           if (elect_one()) {
             const uint64_t bd = q_desc + (n & 1) * (kTileBytes >> 4);
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D / 16; ++k)
               tc_mma_ts(utm + 128 * b, utm + 384 + (D / 2) * b + 8 * k, bd + (k / 4) * (kHalfBytes >> 4) + (k % 4) * 2, id_qk, k > 0);
             tc_commit(&sh.s_full[b]);
@@ -784,7 +789,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
             const uint32_t g = wide ? 0 : b;
             const uint64_t ad = v_desc + b * (kTileBytes >> 4), bd = p_desc + g * (kQ8PBytes / 2 >> 4);
             const bool more = i >= (wide ? 1 : 2);
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < kAtTile / 16; ++k)
               tc_mma(utm + 256 + 64 * g, ad + k * (2048 >> 4), bd + k * (2048 >> 4), id, more || k > 0);
             if (wide || b == 0) tc_commit(&sh.pv_done[0]);
@@ -990,18 +995,16 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
           const uint32_t dst = tmem + lanes + 384 + (D / 2) * b;
           if ((lane & 7) == 0) sh.key_exp[j & 3][key >> 3] = sh.scales[0][slot][key >> 3];
           if (!kBf16 || !k_bf16) {
-            uint4 w[D / 16];
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) w[c] = codes(tile, c);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 16; c += 4) {
               uint32_t d[32];
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                codes_f16(w[c + x].x, d[8 * x], d[8 * x + 1]);
-                codes_f16(w[c + x].y, d[8 * x + 2], d[8 * x + 3]);
-                codes_f16(w[c + x].z, d[8 * x + 4], d[8 * x + 5]);
-                codes_f16(w[c + x].w, d[8 * x + 6], d[8 * x + 7]);
+                const uint4 w = codes(tile, c + x);
+                codes_f16(w.x, d[8 * x], d[8 * x + 1]);
+                codes_f16(w.y, d[8 * x + 2], d[8 * x + 3]);
+                codes_f16(w.z, d[8 * x + 4], d[8 * x + 5]);
+                codes_f16(w.w, d[8 * x + 6], d[8 * x + 7]);
               }
               tmem_st32(dst + 8 * c, d);
             }
@@ -1041,16 +1044,14 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
           if (!kBf16 || !wide) {
             const __half2 h = __float2half2_rn(two_to(e));  // e: -15 .. 8
             const uint32_t scale = *reinterpret_cast<const uint32_t*>(&h);
-            uint4 w[D / 16];
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) w[c] = live ? codes(tile, c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
+              const uint4 w = live ? codes(tile, c) : make_uint4(0, 0, 0, 0);
               uint32_t d[8];
-              codes_f16(w[c].x, d[0], d[1]);
-              codes_f16(w[c].y, d[2], d[3]);
-              codes_f16(w[c].z, d[4], d[5]);
-              codes_f16(w[c].w, d[6], d[7]);
+              codes_f16(w.x, d[0], d[1]);
+              codes_f16(w.y, d[2], d[3]);
+              codes_f16(w.z, d[4], d[5]);
+              codes_f16(w.w, d[6], d[7]);
 #pragma unroll
               for (int x = 0; x < 8; ++x) d[x] = mul_f16x2(d[x], scale);
               put(2 * c, d);

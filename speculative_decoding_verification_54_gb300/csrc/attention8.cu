@@ -39,6 +39,14 @@ int device8_sms(int* sms) {
       return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) ==
              cudaSuccess;
     };
+    // the attention's warpgroups share out the registers it is launched with
+    auto regs_fit = [](auto kernel) {
+      cudaFuncAttributes a;
+      return cudaFuncGetAttributes(&a, kernel) == cudaSuccess && a.numRegs == kQ8LaunchRegs;
+    };
+    if (!regs_fit(attend8_kernel<__nv_bfloat16, 64>) || !regs_fit(attend8_kernel<__nv_bfloat16, 128>) ||
+        !regs_fit(attend8_kernel<__half, 64>) || !regs_fit(attend8_kernel<__half, 128>))
+      return SPEC_ERR_CUDA;
     if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         !raise(attend8_kernel<__nv_bfloat16, 64>, q8_smem_bytes<64>()) ||
         !raise(attend8_kernel<__nv_bfloat16, 128>, q8_smem_bytes<128>()) ||
