@@ -77,8 +77,9 @@ template <int D>
 struct Q8Shared {
   static constexpr int kSlots = 32 * 1024 / (kAtTile * D);  // of the key ring and of the value ring
   uint64_t raw_full[2][kSlots], raw_empty[2][kSlots];       // [keys, values]
-  uint64_t kc_full[2], kc_empty[2], vc_full[2], vc_empty[2];
-  uint64_t s_full[2], p_full[2], pv_done[2], meet[2], o_free, q_full[2], q_ready[2], q_empty[2], part_full[kQ8Queue], part_empty[kQ8Queue], done;
+  uint64_t kc_full[2], vc_full[2];
+  uint64_t s_full[2], pv_done[2];  // the products of tile j (places j % 2) are complete: their operands too are free
+  uint64_t p_full[2], meet[2], o_free, q_full[2], q_ready[2], q_empty[2], part_full[kQ8Queue], part_empty[kQ8Queue], done;
   __align__(16) float neg_ref[2][kAtTile / 2];  // per group: minus its columns' references (log2)
   float unit[2];                                // log2 of the unit of the groups' O
   int8_t scales[2][kSlots][16];                 // [keys, values] exponents of 8 keys each
@@ -211,7 +212,7 @@ struct Q8Softmax {
   uint32_t tmem;
   int g, quad, lane, key;
   bool ok;
-  uint32_t steps;  // tiles this group has had
+  uint32_t next;   // 1 + the last tile that this group had
   uint32_t meets;  // parts in which the groups met
   int q_exp;       // log2 of the unit of the part's queries
 
@@ -219,6 +220,11 @@ struct Q8Softmax {
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.batch.status, kWaitLimitCycles));
   }
+
+  // The last product of this group's weights is complete.  (Its barrier's next
+  // phase needs weights that this group has not written, or follows a part that
+  // it has not ended.)
+  __device__ __forceinline__ bool products_done() const { return wait(&sh.pv_done[(next - 1) & 1], ((next - 1) >> 1) & 1); }
 
   // Which of C columns from col0 on see this thread's key of tile t, bit by column.
   // (Loops that are not unrolled here and below: code that runs once a part or
@@ -332,7 +338,7 @@ struct Q8Softmax {
         }
       };
       float e[C];  // weights
-      bool waited = steps == 0, wide = false;
+      bool waited = next == 0, wide = false;
       // Weights by the references as they are.  If one is too large (or the unit of
       // the values changed) the references are set anew, and once more.
 #pragma unroll 1
@@ -364,7 +370,7 @@ struct Q8Softmax {
         if (!group_any(g, fmaxf(over[0], over[1]) > kQ8Most || now != unit || !ok)) break;
         if (turn > 1) break;  // (never: the references are right after one turn)
         // (O may be multiplied: the last product into it is complete)
-        if (ok && !waited) ok = wait(&sh.pv_done[g], (steps - 1) & 1);
+        if (ok && !waited) ok = products_done();
         waited = true;
         if (group_any(g, !ok)) {
           ok = false;
@@ -413,7 +419,7 @@ struct Q8Softmax {
         unit = now;
         group_any(g, false);  // the maxima's place may be written again
       }
-      if (!waited) ok = wait(&sh.pv_done[g], (steps - 1) & 1) && ok;
+      if (!waited) ok = products_done() && ok;
       // the sums keep the weights in 32 bits, P ([key][64 rows], 128-byte swizzle)
       // in 16 (half a step off at most)
 #pragma unroll
@@ -434,11 +440,11 @@ struct Q8Softmax {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_full[g]);
-      ++steps;
+      next = j + 1;
     }
 
     // ---- the part's results ----
-    if (steps > 0) ok = wait(&sh.pv_done[g], (steps - 1) & 1) && ok;
+    if (next > 0) ok = products_done() && ok;
     if (group_any(g, !ok)) {
       ok = false;
       return;
@@ -561,9 +567,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
         mbar_init(&sh.raw_empty[v][i], 4);  // converter warps
       }
       mbar_init(&sh.kc_full[v], 4);
-      mbar_init(&sh.kc_empty[v], 1);
       mbar_init(&sh.vc_full[v], 4);
-      mbar_init(&sh.vc_empty[v], 1);
       mbar_init(&sh.s_full[v], 1);
       mbar_init(&sh.q_full[v], 1);
       mbar_init(&sh.q_empty[v], 1);
@@ -768,7 +772,6 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
             for (int k = 0; k < D / 16; ++k)
               tc_mma_ts(utm + 128 * b, utm + 384 + (D / 2) * b + 8 * k, bd + (k / 4) * (kHalfBytes >> 4) + (k % 4) * 2, id_qk, k > 0);
             tc_commit(&sh.s_full[b]);
-            tc_commit(&sh.kc_empty[b]);
             if (i + 1 == tiles) tc_commit(&sh.q_empty[n & 1]);
           }
           __syncwarp();
@@ -792,9 +795,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
 #pragma unroll 1
             for (int k = 0; k < kAtTile / 16; ++k)
               tc_mma(utm + 256 + 64 * g, ad + k * (2048 >> 4), bd + k * (2048 >> 4), id, more || k > 0);
-            if (wide || b == 0) tc_commit(&sh.pv_done[0]);
-            if (wide || b == 1) tc_commit(&sh.pv_done[1]);
-            tc_commit(&sh.vc_empty[b]);
+            tc_commit(&sh.pv_done[b]);
           }
           __syncwarp();
           if (i + 2 < tiles) qk(i + 2);
@@ -988,7 +989,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
         const uint32_t j = base + i, b = j & 1, slot = j % kSlots, use = j / kSlots;
         // keys, to TMEM: the codes' values, their scales count in the scores
         if (!wait(&sh.raw_full[0][slot], use & 1)) break;
-        if (j >= 2 && !wait(&sh.kc_empty[b], ((j >> 1) & 1) ^ 1)) break;
+        if (j >= 2 && !wait(&sh.s_full[b], ((j >> 1) & 1) ^ 1)) break;
         tc_fence_after();
         {
           const uint8_t* const tile = ring + slot * kRawBytes;
@@ -1031,7 +1032,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
         // values, to a swizzled tile, as multiples of their unit; past the last entry
         // zeros (zero times what stands there must be zero)
         if (!wait(&sh.raw_full[1][slot], use & 1)) break;
-        if (j >= 2 && !wait(&sh.vc_empty[b], ((j >> 1) & 1) ^ 1)) break;
+        if (j >= 2 && !wait(&sh.pv_done[b], ((j >> 1) & 1) ^ 1)) break;
         {
           const uint8_t* const tile = ring + (kSlots + slot) * kRawBytes;
           const int e = sh.scales[1][slot][key >> 3] - sh.raw_unit[slot];
