@@ -35,7 +35,8 @@ struct Append8Params {
   AppendParams a;  // (its cache: the 16-bit pools; with 8 bits only n_heads counts)
   Paged8View c8;
   const float *q_weight, *k_weight;  // [D] or null: no norm
-  float eps;
+  float eps, inv_dims;  // 1 / D
+  int unit_floats; // of a position's cosines and sines
   int lanes;       // lanes of a row: a power of two
   int unit_warps;  // warps of a unit
 };
@@ -46,73 +47,109 @@ struct RowLane {
   bool live, two, paired;
 };
 
-// Two vectors whose dims' partners stand anywhere in the row: read one by one.  (Not
-// inlined: it would be most of the kernel's code, and the others waited for it.)
-struct Row16 {
-  float x[16];
-};
-template <typename T>
-__device__ __noinline__ Row16 turn_apart(Row16 v, int d0, int d1, int half, const uint16_t* row, const float2* cs,
-                                         const float* weight, float r) {
+// How a row's pairs stand: a whole number of vectors apart (both of a lane's vectors
+// turn together), side by side, or anywhere (the partner dims are read one by one).
+// A kernel each: code that a call does not use cost the others 10 to 20 percent.
+enum Pairs { kApart8, kNeighbours, kAnywhere };
+
+// two fp32 products at once
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void split2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+// Where cosine (or sine) of angle f stands in a position's table: kAnywhere in
+// order of f, else as the lanes read them, four of a lane's eight angles at a time,
+// neighbouring lanes side by side.
+template <Pairs kPairs>
+__device__ __forceinline__ int table_index(int f, int half, bool sine) {
+  if (kPairs == kAnywhere) return 2 * f + (sine ? 1 : 0);
+  const int vectors = (half + 7) >> 3, e = f & 7;
+  return (((sine ? 2 : 0) + (e >> 2)) * vectors + (f >> 3)) * 4 + (e & 3);
+}
+
+// The norms' factors of kRows rows (without weights): their sums of squares go over
+// the row's lanes side by side.  All lanes of a warp call it.
+template <typename T, int kRows>
+__device__ __forceinline__ void row_factors(const Append8Params& p, const uint4 (&a)[kRows], const uint4 (&b)[kRows],
+                                            float (&r)[kRows]) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int d = e < 8 ? d0 + e : d1 + e - 8;
-    if (d >= 2 * half) continue;
-    const bool first = d < half;
-    const int o = first ? d + half : d - half;
-    const float2 w = cs[unit_index(first ? d : o, half)];
-    float z = Pack16<T>::up(row[o]);
-    if (weight != nullptr) z = z * r * weight[o];
-    v.x[e] = fmaf(z, first ? -w.y : w.y, v.x[e] * w.x);
+  for (int i = 0; i < kRows; ++i) r[i] = 1.f;
+  if (p.q_weight == nullptr && p.k_weight == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    float x[8], y[8];
+    unpack8<T>(a[i], x);
+    unpack8<T>(b[i], y);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      s0 = fmaf(x[e], x[e], s0);
+      s1 = fmaf(y[e], y[e], s1);
+    }
+    r[i] = s0 + s1;
   }
-  return v;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    if (s >= p.lanes) continue;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) r[i] += __shfl_xor_sync(0xffffffffu, r[i], s);
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) r[i] = rsqrtf(fmaf(r[i], p.inv_dims, p.eps));
 }
 
 // A row's two vectors in fp32, normalised and rotated.  `row`: the row in memory
-// (pairs whose other dim is in no vector of the lane are read there).  All lanes
-// of a warp call it.
-template <typename T, bool kInterleaved>
+// (pairs whose other dim is in no vector of the lane are read there).
+// `weights`: float4s of w for this side in shared memory (weight_index), or null.
+template <typename T, Pairs kPairs>
 __device__ __forceinline__ void row_values(const Append8Params& p, const RowLane& u, uint4 av, uint4 bv, bool turn,
-                                           const float* weight, const uint16_t* row, const float2* cs, float (&x)[8],
-                                           float (&y)[8]) {
+                                           const float4* weights, const float* all_weights, const uint16_t* row,
+                                           float r, const float* cs, float (&x)[8], float (&y)[8]) {
   const int half = p.a.half, rot = 2 * half;
   unpack8<T>(av, x);
   unpack8<T>(bv, y);
-  float r = 1.f;
-  if (p.q_weight != nullptr || p.k_weight != nullptr) {
-    float sum = 0.f;
+  if (weights != nullptr) {
+    const uint64_t r2 = pair2(r, r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], fmaf(y[e], y[e], sum));
-    for (int s = p.lanes >> 1; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-    if (weight != nullptr) {
-      r = __frsqrt_rn(sum / static_cast<float>(p.a.D) + p.eps);
-      if (u.live) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * r * weight[u.d0 + e];
-        if (u.two) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = y[e] * r * weight[u.d1 + e];
-        }
-      }
+    for (int v = 0; v < 4; ++v) {
+      const float4 w = weights[v * p.lanes];
+      float* const z = v < 2 ? x + 4 * v : y + 4 * (v - 2);
+      split2(mul2(mul2(pair2(z[0], z[1]), r2), pair2(w.x, w.y)), z[0], z[1]);
+      split2(mul2(mul2(pair2(z[2], z[3]), r2), pair2(w.z, w.w)), z[2], z[3]);
     }
   }
-  if (!turn || !u.live) return;
-  if (u.paired || kInterleaved) {
-    if (kInterleaved && u.d0 >= rot) return;
+  if (!turn || !u.live || u.d0 >= rot) return;
+  if (kPairs != kAnywhere) {
+    if (kPairs == kApart8 && !u.paired) return;
+    // the lane's eight angles
+    const int vectors = (half + 7) >> 3;
+    const float4* const at = reinterpret_cast<const float4*>(cs) + (kPairs == kApart8 ? u.d0 >> 3 : u.d0 >> 4);
     float c[8], s[8];
+    *reinterpret_cast<float4*>(c) = at[0];
+    *reinterpret_cast<float4*>(c + 4) = at[vectors];
+    *reinterpret_cast<float4*>(s) = at[2 * vectors];
+    *reinterpret_cast<float4*>(s + 4) = at[3 * vectors];
+    if (kPairs == kApart8) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int f = kInterleaved ? (u.d0 >> 1) + e : u.d0 + e;
-      const float2 w = f < half ? cs[unit_index(f, half)] : make_float2(1.f, 0.f);
-      c[e] = w.x;
-      s[e] = w.y;
-    }
-    if (!kInterleaved) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float t = fmaf(y[e], -s[e], x[e] * c[e]);
-        y[e] = fmaf(x[e], s[e], y[e] * c[e]);
-        x[e] = t;
+      for (int e = 0; e < 8; e += 2) {
+        const uint64_t x2 = pair2(x[e], x[e + 1]), y2 = pair2(y[e], y[e + 1]), c2 = pair2(c[e], c[e + 1]);
+        split2(fma2(y2, pair2(-s[e], -s[e + 1]), mul2(x2, c2)), x[e], x[e + 1]);
+        split2(fma2(x2, pair2(s[e], s[e + 1]), mul2(y2, c2)), y[e], y[e + 1]);
       }
     } else {
 #pragma unroll
@@ -129,25 +166,27 @@ __device__ __forceinline__ void row_values(const Append8Params& p, const RowLane
         }
       }
     }
-  } else if (u.d0 < rot && (half & 7) != 0) {  // pairs not a whole number of vectors apart
-    Row16 v;
+  } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v.x[e] = x[e];
-      v.x[8 + e] = y[e];
-    }
-    v = turn_apart<T>(v, u.d0, u.two ? u.d1 : rot, half, row, cs, weight, r);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = v.x[e];
-      y[e] = v.x[8 + e];
+    for (int e = 0; e < 16; ++e) {
+      const int d = e < 8 ? u.d0 + e : u.d1 + e - 8;
+      if (d >= rot || (e >= 8 && !u.two)) continue;
+      const bool first = d < half;
+      const int o = first ? d + half : d - half;
+      const float2 w = reinterpret_cast<const float2*>(cs)[first ? d : o];
+      float z = Pack16<T>::up(row[o]);
+      if (weights != nullptr) z = z * r * all_weights[o];
+      float& to = e < 8 ? x[e & 7] : y[e & 7];
+      to = fmaf(z, first ? -w.y : w.y, to * w.x);
     }
   }
 }
 
-template <typename T, bool kInterleaved, bool k8>
-__global__ void __launch_bounds__(kA8Threads, 2) append_norm_kernel(const __grid_constant__ Append8Params p) {
-  extern __shared__ float2 ap_units[];  // [positions of the CTA][half]
+// Three CTAs an SM with a 16-bit cache, two with an 8-bit one, whose units take
+// 64 registers.
+template <typename T, Pairs kPairs, bool k8>
+__global__ void __launch_bounds__(kA8Threads, k8 ? 2 : 3) append_norm_kernel(const __grid_constant__ Append8Params p) {
+  extern __shared__ __align__(16) float ap8_units[];  // [positions of the CTA][unit_floats]
   __shared__ int64_t s_dst[kA8MaxOwn];  // element offset of the entry in the pools, -1: not written
   __shared__ int64_t s_entry[kA8MaxOwn];
   __shared__ int s_page[kA8MaxOwn];
@@ -155,6 +194,7 @@ __global__ void __launch_bounds__(kA8Threads, 2) append_norm_kernel(const __grid
   __shared__ int16_t s_lead[kA8MaxOwn + 1];  // places of the leads, then the end
   __shared__ int s_begin, s_end, s_leads;
   __shared__ float s_top[kA8Warps];
+  __shared__ float4 s_weights[2][4 * 32];  // [query, key][a lane's fourths of 16 dims][lane of a row]
   const PagedBatch& batch = p.a.batch;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n0 = static_cast<int>(blockIdx.x) * p.a.tile;
@@ -165,6 +205,21 @@ __global__ void __launch_bounds__(kA8Threads, 2) append_norm_kernel(const __grid
   const int64_t page_stride = k8 ? p.c8.page_stride : p.a.cache.page_stride;
   const int64_t slot_stride = k8 ? p.c8.slot_stride : p.a.cache.slot_stride;
   const int64_t n_pages = k8 ? p.c8.n_pages : p.a.cache.n_pages;
+  // ---- this lane's part of every row it visits ----
+  const int vpr = p.a.D >> 3, upr = (vpr + 1) >> 1, rows_at_once = 32 / p.lanes;
+  const int u = lane & (p.lanes - 1), row_of_warp = lane / p.lanes;
+  const int hv = p.a.half >> 3;
+  // the unit u of a row: the first vectors of its two
+  auto first_vector = [&](int u) {
+    return kPairs != kApart8 ? 2 * u : u < hv ? u : 2 * hv + 2 * (u - hv);
+  };
+  auto second_vector = [&](int u) { return kPairs == kApart8 && u < hv ? u + hv : first_vector(u) + 1; };
+  RowLane my;
+  my.live = u < upr;
+  my.paired = kPairs == kApart8 && u < hv;
+  my.two = second_vector(u) < vpr;
+  my.d0 = 8 * first_vector(u);
+  my.d1 = 8 * second_vector(u);
   grid_dep_launch();
   grid_dep_wait();
 
@@ -175,6 +230,17 @@ __global__ void __launch_bounds__(kA8Threads, 2) append_norm_kernel(const __grid
     if (at > batch.q_indptr[b + 1] || (b == 0 && at != 0) || (b == batch.B - 1 && batch.q_indptr[b + 1] > batch.N))
       atomicOr(batch.status, kStatusBadCache);
   }
+
+  // the norms' weights as the lanes read them: neighbours side by side
+  if (p.q_weight != nullptr || p.k_weight != nullptr) {
+    const int i = tid & 127, side = tid >> 7, v = i / p.lanes, l = i - v * p.lanes;  // fourth v of lane l's dims
+    const float* const from = side == 0 ? p.q_weight : p.k_weight;
+    const int d = 8 * (v < 2 ? first_vector(l) : second_vector(l)) + 4 * (v & 1);
+    if (v < 4 && from != nullptr)
+      s_weights[side][i] = d + 4 <= p.a.D ? make_float4(from[d], from[d + 1], from[d + 2], from[d + 3]) : make_float4(0, 0, 0, 0);
+  }
+  const float4* const q_weights = p.q_weight != nullptr ? s_weights[0] + u : nullptr;
+  const float4* const k_weights = p.k_weight != nullptr ? s_weights[1] + u : nullptr;
 
   // ---- the entries of the positions, a thread each ----
   for (int t = tid; t < look; t += kA8Threads) {
@@ -250,25 +316,17 @@ __global__ void __launch_bounds__(kA8Threads, 2) append_norm_kernel(const __grid
         const int64_t pos = p.a.positions != nullptr
                                 ? static_cast<int64_t>(p.a.positions[static_cast<int64_t>(a) * batch.N + n0 + t])
                                 : p.a.position_base + s_entry[t];
-        if (in_bounds(t < kA8MaxOwn && unit_index(f, p.a.half) >= 0 && unit_index(f, p.a.half) < p.a.half, batch.status))
-          ap_units[(t - begin) * p.a.half + unit_index(f, p.a.half)] = unit_of(pos, turn64);
+        const int c = table_index<kPairs>(f, p.a.half, false), s = table_index<kPairs>(f, p.a.half, true);
+        if (in_bounds(t < kA8MaxOwn && c >= 0 && c < p.unit_floats && s >= 0 && s < p.unit_floats, batch.status)) {
+          const float2 w = unit_of(pos, turn64);
+          ap8_units[(t - begin) * p.unit_floats + c] = w.x;
+          ap8_units[(t - begin) * p.unit_floats + s] = w.y;
+        }
       }
     }
     __syncthreads();
   }
 
-  // ---- this lane's part of every row it visits ----
-  const int vpr = p.a.D >> 3, upr = (vpr + 1) >> 1, rows_at_once = 32 / p.lanes;
-  const int u = lane & (p.lanes - 1), row_of_warp = lane / p.lanes;
-  const int hv = p.a.half >> 3;
-  RowLane my;
-  my.live = u < upr;
-  my.paired = !kInterleaved && (p.a.half & 7) == 0 && u < hv;
-  const int v0 = my.paired ? u : !kInterleaved && (p.a.half & 7) == 0 ? 2 * hv + 2 * (u - hv) : 2 * u;
-  const int v1 = my.paired ? u + hv : v0 + 1;
-  my.two = v1 < vpr;
-  my.d0 = 8 * v0;
-  my.d1 = 8 * v1;
   const int Hq = p.a.n_q_heads, Hk = p.a.cache.n_heads;
 
   // ---- queries (and with a 16-bit cache keys and values): (position, row) pairs in one sequence ----
@@ -309,14 +367,17 @@ __global__ void __launch_bounds__(kA8Threads, 2) append_norm_kernel(const __grid
           ++t_first;
         }
       }
+      float factors[kAppendBatch];
+      row_factors<T>(p, a, b, factors);
 #pragma unroll
       for (int i = 0; i < kAppendBatch; ++i) {
         const int t = max(ts[i], begin), row = rs[i];
         const int64_t n = n0 + t;
         const bool is_q = row < Hq, is_v = row >= Hq + Hk;
         float x[8], y[8];
-        row_values<T, kInterleaved>(p, my, a[i], b[i], ts[i] >= 0 && !is_v, is_v ? nullptr : is_q ? p.q_weight : p.k_weight,
-                                    p.a.row_src(n, row), ap_units + (t - begin) * p.a.half, x, y);
+        row_values<T, kPairs>(p, my, a[i], b[i], ts[i] >= 0 && !is_v, is_v ? nullptr : is_q ? q_weights : k_weights,
+                              is_q ? p.q_weight : p.k_weight, p.a.row_src(n, row), factors[i],
+                              ap8_units + (t - begin) * p.unit_floats, x, y);
         if (ts[i] < 0) continue;
         uint16_t* dst;
         if (is_q) {
@@ -365,14 +426,15 @@ __global__ void __launch_bounds__(kA8Threads, 2) append_norm_kernel(const __grid
         b[i] = ld_once(src + my.d1);  // D is a multiple of 16: there are always two
       }
     }
-    float x[kA8Steps][8], y[kA8Steps][8], top = 0.f;
+    float x[kA8Steps][8], y[kA8Steps][8], factors[kA8Steps], top = 0.f;
+    row_factors<T>(p, a, b, factors);
 #pragma unroll
     for (int i = 0; i < kA8Steps; ++i) {
       const int r = (i * p.unit_warps + part) * rows_at_once + row_of_warp;
       const bool mine = writes && r < rows;
       const int t = t0 + (mine ? r : 0);
-      row_values<T, kInterleaved>(p, my, a[i], b[i], mine && !is_v, is_v ? nullptr : p.k_weight,
-                                  p.a.row_src(n0 + t, Hq + h), ap_units + (t - begin) * p.a.half, x[i], y[i]);
+      row_values<T, kPairs>(p, my, a[i], b[i], mine && !is_v, is_v ? nullptr : k_weights, p.k_weight,
+                            p.a.row_src(n0 + t, Hq + h), factors[i], ap8_units + (t - begin) * p.unit_floats, x[i], y[i]);
       if (mine && my.live) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(finite_abs(x[i][e]), finite_abs(y[i][e])));

@@ -16,7 +16,7 @@ using namespace specv;
 
 namespace {
 
-constexpr int kAppendSmem = 48 * 1024;
+constexpr int kAppendSmem = 32 * 1024;
 constexpr int kAppend8Smem = kA8MaxOwn * 128 * static_cast<int>(sizeof(float2));  // rotated pairs of up to 256 dims
 
 struct Device8 {
@@ -52,10 +52,12 @@ int device8_sms(int* sms) {
         !raise(attend8_kernel<__nv_bfloat16, 128>, q8_smem_bytes<128>()) ||
         !raise(attend8_kernel<__half, 64>, q8_smem_bytes<64>()) ||
         !raise(attend8_kernel<__half, 128>, q8_smem_bytes<128>()) ||
-        !raise(append_norm_kernel<__nv_bfloat16, false, true>, kAppend8Smem) ||
-        !raise(append_norm_kernel<__nv_bfloat16, true, true>, kAppend8Smem) ||
-        !raise(append_norm_kernel<__half, false, true>, kAppend8Smem) ||
-        !raise(append_norm_kernel<__half, true, true>, kAppend8Smem))
+        !raise(append_norm_kernel<__nv_bfloat16, kApart8, true>, kAppend8Smem) ||
+        !raise(append_norm_kernel<__nv_bfloat16, kNeighbours, true>, kAppend8Smem) ||
+        !raise(append_norm_kernel<__nv_bfloat16, kAnywhere, true>, kAppend8Smem) ||
+        !raise(append_norm_kernel<__half, kApart8, true>, kAppend8Smem) ||
+        !raise(append_norm_kernel<__half, kNeighbours, true>, kAppend8Smem) ||
+        !raise(append_norm_kernel<__half, kAnywhere, true>, kAppend8Smem))
       return SPEC_ERR_CUDA;
     d.ready = true;
   }
@@ -134,8 +136,9 @@ bool encode_pool8(CUtensorMap* m, const void* base, const spec_kv_cache8* c, int
 template <typename T, bool k8>
 int launch_norm(const Append8Params& p, int interleaved, size_t smem, cudaStream_t s) {
   const dim3 grid((p.a.batch.N + p.a.tile - 1) / p.a.tile);
-  const cudaError_t e = interleaved ? launch_pdl(append_norm_kernel<T, true, k8>, grid, dim3(kA8Threads), smem, s, p)
-                                    : launch_pdl(append_norm_kernel<T, false, k8>, grid, dim3(kA8Threads), smem, s, p);
+  const cudaError_t e = interleaved ? launch_pdl(append_norm_kernel<T, kNeighbours, k8>, grid, dim3(kA8Threads), smem, s, p)
+                        : p.a.half % 8 == 0 ? launch_pdl(append_norm_kernel<T, kApart8, k8>, grid, dim3(kA8Threads), smem, s, p)
+                                            : launch_pdl(append_norm_kernel<T, kAnywhere, k8>, grid, dim3(kA8Threads), smem, s, p);
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
@@ -157,7 +160,10 @@ int append_norm(Append8Params& p, int dtype, int block, const float* q_weight, c
   p.unit_warps = k8 ? block * p.lanes / (32 * kA8Steps) : 1;
   if (p.unit_warps < 1) p.unit_warps = 1;
   p.a.tile = (p.a.batch.N + 3 * sms - 1) / (3 * sms);
-  const int bytes = p.a.half * static_cast<int>(sizeof(float2)), rest = k8 ? block - 1 : 0;
+  // the cosines and sines of a position: vectors of eight angles, but for pairs anywhere
+  p.unit_floats = !interleaved && p.a.half % 8 != 0 ? 2 * p.a.half : 16 * ((p.a.half + 7) / 8);
+  p.inv_dims = 1.f / static_cast<float>(p.a.D);
+  const int bytes = p.unit_floats * static_cast<int>(sizeof(float)), rest = k8 ? block - 1 : 0;
   const int most = !k8 && p.a.half > 0 ? kAppendSmem / bytes : kAppendMaxTile;
   if (p.a.tile > most) p.a.tile = most;
   if (p.a.tile > kAppendMaxTile) p.a.tile = kAppendMaxTile;
