@@ -72,6 +72,27 @@ __device__ __forceinline__ void split2(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
 
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("{\n\t.reg .f32 x, y;\n\tabs.f32 x, %2;\n\tabs.f32 y, %3;\n\tmax.f32 %0, %1, x, y;\n\t}" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// code8 of values whose finite ones are below the largest code: x * inv, and an
+// infinity times 0 makes it NaN.
+__device__ __forceinline__ uint2 code8_near(const float* x, float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t z = mul2(pair2(x[2 * i], x[2 * i + 1]), pair2(inv, inv));
+    float a, b;
+    split2(fma2(z, pair2(0.f, 0.f), z), a, b);
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(b), "f"(a));  // the first goes to the high byte
+    w[i] = d;
+  }
+  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
 // Where cosine (or sine) of angle f stands in a position's table: kAnywhere in
 // order of f, else as the lanes read them, four of a lane's eight angles at a time,
 // neighbouring lanes side by side.
@@ -435,9 +456,20 @@ __global__ void __launch_bounds__(kA8Threads, k8 ? 2 : 3) append_norm_kernel(con
       const int t = t0 + (mine ? r : 0);
       row_values<T, kPairs>(p, my, a[i], b[i], mine && !is_v, is_v ? nullptr : k_weights, p.k_weight,
                             p.a.row_src(n0 + t, Hq + h), factors[i], ap8_units + (t - begin) * p.unit_floats, x[i], y[i]);
-      if (mine && my.live) {
+      if (mine && my.live) {  // (a NaN is no maximum)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(finite_abs(x[i][e]), finite_abs(y[i][e])));
+        for (int e = 0; e < 8; ++e) top = max3_abs(top, x[i][e], y[i][e]);
+      }
+    }
+    if (__any_sync(0xffffffffu, top == INFINITY)) {  // an infinity does not count
+      top = 0.f;
+#pragma unroll
+      for (int i = 0; i < kA8Steps; ++i) {
+        const int r = (i * p.unit_warps + part) * rows_at_once + row_of_warp;
+        if (writes && r < rows && my.live) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(finite_abs(x[i][e]), finite_abs(y[i][e])));
+        }
       }
     }
 #pragma unroll
@@ -468,6 +500,7 @@ __global__ void __launch_bounds__(kA8Threads, k8 ? 2 : 3) append_norm_kernel(con
       }
     }
     const float inv = two_to(-now);
+    const bool far = now == Scale8<T>::kHigh;  // values may lie past the largest code
 #pragma unroll
     for (int i = 0; i < kA8Steps; ++i) {
       const int r = (i * p.unit_warps + part) * rows_at_once + row_of_warp;
@@ -477,8 +510,8 @@ __global__ void __launch_bounds__(kA8Threads, k8 ? 2 : 3) append_norm_kernel(con
                      batch.status))
         continue;
       uint8_t* const at = pool + dst0 + r * p.c8.slot_stride + head * p.c8.head_stride;
-      *reinterpret_cast<uint2*>(at + my.d0) = code8(x[i], inv, most);
-      *reinterpret_cast<uint2*>(at + my.d1) = code8(y[i], inv, most);
+      *reinterpret_cast<uint2*>(at + my.d0) = far ? code8(x[i], inv, most) : code8_near(x[i], inv);
+      *reinterpret_cast<uint2*>(at + my.d1) = far ? code8(y[i], inv, most) : code8_near(y[i], inv);
     }
   }
 }
