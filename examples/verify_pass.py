@@ -15,6 +15,9 @@ no later one is visible; its last layer looks HOP positions back and copies what
 the first one left there.  Without its layers it would count on from the newest
 token.
 
+The cache is one of 16 bits, or (codes=True) of 8: e4m3 codes with a scale for each
+page and head, through spec_kv_append8 and spec_prefix_attention8.
+
     python examples/verify_pass.py            # needs the GPU and the built library
 """
 import os
@@ -81,12 +84,20 @@ class Target:
 class Cache:
     """Pages of every layer, the prefix's and the sequences' tables."""
 
-    def __init__(self, model, B, prefix_len, max_len, device="cuda"):
+    def __init__(self, model, B, prefix_len, max_len, device="cuda", codes=False):
         shared, width = -(-prefix_len // PAGE), -(-max_len // PAGE)
         total = shared + B * width
         shape = (total, PAGE, model.n_heads, model.D)
-        self.layers = [sv.make_kv_cache(*(torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in "kv"))
-                       for _ in model.layers]
+        if codes:
+            def pools():
+                return [torch.zeros(shape, dtype=torch.uint8, device=device) for _ in "kv"] + \
+                    [torch.zeros((total, 1, model.n_heads), dtype=torch.uint8, device=device) for _ in "kv"]
+            self.layers = [sv.make_kv_cache8(*pools()) for _ in model.layers]
+            self.append, self.attend = sv.spec_kv_append8, sv.spec_prefix_attention8
+        else:
+            self.layers = [sv.make_kv_cache(*(torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in "kv"))
+                           for _ in model.layers]
+            self.append, self.attend = sv.spec_kv_append, sv.spec_prefix_attention
         order = torch.randperm(total, device=device, dtype=torch.int32)
         self.prefix_table, self.prefix_len = order[:shared].contiguous(), prefix_len
         self.table = order[shared:].reshape(B, width).contiguous()
@@ -106,10 +117,10 @@ def forward(model, cache, tokens, q_len, kv_len, table, prefix_len, ws):
     for (w_qkv, w_out), layer in zip(model.layers, cache.layers):
         x = torch.nn.functional.rms_norm(h, (model.hidden,))
         q, k, v = (x @ w_qkv.T).split([Hq * D, Hk * D, Hk * D], dim=1)
-        sv.spec_kv_append(layer, q.unflatten(1, (Hq, D)), k.unflatten(1, (Hk, D)), v.unflatten(1, (Hk, D)), q_turned,
-                          indptr, table, lens, ws, inv_freq=model.inv_freq, position_base=prefix_len)
-        sv.spec_prefix_attention(layer, q_turned, out, indptr, table, lens, ws, prefix_table=cache.prefix_table,
-                                 prefix_len=prefix_len)
+        cache.append(layer, q.unflatten(1, (Hq, D)), k.unflatten(1, (Hk, D)), v.unflatten(1, (Hk, D)), q_turned,
+                     indptr, table, lens, ws, inv_freq=model.inv_freq, position_base=prefix_len)
+        cache.attend(layer, q_turned, out, indptr, table, lens, ws, prefix_table=cache.prefix_table,
+                     prefix_len=prefix_len)
         h = h + out.flatten(1) @ w_out.T
     return torch.nn.functional.rms_norm(h, (model.hidden,))
 
@@ -124,14 +135,14 @@ def draft(text, gamma, vocab):
     return text[first:]
 
 
-def generate(model, prefix, prompts, new_tokens, gamma):
+def generate(model, prefix, prompts, new_tokens, gamma, codes=False):
     """Greedy continuations of `prompts` behind the shared `prefix`, `gamma`
-    drafts a round (0: plain decoding).  Returns the tokens and the number of
+    drafts a round (0: plain decoding), over a cache of 16 bits or of 8.  Returns the tokens and the number of
     passes of the target."""
     device = prefix.device
     B = len(prompts)
     max_len = max(p.shape[0] for p in prompts) + new_tokens + gamma + 1
-    cache = Cache(model, B, prefix.shape[0], max_len, device)
+    cache = Cache(model, B, prefix.shape[0], max_len, device, codes)
     most = max(prefix.shape[0], sum(p.shape[0] for p in prompts), B * (gamma + 1))
     ws = sv.make_attention_workspace(B, most, model.n_q_heads, model.D, device)
     # the prefix once, as a sequence that lives in the shared pages
@@ -198,9 +209,12 @@ def main():
     prefix, prompts = inputs(model)
     plain, plain_passes = generate(model, prefix, prompts, 48, 0)
     spec, spec_passes = generate(model, prefix, prompts, 48, 4)
+    small, small_passes = generate(model, prefix, prompts, 48, 4, codes=True)
     same = sum(a == b for x, y in zip(plain, spec) for a, b in zip(x, y))
     print(f"plain: {plain_passes} passes, speculative: {spec_passes} passes, "
           f"{same} of {sum(map(len, plain))} tokens the same")
+    same = sum(a == b for x, y in zip(plain, small) for a, b in zip(x, y))
+    print(f"over a cache in 8 bits: {small_passes} passes, {same} tokens the same")
     return plain, spec, plain_passes, spec_passes
 
 

@@ -9,26 +9,50 @@
 //                                     key), Q from shared memory
 //   O^T += V^T P^T [dims x rows]      V, converted, and P from shared memory
 //
-// The keys are the 128 lanes of a product and the rows its columns: 32, 64 or
+// The keys are the 128 lanes of a product and the rows its columns: 16, 32, 64 or
 // 128 of them, as many as an item has, where the other way around a decode step's few
 // rows would take a product's 128 lanes and its softmax those lanes' exponentials.
 // A key converted for S^T goes straight to TMEM, not through shared memory.
 //
+// Types.  The products are fp16 with a bf16 cache too, wherever that is exact: the
+// conversion from e4m3 is one instruction a pair, and to bf16 it is ten.  A key's
+// scale counts in its scores, not in its values; queries are multiples of one power
+// of two (a part whose rows differ by more than 2^20, or are not finite, keeps bf16
+// queries and keys); values are multiples of another (a tile with blocks too small
+// for it has bf16 values and weights).
+//
 // An item is a row tile (up to 128 rows) against all tiles of 128 keys it sees.
 // One CTA per SM, 16 warps:
-//   warps 0-3, 4-7   softmax groups 0 and 1: a thread a key, each group half of
-//                    the columns.  Weights go to shared memory as P.
-//   warps 8-11       converters: a thread a key: its codes from the raw ring, as
+//   warps 0-3, 4-7   softmax groups 0 and 1, a thread a key.  Up to 64 rows they
+//                    alternate tiles, each with a reference, sums and an O of its own
+//                    that are joined at the end of the part; above, they share each
+//                    tile's columns.  Weights go to shared memory as P.
+//   warps 8-11       converters, a thread a key: its codes from the raw ring, as
 //                    16-bit values to TMEM (K) or to a swizzled tile (V; past the
-//                    last entry zeros).
+//                    last entry zeros); at a part's start its queries.
 //   warp 12          the scheduler, as in attend.cuh; warp 13 issues the products;
 //   warps 14, 15     load key and value codes (TMA) and the blocks' scales.
 // TMEM: two S^T (128 columns each), O^T (128), two K (D / 2 each).
 //
 // A row's reference m is shared by the 128 threads of a group: a barrier with a
-// vote per tile says whether any score passes it by more than 2^8, and only then
-// are the columns' maxima taken and O and the sums multiplied.  The sums are
-// kept by key in registers (fp32) and added up over the lanes once a part.
+// vote per tile says whether any weight passes 2^15, and only then are the columns'
+// maxima taken and O and the sums multiplied.  The sums are kept by key in
+// registers (fp32) and added up over the lanes once a part.
+//
+// What bounds it.  16 caches of up to 32,768 entries (472 MB): 127 us, 3.7 TB/s (the
+// 16-bit call 150 us on twice the bytes).  A tile of 128 keys takes 2,400 clocks
+// with few rows; HBM would need 1,450.  Two chains are that long: the converters'
+// (keys 450, values 950, four waits) and the issuer's (16 products of 50 to 60
+// clocks each as issued, and their waits).  With 128 rows it is the softmax warps'
+// 3,500.  All of it runs at the rate of instruction fetches (a warp of every
+// SM quarter has code of its own): loops that are not unrolled, and code that runs
+// once a part kept short, took long caches from 385 to 127 us, long drafts from 2,083 to
+// 670.  Tried and not kept: converters for keys and values apart, 20 warps (160
+// registers for the softmax, more code at once: 138 us and 905); an issuer for
+// each product besides (180 and 1,059); products unrolled with their operands in
+// uniform registers (15 clocks an instruction by itself, no change here); values
+// converted four vectors at a time, or one ahead (127 to 133); bf16 products
+// throughout (207 and 1,091).
 #pragma once
 
 #include "attend.cuh"

@@ -167,6 +167,8 @@ int append_norm(Append8Params& p, int dtype, int block, const float* q_weight, c
   const int most = !k8 && p.a.half > 0 ? kAppendSmem / bytes : kAppendMaxTile;
   if (p.a.tile > most) p.a.tile = most;
   if (p.a.tile > kAppendMaxTile) p.a.tile = kAppendMaxTile;
+  // whole blocks, so that the CTAs have equally many
+  if (k8 && p.a.tile > block) p.a.tile -= p.a.tile % block;
   const size_t smem = static_cast<size_t>(p.a.tile + rest) * bytes;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dtype == SPEC_BF16 ? launch_norm<__nv_bfloat16, k8>(p, interleaved, smem, s)

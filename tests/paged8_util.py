@@ -17,16 +17,13 @@ class Problem8(Problem):
         self.codes, self.scales = [], []
         for i in range(2):
             x = self.pools[i].double().cpu().numpy() * 2.0 ** rng.uniform(-spread, spread, self.pools[i].shape[:3])[..., None]
-            codes = np.full(x.shape, 0x7F, dtype=np.uint8)
-            scales = np.full((x.shape[0], page // block, Hk), 255, dtype=np.uint8)
-            for p in range(x.shape[0]):
-                for k in range(page // block):
-                    for h in range(Hk):
-                        part = x[p, k * block:(k + 1) * block, h]
-                        if np.isfinite(part).any():
-                            e = paged8.exponent(part, dtype)
-                            scales[p, k, h] = e + 127
-                            codes[p, k * block:(k + 1) * block, h] = paged8.quantise(part, e, dtype)
+            # (paged8.exponent and quantise for all blocks at once)
+            blocks = x.reshape(x.shape[0], page // block, block, Hk, D)
+            live = np.isfinite(blocks)
+            top = np.abs(np.where(live, blocks, 0)).max(axis=(2, 4))
+            e = np.maximum(np.frexp(top)[1] - 8, paged8.LOW[dtype])
+            scales = np.where(live.any(axis=(2, 4)), e + 127, 255).astype(np.uint8)
+            codes = paged8.quantise(blocks, e[:, :, None, :, None].astype(np.float64), dtype).reshape(x.shape)
             self.codes.append(self._pool(codes, heads_first))
             self.scales.append(torch.from_numpy(scales).cuda())
         self.refresh()
