@@ -72,7 +72,7 @@ struct Attend8Params : AttendParams {
   Paged8View c8;
   // As AttendParams has them: a key tile takes some 3,600 clocks with over 64 rows
   // and 2,300 with fewer, a part's queries, first scores and results 12,000.
-  static constexpr int kWide = 9, kNarrow = 6, kFixed = 30;
+  static constexpr int kWide = 10, kNarrow = 6, kFixed = 24;
   static constexpr bool kCodes = true;
   __device__ __forceinline__ int64_t head_stride() const { return c8.head_stride; }
   __device__ __forceinline__ int64_t entry_at(int64_t page, int slot) const {
