@@ -19,7 +19,11 @@
 // its scale only rises, and when it does their codes are rewritten (exact but
 // for e4m3's subnormals).
 //
-// Bound by the copies: q, k, v read once, q (16 bits) and codes written once.
+// What bounds it: q, k, v read once, q (16 bits) and codes written once.  To 16 bits
+// 32,768 positions of 256 dims take 186 us, 5.8 TB/s (0.86 of the measured copy
+// bandwidth).  To 8 bits some 16,400 positions of 32 + 8 + 8 heads of 128 take 107 us
+// for 62: a unit's 64 values a lane leave two CTAs an SM (computed twice instead, for
+// three CTAs, they spill: 130 us).  CTAs of whole blocks: 107 us, of 24 positions 118.
 #pragma once
 
 #include "kvappend.cuh"
