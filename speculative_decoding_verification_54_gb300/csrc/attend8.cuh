@@ -51,8 +51,9 @@
 // registers for the softmax, more code at once: 138 us and 905); an issuer for
 // each product besides (180 and 1,059); products unrolled with their operands in
 // uniform registers (15 clocks an instruction by itself, no change here); values
-// converted four vectors at a time, or one ahead (127 to 133); bf16 products
-// throughout (207 and 1,091).
+// converted four vectors at a time, or one ahead (127 to 133); values converted by
+// the softmax groups (129 and 778), and the next scores issued before the output
+// besides (128 and 894); bf16 products throughout (207 and 1,091).
 #pragma once
 
 #include "attend.cuh"
