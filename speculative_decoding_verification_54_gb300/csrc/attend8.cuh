@@ -68,6 +68,7 @@ static_assert(2 * kQ8SoftmaxRegs + kQ8ConvertRegs + kQ8OtherRegs == kQ8Threads /
               "a share above the launch's registers would be waited for for ever");
 constexpr int kQ8Queue = 2;          // parts queued ahead
 constexpr float kQ8Unset = 3.0e38f;  // minus the reference of a row that has seen nothing
+constexpr float kQ8LeastFactor = 0x1p-126f, kQ8MostFactor = 0x1p127f;  // of a score
 
 struct Attend8Params : AttendParams {
   Paged8View c8;
@@ -349,7 +350,9 @@ struct Q8Softmax {
       ok = wait(&sh.s_full[j & 1], (j >> 1) & 1) && ok;
       tc_fence_after();
       // this key's scale (its converter's write came before its product)
-      const float scale = q_scale * two_to(sh.key_exp[j & 3][key >> 3]);
+      // Neither 0 nor infinite: a hidden score (-infinity) times 0 or a score of 0 times
+      // infinity would be NaN.  (What is raised to 2^-126 has scores below 2^-90.)
+      const float scale = fminf(fmaxf(q_scale * two_to(sh.key_exp[j & 3][key >> 3]), kQ8LeastFactor), kQ8MostFactor);
       const uint64_t scale2 = f32x2(scale, scale);
       const bool ragged = open - t * kAtTile < kAtTile;
       uint64_t bits = ~0ull;
