@@ -123,6 +123,7 @@ struct AttendParams {
   static constexpr int kWide = 8, kNarrow = 5, kFixed = 15;
   // the cache's entries one by one: 16-bit values as they are
   static constexpr bool kCodes = false;
+  static constexpr float kFar = INFINITY;
   __device__ __forceinline__ int64_t head_stride() const { return cache.head_stride; }
   __device__ __forceinline__ int64_t entry_at(int64_t page, int slot) const {
     return page * cache.page_stride + slot * cache.slot_stride;
@@ -1021,7 +1022,9 @@ __device__ __noinline__ void sum_row_again(const P& p, int n, int hq, float m, f
           for (int e = 0; e < 8; ++e) dot = fmaf(x[e], y[e], dot);
         }
       }
-      const float w = ex2(fmaf(dot, p.scale_log2, -m)) * inv;
+      // (the sum's scores past kFar were rounded first)
+      const float x = P::kCodes && fabsf(m) >= P::kFar ? __fadd_rn(__fmul_rn(dot, p.scale_log2), -m) : fmaf(dot, p.scale_log2, -m);
+      const float w = ex2(x) * inv;
       const unsigned any = __ballot_sync(0xffffffffu, valid);
 #pragma unroll 1
       for (int u = 0; u < 32; u += 4) {

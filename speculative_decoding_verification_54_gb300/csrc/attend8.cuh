@@ -76,6 +76,9 @@ struct Attend8Params : AttendParams {
   // and 2,300 with fewer, a part's queries, first scores and results 12,000.
   static constexpr int kWide = 10, kNarrow = 6, kFixed = 24;
   static constexpr bool kCodes = true;
+  // Scores (log2) from which fp32's step is 2: the difference that a product and sum in
+  // one leaves between the score of a row's maximum and its rounded reference.
+  static constexpr float kFar = 0x1p24f;
   __device__ __forceinline__ int64_t head_stride() const { return c8.head_stride; }
   __device__ __forceinline__ int64_t entry_at(int64_t page, int slot) const {
     return page * c8.page_stride + slot * c8.slot_stride;
@@ -106,7 +109,12 @@ struct Q8Shared {
   uint64_t kc_full[2], vc_full[2];
   uint64_t s_full[2], pv_done[2];  // the products of tile j (places j % 2) are complete: their operands too are free
   uint64_t p_full[2], meet[2], o_free, q_full[2], q_ready[2], q_empty[2], part_full[kQ8Queue], part_empty[kQ8Queue], done;
-  __align__(16) float neg_ref[2][kAtTile / 2];  // per group: minus its columns' references (log2)
+  __align__(16) float neg_ref[2][kAtTile / 2];  // per group: minus its columns' references (log2); 0 where far
+  float ref[2][kAtTile / 2];                    // the same, far or not
+  // Infinite once a reference of the part has passed kFar, else -infinity.  All tiles then take
+  // the way of those whose references are set, which puts scores less references into TMEM.
+  float far[2];
+  int columns[2];                               // of the groups' that are rows
   float unit[2];                                // log2 of the unit of the groups' O
   int8_t scales[2][kSlots][16];                 // [keys, values] exponents of 8 keys each
   int8_t key_exp[4][16];                        // of the keys of tile j % 4
@@ -230,6 +238,23 @@ template <typename T>
 constexpr float kQ8Top = std::is_same<T, __half>::value ? 7.f : 4.f;
 constexpr float kQ8Most = 15.f;
 
+// Scores in TMEM, rounded, less their references, over the factor (off by 2^-23 of the
+// difference): a reference of 0 then gives their weights.
+inline __device__ __noinline__ void far_scores(uint32_t tm, int columns, float scale, const float* ref) {
+  float less;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(less) : "f"(scale));
+#pragma unroll 1
+  for (int c = 0; c < columns; c += 8) {
+    uint32_t s[8];
+    tmem_load<8>(tm + c, s);
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      s[x] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(s[x]), scale), ref[c + x]) * less);
+    tmem_st8(tm + c, s);
+  }
+  tmem_st_wait();
+}
+
 template <typename T, int D>
 struct Q8Softmax {
   const Attend8Params& p;
@@ -334,7 +359,11 @@ struct Q8Softmax {
     const int tiles = a.t1 - a.t0, rows = a.n0 * p.group;
     // entries below this one are seen by all rows
     const int open = a.line == 0 ? a.len : p.draft_mask != nullptr ? a.old : a.old + (a.first - a.seq_first) + 1;
-    if (mine < C) neg_ref[mine] = kQ8Unset;
+    if (mine < C) neg_ref[mine] = sh.ref[g][mine] = kQ8Unset;
+    if (mine == 0) {
+      sh.far[g] = -INFINITY;
+      sh.columns[g] = rows - col0;
+    }
     uint64_t l2[C / 2];
 #pragma unroll
     for (int c = 0; c < C / 2; ++c) l2[c] = 0;
@@ -371,7 +400,7 @@ struct Q8Softmax {
       // the values changed) the references are set anew, and once more.
 #pragma unroll 1
       for (int turn = 0;; ++turn) {
-        float over[2] = {-INFINITY, -INFINITY};
+        float over[2] = {sh.far[g], -INFINITY};
 #pragma unroll
         for (int c0 = 0; c0 < C; c0 += kChunk) {
           uint32_t s[kChunk];
@@ -396,7 +425,7 @@ struct Q8Softmax {
           if (i == i0) unit = now;
         }
         if (!group_any(g, fmaxf(over[0], over[1]) > kQ8Most || now != unit || !ok)) break;
-        if (turn > 1) break;  // (never: the references are right after one turn)
+        if (turn > 1) break;  // (far, or scores that are not finite: the references are right after one turn)
         // (O may be multiplied: the last product into it is complete)
         if (ok && !waited) ok = products_done();
         waited = true;
@@ -418,12 +447,18 @@ struct Q8Softmax {
         group_any(g, false);
         if (mine < C) {
           const float m = fmaxf(max3(c0s[mine], c1s[mine], c2s[mine]), c3s[mine]);
-          const float n = neg_ref[mine];
+          const float n = sh.ref[g][mine];
           const bool up = m + n > kQ8Most;
           c0s[mine] = up ? ex2(kTop - (m + n)) : 1.f;  // (0 at a row's first keys)
-          if (up) neg_ref[mine] = kTop - m;
+          if (up) neg_ref[mine] = sh.ref[g][mine] = kTop - m;
+          if (mine < sh.columns[g] && m > -INFINITY && fabsf(m) >= Attend8Params::kFar) sh.far[g] = INFINITY;
         }
         group_any(g, false);
+        if (sh.far[g] > 0.f) {
+          far_scores(tm_s, C, scale, sh.ref[g]);
+          if (mine < C) neg_ref[mine] = 0.f;
+          turn = 1;
+        }
         if (i > i0) {
 #pragma unroll
           for (int c = 0; c < C / 2; ++c) {
@@ -495,7 +530,7 @@ struct Q8Softmax {
       group_any(g, false);  // all sums have been read
       if (mine < C) {
         places[mine] = place(a, rows, col0 + mine);
-        store_ml(a, places[mine], col0 + mine, neg_ref[mine] == kQ8Unset ? -INFINITY : -neg_ref[mine], l);
+        store_ml(a, places[mine], col0 + mine, sh.ref[g][mine] == kQ8Unset ? -INFINITY : -sh.ref[g][mine], l);
       }
       group_any(g, false);
       tc_fence_after();
@@ -531,7 +566,7 @@ struct Q8Softmax {
       float* const factor = c3s;  // [2][kHalf]
       if (mine < kHalf) {
         const int c = g * kHalf + mine;
-        const float n0 = sh.neg_ref[0][c], n1 = sh.neg_ref[1][c], m = fmaxf(-n0, -n1);
+        const float n0 = sh.ref[0][c], n1 = sh.ref[1][c], m = fmaxf(-n0, -n1);
         const float f0 = n0 == kQ8Unset ? 0.f : ex2(-n0 - m), f1 = n1 == kQ8Unset ? 0.f : ex2(-n1 - m);
         // (a part of one tile has one O, in the group of its buffer: the other is not looked at)
         factor[mine] = tiles > 1 || (base & 1) == 0 ? f0 * sh.unit[0] : -1.f;

@@ -162,3 +162,55 @@ def test_factors_of_scores_past_the_largest(sv, form):  # noqa: F811
     pr.scales[0][pr.ptable.long()] = 120 + 127
     pr.refresh()
     _check(sv, pr)
+
+
+# ---------------------------------------------------------------------------
+# scores larger than fp32 resolves
+# ---------------------------------------------------------------------------
+@FORM
+@pytest.mark.parametrize("dtype,log2", [("bf16", x) for x in (20, 25, 27, 29, 31, 33, 36, 40, 60, 100)] +
+                         [("fp16", x) for x in (20, 23, 26)])
+@pytest.mark.parametrize("how", ["equal", "negative", "two", "rising"])
+def test_large_scores(sv, form, dtype, log2, how):  # noqa: F811
+    """Scores of some 2^log2 in one dim, exact as products: keys of the largest score share the
+    weight, the others have none."""
+    import torch
+    pr = _make(71, dtype, 64, form, 700)
+    rng = np.random.default_rng(log2)
+    a = log2 // 2 if dtype == "bf16" else 14
+    b = log2 - a  # the keys' part
+    tiles = 6
+
+    def keys(t, c):
+        code = {"equal": 0x73, "negative": 0xF3, "two": 0x73 if t % 3 else 0x6B, "rising": 0x73}[how]
+        return np.broadcast_to(np.where(np.arange(64) == 0, code, 0), c.shape)
+
+    # 1.375 2^(b + 3), or half of that; rising: by a power of two a tile
+    _edit(pr, 0, keys, lambda t, e: b - 4 - (0 if how != "rising" else tiles - 1 - t // 128))
+    # every row a mantissa of its own
+    pr.q = pr.q * 0
+    m = torch.from_numpy(rng.integers(128, 256, pr.q.shape[:2]) / 128.0).cuda()
+    pr.q[..., 0] = (m * 2.0 ** a).to(pr.q.dtype)
+    _check(sv, pr, exact_scores=True)
+
+
+@FORM
+@pytest.mark.parametrize("log2", [25, 31, 40, 60])
+def test_large_scores_beside_a_hidden_nan(sv, form, log2):  # noqa: F811
+    """The same, summed again key by key, for a value that is not finite and that only the last
+    row sees."""
+    pr = _make(72, "bf16", 64, form, 700)
+    _edit(pr, 0, lambda t, c: np.broadcast_to(np.where(np.arange(64) == 0, 0x73, 0), c.shape), lambda t, e: log2 // 2 - 4)
+    pr.q = pr.q * 0
+    pr.q[..., 0] = 1.59375 * 2.0 ** (log2 - log2 // 2)
+    want, wl, tol, ltol = _exact(pr, exact_scores=True)
+    page, slot = _where(pr, 699)
+    pr.codes[1][page, slot, 0, 5] = 0x7F
+    for copies in (COPIES, 1):
+        got, gl = _run(sv, pr, copies=copies)
+        assert (np.abs(gl - wl) <= ltol).all()
+        assert (np.abs(got - want)[:, :-1] <= tol[:-1]).all()
+        first = pr.Hq // pr.Hk  # the heads that read key head 0
+        assert np.isnan(got[:, -1, :first, 5]).all()
+        got[:, -1, :first, 5] = want[-1, :first, 5]
+        assert (np.abs(got - want) <= tol).all()
