@@ -467,13 +467,14 @@ struct Q8Softmax {
             l2[c] = f32x2(x * c0s[2 * c], y * c0s[2 * c + 1]);
           }
           if (D == 128 || quad < 2) {
-            const float units = two_to(max(unit - now, -126));
+            // (units may be 2^220 apart: two steps, each a normal number)
+            const float units = two_to(max(unit - now, -126)), more = two_to(min(unit - now + 126, 0));
 #pragma unroll 1
             for (int c = 0; c < C; c += 16) {
               uint32_t o[16];
               tmem_load<16>(tm_o + c, o);
 #pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * (c0s[c + x] * units));
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * c0s[c + x] * units * more);
               tmem_st16(tm_o + c, o);
             }
             tmem_st_wait();

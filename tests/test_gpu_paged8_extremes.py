@@ -165,6 +165,46 @@ def test_factors_of_scores_past_the_largest(sv, form):  # noqa: F811
 
 
 # ---------------------------------------------------------------------------
+# values of blocks that are far apart
+# ---------------------------------------------------------------------------
+def _weightless(pr, first, count):
+    """Keys first .. first + count - 1 whose weights are nothing: -128 in every dim, before
+    queries of ones (whose other scores are small)."""
+    pr.q = pr.q * 0 + 1.0
+    inside = lambda t: first <= t < first + count  # noqa: E731
+    _edit(pr, 0, lambda t, c: np.full_like(c, 0xF0) if inside(t) else None, lambda t, e: 0 if inside(t) else None)
+
+
+@FORM
+@pytest.mark.parametrize("apart", [100, 120, 131, 150, 200])
+def test_a_hidden_block_of_much_larger_values(sv, form, apart):  # noqa: F811
+    """The last block's values are 2^apart times the others' and have no weight: what the tiles
+    before it gave stands (where fp32 can hold it beside them), or is lost; it is not enlarged.
+    In the last tile small values may be lost from 2^110 on."""
+    pr = _make(41, "bf16", 64, form, 704)
+    _weightless(pr, 688, 16)
+    _edit(pr, 1, lambda t, c: c & 0x7F, lambda t, e: e - 80 if t < 688 else e - 80 + apart)  # (values of one sign)
+    want, wl, tol, ltol = _exact(pr)
+    got, gl = _run(sv, pr)
+    assert (np.abs(gl - wl) <= ltol).all()
+    # at most the last tile's values
+    V, K, q = (_f64(x) for x in (pr.pools[1], pr.pools[0], pr.q))
+    group, lost = pr.Hq // pr.Hk, np.zeros_like(want)
+    for h in range(pr.Hq):
+        for t in range(640, 688):
+            page, slot = _where(pr, t)
+            w = np.exp(pr.D ** -0.5 * (K[page, slot, h // group] @ q[0, h]) - wl[:, h])
+            lost[:, h] += w[:, None] * np.abs(V[page, slot, h // group])
+    if apart <= 110:
+        lost *= 0
+    assert (np.abs(want) > 4 * (tol + lost)).all()
+    if apart <= 131:  # (sums in units of 2^(apart - 87) are not below 2^-126)
+        assert (np.abs(got - want) <= tol + lost).all()
+    else:
+        assert (np.abs(got) <= np.abs(want) + tol + lost).all()
+
+
+# ---------------------------------------------------------------------------
 # scores larger than fp32 resolves
 # ---------------------------------------------------------------------------
 @FORM
