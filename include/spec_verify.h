@@ -604,7 +604,12 @@ int spec_kv_read8(const spec_kv_cache8 *cache, const int32_t *out_indptr, int R,
 
 /*
  * spec_prefix_attention over an 8-bit cache: the same arguments, outputs, masks,
- * precision (over the values that the codes stand for), limits and workspace.
+ * limits and workspace, and the same precision over the values that the codes stand
+ * for, but for this.  With a bf16 cache too the weights are rounded to fp16 (where
+ * small, off by up to 2^-29 of the row's largest), except for key tiles with value
+ * blocks whose scales are 2^16 or more below or 2^8 or more above those of the first
+ * tile that a CTA took, which have bf16 weights.  Blocks of values 2^110 or more below
+ * the largest of the sequence may be lost.
  */
 int spec_prefix_attention8(const spec_kv_cache8 *cache, const void *q, int64_t q_pos_stride,
                            int64_t q_head_stride, int n_q_heads, int N, const int32_t *q_indptr,

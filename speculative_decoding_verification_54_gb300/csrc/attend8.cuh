@@ -19,7 +19,7 @@
 // scale counts in its scores, not in its values; queries are multiples of one power
 // of two (a part whose rows differ by more than 2^20, or are not finite, keeps bf16
 // queries and keys); values are multiples of another (a tile with blocks too small
-// for it has bf16 values and weights).
+// for it has bf16 values and weights, and so have all tiles once the unit has risen).
 //
 // An item is a row tile (up to 128 rows) against all tiles of 128 keys it sees.
 // One CTA per SM, 16 warps:
@@ -877,7 +877,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
       // The values' unit (bf16 caches): they are converted to fp16 as multiples of
       // 2^unit, exact for blocks whose exponents are within unit - 15 .. unit + 7.
       // It is the first tile's largest exponent and rises where one passes that range;
-      // a tile with a block below it is converted to bf16 instead.
+      // a tile with a block below it is converted to bf16 instead.  So are all tiles once
+      // it has risen: weights too small for fp16 may count there, since the ones that the
+      // references were set at stand before much smaller values.
       const int values = warp == 15 ? 1 : 0;
       const CUtensorMap* const map = values ? &p.tmV : &p.tmK;
       const uint8_t* const scales = values ? p.c8.v_scales : p.c8.k_scales;
@@ -920,7 +922,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
           return page < p.n_pages ? scales[p.c8.scale_at(page, static_cast<int>(key % page_size), head)] : 256;
         };
         int unit = 0;
-        bool any = false;  // unit is set
+        int low = -1000;  // tiles with a block below it have bf16 values (-1000: the unit is not set)
         // pages three tiles ahead, scales two
         int page0 = page_at(0), page1 = page_at(1), page2 = page_at(2);
         uint32_t scale0 = scale_of(0, page0), scale1 = scale_of(1, page1);
@@ -948,11 +950,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
           int wide = 0;
           if (kBf16 && values) {
             const int most = __reduce_max_sync(0xffffffffu, none ? -1000 : e), least = __reduce_min_sync(0xffffffffu, none ? 1000 : e);
-            if (most > -1000 && (!any || most > unit + 7)) {
+            if (most > -1000 && (low == -1000 || most > unit + 7)) {
+              low = low == -1000 ? most - 15 : 1000;
               unit = most;
-              any = true;
             }
-            wide = least < unit - 15;
+            wide = least < low;
           }
           if (lane < 16) sh.scales[values][slot][lane] = static_cast<int8_t>(none && values ? unit : e);
           if (values && lane == 0) {

@@ -204,6 +204,23 @@ def test_a_hidden_block_of_much_larger_values(sv, form, apart):  # noqa: F811
         assert (np.abs(got) <= np.abs(want) + tol + lost).all()
 
 
+@FORM
+@pytest.mark.parametrize("log2", [6, 20, 28, 30, 31, 34, 40])
+@pytest.mark.parametrize("first,count", [(16, 16), (128, 128), (256, 128), (304, 16), (384, 256), (512, 192)])
+def test_small_weights_of_large_values(sv, form, log2, first, count):  # noqa: F811
+    """One key of the first tile has the weight 1, all others 2^-log2, and some have values of
+    2^log2 (a block, whole tiles): they count as much as the one."""
+    pr = _make(51, "bf16", 64, form, 704)
+    one, large = 7, lambda t: first <= t < first + count  # noqa: E731
+    # scores: q_0 k_0, keys of 0 but the one's 4
+    keys = lambda t, c: np.broadcast_to(np.where((np.arange(64) == 0) & (t == one), 0x48, 0), c.shape)  # noqa: E731
+    _edit(pr, 0, keys, lambda t, e: 0)
+    _edit(pr, 1, None, lambda t, e: -7 + (log2 if large(t) else 0))
+    pr.q = pr.q * 0
+    pr.q[..., 0] = log2 * np.log(2.0) * 8 / 4
+    _check(sv, pr, small=lambda t: not large(t))
+
+
 # ---------------------------------------------------------------------------
 # scores larger than fp32 resolves
 # ---------------------------------------------------------------------------
