@@ -17,7 +17,7 @@
 // Types.  The products are fp16 with a bf16 cache too, wherever that is exact: the
 // conversion from e4m3 is one instruction a pair, and to bf16 it is ten.  A key's
 // scale counts in its scores, not in its values; queries are multiples of one power
-// of two (a part whose rows differ by more than 2^20, or are not finite, keeps bf16
+// of two (a part with dims more than 2^31 below its largest, or not finite, keeps bf16
 // queries and keys); values are multiples of another (a tile with blocks too small
 // for it has bf16 values and weights, and so have all tiles once the unit has risen).
 //
@@ -122,7 +122,7 @@ struct Q8Shared {
   int8_t raw_wide[kSlots], v_wide[2];           // whether they are converted to bf16 (else fp16)
   int16_t q_exp[2];                             // log2 of the unit of a part's queries
   int8_t q_bf16[2];                             // whether they stay bf16
-  uint32_t row_max[kAtTile];
+  uint32_t row_ends[kAtTile];  // of the queries' rows: largest magnitude, smallest that is not 0 less 1 (upper half)
   AtPart parts[kQ8Queue];
   uint32_t tmem;
 };
@@ -1003,33 +1003,41 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
       if (line < 0) break;
       bool k_bf16 = false;
       if (kBf16) {
-        // The queries as fp16 times 2^unit: the largest gets 2^14 or more, and what
-        // is not below 2^-20 of it keeps bf16's 8 bits 2^10 times over.  Rows
-        // smaller than that, or not finite: they stay bf16, and so do the keys.
+        // The queries as fp16 times 2^unit: the largest gets 2^14 or more, and what has an
+        // exponent up to 31 below its, 2^-17 or more, has bf16's 8 bits above fp16's last,
+        // 2^-24.  With smaller ones (zeros are none), or any not finite, all stay bf16, and
+        // so do the keys: either way the products are exact, whatever rows share the part.
         wait(&sh.q_full[n & 1], (n >> 1) & 1);
         uint8_t* const qt = qbuf + (n & 1) * kTileBytes;
-        uint32_t top = 0;  // of this thread's row
+        // of this thread's row, two values at a time: magnitudes with bit 15 set, the largest;
+        // less 1 and signed, where zero is the largest, the smallest
+        uint32_t top2 = 0, low2 = 0x7fff7fffu;
         if (ok && key < rows) {
 #pragma unroll
           for (int c = 0; c < D / 8; ++c) {
             const uint4 w = *reinterpret_cast<const uint4*>(qt + (c / 8) * kHalfBytes + key * 128 + (((c % 8) ^ (key & 7)) << 4));
             const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0x7fffu, x[i] >> 16 & 0x7fffu));
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t y = x[i] | 0x80008000u;
+              top2 = __vmaxu2(top2, y);
+              low2 = __vmins2(low2, y - 0x00010001u);
+            }
           }
         }
-        sh.row_max[key] = top;
+        sh.row_ends[key] = __vmaxu2(top2 & 0x7fff7fffu, top2 >> 16 & 0x7fffu) & 0xffffu |
+                           (__vmins2(low2, low2 >> 16 | low2 << 16) ^ 0x80008000u) << 16;
         if (group_any(2, !ok)) break;
         uint32_t most = 0, least = 0xffff;
 #pragma unroll
         for (int r = 0; r < kAtTile; r += 32) {
-          const uint32_t x = sh.row_max[r + lane];
-          most = max(most, x);
-          least = min(least, x == 0 ? 0xffffu : x);
+          const uint32_t x = sh.row_ends[r + lane];
+          most = max(most, x & 0xffffu);
+          least = min(least, x >> 16);
         }
         most = __reduce_max_sync(0xffffffffu, most);
         least = __reduce_min_sync(0xffffffffu, least);
-        k_bf16 = most >= 0x7f80u || (least >> 7) + 20 < (most >> 7);
+        k_bf16 = most >= 0x7f80u || (least + 1 >> 7) + 31 < (most >> 7);
         const int e = most == 0 || k_bf16 ? 0 : max(static_cast<int>(most >> 7) - 127 - 14, -120);
         if (!k_bf16) {
           const float f = two_to(-e);

@@ -222,6 +222,29 @@ def test_small_weights_of_large_values(sv, form, log2, first, count):  # noqa: F
 
 
 # ---------------------------------------------------------------------------
+# queries whose dims are far apart
+# ---------------------------------------------------------------------------
+@FORM
+@pytest.mark.parametrize("apart", [20, 28, 31, 32, 33, 35, 37, 45])
+@pytest.mark.parametrize("rows", ["each", "beside"])
+def test_small_dims_of_queries_against_large_keys(sv, form, apart, rows):  # noqa: F811
+    """Dims 2^apart below the largest one of their row (or of another row), which decide the
+    scores: keys are 2^apart times larger there, and 0 where the largest is."""
+    import torch
+    pr = _make(61, "bf16", 64, form, 460)
+    rng = np.random.default_rng(apart)
+    small = rng.uniform(1, 2, pr.q.shape) * rng.choice([-1.0, 1.0], pr.q.shape) * 2.0 ** -apart
+    small[..., 0] = 1.0 if rows == "each" else 2.0 ** -20
+    small[..., 1] = 0.0
+    if rows == "beside":
+        small[0] = 0.0
+        small[0, :, 1] = 1.0  # the first position's rows: the largest dim alone, hidden by keys of 0
+    pr.q = torch.from_numpy(small).to(torch.bfloat16).cuda()
+    _edit(pr, 0, lambda t, c: np.where(np.arange(64) < 2, 0, c), lambda t, e: e + apart)
+    _check(sv, pr)
+
+
+# ---------------------------------------------------------------------------
 # scores larger than fp32 resolves
 # ---------------------------------------------------------------------------
 @FORM
