@@ -167,12 +167,34 @@ def test_factors_of_scores_past_the_largest(sv, form):  # noqa: F811
 # ---------------------------------------------------------------------------
 # values of blocks that are far apart
 # ---------------------------------------------------------------------------
+@FORM
+@pytest.mark.parametrize("dtype,low,high", [("bf16", -30, 30), ("bf16", -6, 6), ("fp16", -6, 6)])
+def test_value_scales_far_apart_row_by_row(sv, form, dtype, low, high):  # noqa: F811
+    rng = np.random.default_rng(5)
+    for how in range(4):
+        pr = _make(21 + how, dtype, 64, form, 700)
+        far = [lambda t: low + (high - low) * t // 700, lambda t: high - (high - low) * t // 700,
+               lambda t: int(rng.integers(low, high + 1)), lambda t: high if 300 <= t < 316 else low][how]
+        _edit(pr, 1, None, lambda t, e: np.clip(e + far(t), paged8.LOW[dtype], paged8.HIGH[dtype]))
+        _check(sv, pr)
+
+
 def _weightless(pr, first, count):
     """Keys first .. first + count - 1 whose weights are nothing: -128 in every dim, before
     queries of ones (whose other scores are small)."""
     pr.q = pr.q * 0 + 1.0
     inside = lambda t: first <= t < first + count  # noqa: E731
     _edit(pr, 0, lambda t, c: np.full_like(c, 0xF0) if inside(t) else None, lambda t, e: 0 if inside(t) else None)
+
+
+@FORM
+@pytest.mark.parametrize("at", [0, 128, 320, 688])
+def test_rows_of_small_values_beside_weightless_large_ones(sv, form, at):  # noqa: F811
+    """A block of values 2^40 times the others', at which every row's weight is nothing."""
+    pr = _make(31, "bf16", 64, form, 704)
+    _weightless(pr, at, 16)
+    _edit(pr, 1, None, lambda t, e: e + 40 if t == at else None)
+    _check(sv, pr)
 
 
 @FORM
