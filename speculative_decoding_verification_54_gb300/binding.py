@@ -506,7 +506,7 @@ def _current_device() -> int:
 
 def _cache_of(name, cache, kind, maker):
     """A cache of the other kind is another struct: never handed on."""
-    if type(cache) is not kind:
+    if not isinstance(cache, kind):
         raise SpecVerifyError(SPEC_ERR_INVALID_ARG, f"{name}: a cache of {maker} is wanted, not {type(cache).__name__}")
 
 
@@ -554,7 +554,7 @@ def spec_kv_append(cache, q, k, v, q_out, q_indptr, block_table, kv_len, workspa
     int32 [B] (the new positions counted); inv_freq float32 [rot_dim / 2] (None:
     no rotation); positions int32 [n_axes, N] and axis int32 [rot_dim / 2], or
     None for position_base + the entry's index."""
-    if type(cache) is not SpecKvCache:
+    if not isinstance(cache, SpecKvCache):
         _cache_of("spec_kv_append", cache, SpecKvCache, "make_kv_cache")
     dt, n_heads, D, _, device, i32, f32, _ = cache.expected
     q_shape, k_shape, table_shape, B = q.shape, k.shape, block_table.shape, kv_len.numel()
