@@ -521,7 +521,8 @@ int spec_prefix_attention(const spec_kv_cache *cache, const void *q, int64_t q_p
  *   norm_eps            >= 0
  *
  * Squares are summed in fp32: a head whose sum passes 3.4e38 (values of 1e18 and
- * more) becomes 0.  The other arguments, the workspace and the errors are
+ * more) becomes 0, and with norm_eps 0 one whose sum is below 1e-45 (values of 1e-23
+ * and less, or zeros) infinite or NaN.  The other arguments, the workspace and the errors are
  * spec_kv_append's.
  */
 int spec_kv_append_norm(const spec_kv_cache *cache, const void *q, int64_t q_pos_stride,
@@ -537,8 +538,11 @@ int spec_kv_append_norm(const spec_kv_cache *cache, const void *q, int64_t q_pos
 /*
  * ---------------------------------------------------------------------------
  * The paged cache in 8 bits: keys and values as e4m3 codes with a scale for each
- * block of entries, head and side.  Twice the entries in the same memory, and
- * half the bytes where the attention is bound by the cache's.
+ * block of entries, head and side.  Twice the entries in the same memory.  Its
+ * attention takes less time than over 16 bits where the sequences' own pages bound it
+ * (few new positions and thousands of own entries a sequence: 0.8 to 0.9 of the time),
+ * and more where products and weights do (short caches: 1.1 times; verify passes
+ * behind a long shared prefix: 1.7; hundreds of new positions, many rows: up to twice).
  *
  * A block is `block` neighbouring slots of a page that begin at a multiple of it;
  * its scale is 2^e, kept as the byte e + 127 (the E8M0 format), and a code stands
@@ -609,7 +613,10 @@ int spec_kv_read8(const spec_kv_cache8 *cache, const int32_t *out_indptr, int R,
  * small, off by up to 2^-29 of the row's largest), except for key tiles with value
  * blocks whose scales are 2^16 or more below or 2^8 or more above those of the first
  * tile that a CTA took, which have bf16 weights.  Blocks of values 2^110 or more below
- * the largest of the sequence may be lost.
+ * the largest of the sequence may be lost.  Queries (bf16) are taken exactly; where
+ * their dims are more than 2^31 apart the products are slower.  Where the largest |q|
+ * of neighbouring rows times a block's largest |k| times scale passes 2^145, only scores
+ * of 0 are sure to be right.
  */
 int spec_prefix_attention8(const spec_kv_cache8 *cache, const void *q, int64_t q_pos_stride,
                            int64_t q_head_stride, int n_q_heads, int N, const int32_t *q_indptr,

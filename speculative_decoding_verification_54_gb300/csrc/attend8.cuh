@@ -39,7 +39,7 @@
 // maxima taken and O and the sums multiplied.  The sums are kept by key in
 // registers (fp32) and added up over the lanes once a part.
 //
-// What bounds it.  16 caches of up to 32,768 entries (472 MB): 127 us, 3.7 TB/s (the
+// What bounds it.  16 caches of up to 32,768 entries (472 MB): 125 to 127 us, 3.7 TB/s (the
 // 16-bit call 150 us on twice the bytes).  A tile of 128 keys takes 2,400 clocks
 // with few rows; HBM would need 1,450.  Two chains are that long: the converters'
 // (keys 450, values 950, four waits) and the issuer's (16 products of 50 to 60
@@ -47,13 +47,16 @@
 // 3,500.  All of it runs at the rate of instruction fetches (a warp of every
 // SM quarter has code of its own): loops that are not unrolled, and code that runs
 // once a part kept short, took long caches from 385 to 127 us, long drafts from 2,083 to
-// 670.  Tried and not kept: converters for keys and values apart, 20 warps (160
+// some 700 (666 to 715 on several boxes).  Tried and not kept, against 127 and 670 to
+// 705: converters for keys and values apart, 20 warps (160
 // registers for the softmax, more code at once: 138 us and 905); an issuer for
 // each product besides (180 and 1,059); products unrolled with their operands in
 // uniform registers (15 clocks an instruction by itself, no change here); values
 // converted four vectors at a time, or one ahead (127 to 133); values converted by
 // the softmax groups (129 and 778), and the next scores issued before the output
-// besides (128 and 894); bf16 products throughout (207 and 1,091).
+// besides (128 and 894); bf16 products throughout (207 and 1,091).  Scores past kFar rounded
+// within the loop over tiles, instead of in a function of its own that it calls: long
+// drafts 725 to 760 beside 710.
 #pragma once
 
 #include "attend.cuh"
