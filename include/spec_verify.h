@@ -610,9 +610,9 @@ int spec_kv_read8(const spec_kv_cache8 *cache, const int32_t *out_indptr, int R,
  * spec_prefix_attention over an 8-bit cache: the same arguments, outputs, masks,
  * limits and workspace, and the same precision over the values that the codes stand
  * for, but for this.  With a bf16 cache too the weights are rounded to fp16 (where
- * small, off by up to 2^-29 of the row's largest), except for key tiles with value
- * blocks whose scales are 2^16 or more below or 2^8 or more above those of the first
- * tile that a CTA took, which have bf16 weights.  Blocks of values 2^110 or more below
+ * small, off by up to 2^-29 of the row's largest), until a CTA comes upon value blocks
+ * whose scales are 2^16 or more below or 2^8 or more above those of its part's first
+ * 128 keys: from there on they are bf16.  Blocks of values 2^110 or more below
  * the largest of the sequence may be lost.  Queries (bf16) are taken exactly; where
  * their dims are more than 2^31 apart the products are slower.  Where the largest |q|
  * of neighbouring rows times a block's largest |k| times scale passes 2^145, only scores

@@ -19,7 +19,8 @@
 // scale counts in its scores, not in its values; queries are multiples of one power
 // of two (a part with dims more than 2^31 below its largest, or not finite, keeps bf16
 // queries and keys); values are multiples of another (a tile with blocks too small
-// for it has bf16 values and weights, and so have all tiles once the unit has risen).
+// for it has bf16 values and weights, and so have all tiles of the part after it, and
+// those from which on the unit has risen).
 //
 // An item is a row tile (up to 128 rows) against all tiles of 128 keys it sees.
 // One CTA per SM, 16 warps:
@@ -880,9 +881,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
       // The values' unit (bf16 caches): they are converted to fp16 as multiples of
       // 2^unit, exact for blocks whose exponents are within unit - 15 .. unit + 7.
       // It is the first tile's largest exponent and rises where one passes that range;
-      // a tile with a block below it is converted to bf16 instead.  So are all tiles once
-      // it has risen: weights too small for fp16 may count there, since the ones that the
-      // references were set at stand before much smaller values.
+      // a tile with a block below it is converted to bf16 instead.  So are all tiles after
+      // one of either kind: weights too small for fp16 may count there, since the ones that
+      // the references were set at may stand before much smaller values.
       const int values = warp == 15 ? 1 : 0;
       const CUtensorMap* const map = values ? &p.tmV : &p.tmK;
       const uint8_t* const scales = values ? p.c8.v_scales : p.c8.k_scales;
@@ -958,6 +959,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) attend8_kernel(const __grid_con
               unit = most;
             }
             wide = least < low;
+            if (wide) low = 1000;
           }
           if (lane < 16) sh.scales[values][slot][lane] = static_cast<int8_t>(none && values ? unit : e);
           if (values && lane == 0) {

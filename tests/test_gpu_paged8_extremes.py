@@ -243,6 +243,21 @@ def test_small_weights_of_large_values(sv, form, log2, first, count):  # noqa: F
     _check(sv, pr, small=lambda t: not large(t))
 
 
+@FORM
+@pytest.mark.parametrize("log2", [20, 28, 30, 31, 34, 40])
+def test_small_weights_of_large_values_on_both_sides(sv, form, log2):  # noqa: F811
+    """The same with large values first: two tiles of them, two of small ones that have the keys
+    of weight 1, two of large ones again."""
+    pr = _make(52, "bf16", 64, form, 704)
+    large = lambda t: t < 256 or t >= 512  # noqa: E731
+    keys = lambda t, c: np.broadcast_to(np.where((np.arange(64) == 0) & (t in (260, 390)), 0x48, 0), c.shape)  # noqa: E731
+    _edit(pr, 0, keys, lambda t, e: 0)
+    _edit(pr, 1, None, lambda t, e: -7 + (log2 if large(t) else 0))
+    pr.q = pr.q * 0
+    pr.q[..., 0] = log2 * np.log(2.0) * 8 / 4
+    _check(sv, pr, small=lambda t: not large(t))
+
+
 # ---------------------------------------------------------------------------
 # queries whose dims are far apart
 # ---------------------------------------------------------------------------
